@@ -19,6 +19,13 @@ PyTorch is used for device memory and streams only.
     PairLink(...).broadcast / all_gather     pure movement between the two ranks
     OneShotLink(...).all_reduce(x0, x1)      the one-kernel arm with an in-kernel barrier
 
+The decode step around the fold (``decode.py``):
+
+    PagedCache(k, v)                         a paged key-value cache
+    cache_append(cache, k, v, slots, ...)    rotate and store new tokens
+    attend_paged(out, q, cache, table, lens) one new token per row over its pages
+    fold_softmax(out, outs, lses)            fixed-order join of attention partials
+
 ``stacked`` is a ``[W, len]`` float32 CUDA/HIP tensor (row r = slot r); a view
 with a storage offset is fine as long as it is contiguous.
 """
@@ -49,6 +56,8 @@ EXPORTS = (
     "detfold_pair_all_gather", "detfold_one_shot_init", "detfold_one_shot_all_reduce",
     "detfold_one_shot_rank", "detfold_fold_ranks_timed", "detfold_loopback_round_static",
     "fold_ranks_batch", "fold_ranks_batch_scaled", "detfold_plan_fold_ranks_batch",
+    "detfold_cache_append", "detfold_attend_paged", "detfold_plan_attend",
+    "detfold_attend_workspace", "detfold_fold_softmax",
 )
 MAX_JOBS = 32
 
@@ -138,6 +147,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.detfold_one_shot_init.argtypes = [ctypes.POINTER(OneShotLinkC)]
     lib.detfold_one_shot_all_reduce.argtypes = [ctypes.POINTER(OneShotLinkC), f32p, f32p, i64]
     lib.detfold_one_shot_rank.argtypes = [ctypes.POINTER(OneShotLinkC), i32, f32p, i64, vp]
+    decode.bind(lib)
     for name in EXPORTS:
         if name != "detfold_strerror":
             getattr(lib, name).restype = ctypes.c_int
@@ -611,3 +621,8 @@ def plan_fold_into(dst_addr: int, stage_addr: int, n: int, cu_count: int) -> dic
     _check(load().detfold_plan_fold_into(dst_addr, stage_addr, n, cu_count, ctypes.byref(p)),
            "plan_fold_into")
     return p.as_dict()
+
+
+from . import decode  # noqa: E402  (after what it takes from here)
+from .decode import (PagedCache, attend_paged, attend_workspace, cache_append,  # noqa: E402
+                     fold_softmax, plan_attend)

@@ -1,16 +1,19 @@
 """Build step for ``libdetfold.so`` (hipcc, gfx950 only).
 
-Sources (``csrc/``): fold_kernels.hip (device code and its launches), plan.cpp
-(host-only planning and argument checks), detfold.cpp (call sequences and the
-C ABI), internal.h (their shared declarations).  exports.map limits the
-exported symbols to the C ABI of include/detfold.h.
+Sources (``csrc/``): fold_kernels.hip (the fold's device code and launches),
+plan.cpp (host-only planning and argument checks), detfold.cpp (call sequences
+and the C ABI), internal.h (their shared declarations); of the decode-step
+operators cache_kernels.hip and attend_kernels.hip (device code and launches),
+decode.cpp (checks, planning and the C ABI), decode.h and decode_device.h.
+exports.map limits the exported symbols to the C ABI of include/detfold.h.
 
-fold_kernels.hip is compiled in two passes, so that device-only flags reach
+The .hip files are compiled in two passes, so that device-only flags reach
 the device compiler only: the device pass writes the gfx950 code object
 bundle, and the host pass embeds it (clang's ``-fcuda-include-gpubinary``,
-the step the one-command HIP build performs internally).  Both passes share
-one compilation-unit id, so host and device agree on the names of any
-``__device__`` variable.  plan.cpp and detfold.cpp hold no device code.
+the step the one-command HIP build performs internally).  Both passes of a
+file share one compilation-unit id, so host and device agree on the names of
+any ``__device__`` variable.  The .cpp files hold no device code.  The files
+are compiled side by side.
 
 Flags that fix the fold's bits:
   -ffp-contract=off                 no fused multiply-add anywhere
@@ -33,6 +36,7 @@ import os
 import shutil
 import subprocess
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -41,12 +45,13 @@ KERNELS = os.path.join(CSRC, "fold_kernels.hip")
 HOST_SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "detfold.cpp")]
 SOURCES = [KERNELS] + HOST_SOURCES
 INTERNAL_HEADER = os.path.join(CSRC, "internal.h")
+DECODE_KERNELS = [os.path.join(CSRC, f) for f in ("cache_kernels.hip", "attend_kernels.hip")]
+DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_device.h")]
 EXPORTS_MAP = os.path.join(CSRC, "exports.map")
 HEADER = os.path.join(ROOT, "include", "detfold.h")
 LIB = os.path.join(PKG, "libdetfold.so")
 DIGEST = LIB + ".sha256"
 ARCH = "gfx950"
-CUID = "detfold_fold_kernels"
 
 
 def hipcc() -> str:
@@ -75,7 +80,7 @@ def link_flags() -> list[str]:
 
 def source_digest() -> str:
     h = hashlib.sha256()
-    for path in SOURCES + [INTERNAL_HEADER, EXPORTS_MAP, HEADER]:
+    for path in SOURCES + DECODE_SOURCES + [INTERNAL_HEADER, EXPORTS_MAP, HEADER]:
         with open(path, "rb") as f:
             h.update(os.path.basename(path).encode() + b"\0" + f.read() + b"\0")
     h.update("\0".join(common_flags() + device_flags() + link_flags()).encode())
@@ -95,26 +100,44 @@ def _run(cmd: list[str], cwd: str | None = None) -> None:
     subprocess.run(cmd, check=True, cwd=cwd)
 
 
-def _device_pass(work: str, extra: list[str], temps: bool = False) -> str:
-    bundle = os.path.join(work, "fold_kernels.hipfb")
-    cmd = [hipcc(), "--cuda-device-only", "-cuid=" + CUID] + common_flags() + device_flags() + extra
+def _stem(path: str) -> str:
+    return os.path.splitext(os.path.basename(path))[0]
+
+
+def _cuid(path: str) -> str:
+    return "-cuid=detfold_" + _stem(path)
+
+
+def _device_pass(src: str, work: str, extra: list[str], temps: bool = False) -> str:
+    bundle = os.path.join(work, _stem(src) + ".hipfb")
+    cmd = [hipcc(), "--cuda-device-only", _cuid(src)] + common_flags() + device_flags() + extra
     if temps:
         cmd.append("-save-temps=obj")
-    _run(cmd + ["-c", KERNELS, "-o", bundle], cwd=work)
+    _run(cmd + ["-c", src, "-o", bundle], cwd=work)
     return bundle
 
 
+def _kernel_object(src: str, work: str, extra: list[str]) -> str:
+    bundle = _device_pass(src, work, extra)
+    obj = os.path.join(work, _stem(src) + ".o")
+    _run([hipcc(), "--cuda-host-only", _cuid(src)] + common_flags() + extra +
+         ["-Xclang", "-fcuda-include-gpubinary", "-Xclang", bundle, "-c", src, "-o", obj])
+    return obj
+
+
+def _host_object(src: str, work: str, extra: list[str]) -> str:
+    obj = os.path.join(work, _stem(src) + ".o")
+    _run([hipcc()] + common_flags() + extra + ["-c", src, "-o", obj])
+    return obj
+
+
 def _objects(work: str, extra: list[str]) -> list[str]:
-    bundle = _device_pass(work, extra)
-    kobj = os.path.join(work, "fold_kernels.o")
-    _run([hipcc(), "--cuda-host-only", "-cuid=" + CUID] + common_flags() + extra +
-         ["-Xclang", "-fcuda-include-gpubinary", "-Xclang", bundle, "-c", KERNELS, "-o", kobj])
-    objs = [kobj]
-    for src in HOST_SOURCES:
-        obj = os.path.join(work, os.path.splitext(os.path.basename(src))[0] + ".o")
-        _run([hipcc()] + common_flags() + extra + ["-c", src, "-o", obj])
-        objs.append(obj)
-    return objs
+    kernels = DECODE_KERNELS[::-1] + [KERNELS]
+    hosts = HOST_SOURCES + [s for s in DECODE_SOURCES if s.endswith(".cpp")]
+    with ThreadPoolExecutor(max_workers=min(6, os.cpu_count() or 1)) as pool:
+        jobs = [pool.submit(_kernel_object, s, work, extra) for s in kernels]
+        jobs += [pool.submit(_host_object, s, work, extra) for s in hosts]
+        return [j.result() for j in jobs]
 
 
 def build_library(out: str = LIB, extra: list[str] | None = None) -> str:
@@ -139,10 +162,11 @@ def build_library(out: str = LIB, extra: list[str] | None = None) -> str:
     return out
 
 
-def save_temps(outdir: str) -> None:
-    """Keep the gfx950 assembly of the device pass (for reading our own ISA)."""
+def save_temps(outdir: str, src: str | None = None) -> None:
+    """Keep the gfx950 assembly of a file's device pass (for reading our own
+    ISA); the fold's unless another is named."""
     os.makedirs(outdir, exist_ok=True)
-    _device_pass(outdir, [], temps=True)
+    _device_pass(src or KERNELS, outdir, [], temps=True)
 
 
 if __name__ == "__main__":

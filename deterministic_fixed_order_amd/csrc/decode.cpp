@@ -1,0 +1,298 @@
+// decode.cpp -- the host side of the decode-step operators: argument checks
+// and planning (no device access), and their C ABI.  Every check comes before
+// any HIP call, so an argument error never touches the device; nothing here
+// allocates, synchronizes or keeps a pointer.
+
+#include <cmath>
+#include <cstdint>
+
+#include "decode.h"
+#include "internal.h"
+
+namespace detfold_impl {
+namespace {
+
+constexpr int64_t kMaxCount = (int64_t)1 << 31;   // counts that the kernels hold in 32 bits
+constexpr int64_t kMaxElems = (int64_t)1 << 46;   // extent of one buffer, in elements
+constexpr int32_t kMaxHeads = 1 << 16;
+
+bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+// The elements a strided [n0][n1]...[last] buffer spans, or -1 where a stride
+// is negative or the span passes kMaxElems.  n >= 1 each.
+int64_t span(const int64_t (*dims)[2], int count, int64_t last)
+{
+    int64_t e = last;
+    for (int i = 0; i < count; ++i) {
+        const int64_t n = dims[i][0], s = dims[i][1];
+        if (s < 0 || (n > 1 && s > kMaxElems / (n - 1)))
+            return -1;
+        e += (n - 1) * s;
+        if (e > kMaxElems)
+            return -1;
+    }
+    return e;
+}
+
+int64_t span2(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t last)
+{
+    const int64_t d[2][2] = {{n0, s0}, {n1, s1}};
+    return span(d, 2, last);
+}
+
+// Whether a written [n0][n1][last] buffer has no element twice.
+bool distinct(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t last)
+{
+    if (n0 > 1 && n1 > 1)
+        return s0 >= s1 ? s1 >= last && s0 >= (n1 - 1) * s1 + last : s0 >= last && s1 >= (n0 - 1) * s0 + last;
+    return n1 > 1 ? s1 >= last : n0 <= 1 || s0 >= last;
+}
+
+struct Range {
+    uintptr_t p;
+    uint64_t bytes;
+};
+
+Range range(const void *p, int64_t elems, int size) { return {(uintptr_t)p, p ? (uint64_t)elems * (uint64_t)size : 0}; }
+bool meet(const Range &a, const Range &b) { return ranges_overlap(a.p, a.bytes, b.p, b.bytes); }
+
+int64_t cache_span(const detfold_paged_cache &c, bool values)
+{
+    const int64_t d[3][2] = {{c.pages, values ? c.v_page : c.k_page},
+                             {c.page, values ? c.v_token : c.k_token},
+                             {c.heads, values ? c.v_head : c.k_head}};
+    return span(d, 3, values ? c.v_dim : c.dim);
+}
+
+Range cache_range(const detfold_paged_cache &c, bool values)
+{
+    return range(values ? c.v : c.k, cache_span(c, values), elem_size(c.type));
+}
+
+}  // namespace
+
+bool types_pair(int32_t type, int32_t cache_type)
+{
+    if (type != DETFOLD_F32 && type != DETFOLD_BF16 && type != DETFOLD_F16)
+        return false;
+    return cache_type == type || cache_type == DETFOLD_E4M3 ||
+           (type == DETFOLD_F32 && cache_type == DETFOLD_BF16);
+}
+
+int check_cache(const detfold_paged_cache *c)
+{
+    if (!c || !c->k || !c->v || c->reserved != 0 || c->type < DETFOLD_F32 || c->type > DETFOLD_E4M3)
+        return DETFOLD_EINVAL;
+    if (c->pages < 1 || c->page < 1 || c->pages >= kMaxCount / c->page || c->heads < 1 || c->heads > kMaxHeads)
+        return DETFOLD_EINVAL;
+    for (int32_t d : {c->dim, c->v_dim})
+        if (d < DETFOLD_MIN_HEAD || d > DETFOLD_MAX_HEAD)
+            return DETFOLD_EINVAL;
+    if (cache_span(*c, false) < 0 || cache_span(*c, true) < 0)
+        return DETFOLD_EINVAL;
+    const uintptr_t size = (uintptr_t)elem_size(c->type);
+    if (!aligned(c->k, size) || !aligned(c->v, size) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return DETFOLD_EINVAL;
+    if (c->type != DETFOLD_E4M3 && (c->k_scale || c->v_scale))
+        return DETFOLD_EINVAL;
+    return DETFOLD_OK;
+}
+
+int check_append(const detfold_paged_cache *c, const detfold_append *a)
+{
+    int rc = check_cache(c);
+    if (rc != DETFOLD_OK)
+        return rc;
+    if (!a || a->tokens < 0 || a->tokens >= kMaxCount || a->q_heads < 0 || a->q_heads > kMaxHeads ||
+        a->rot < 0 || a->rot > c->dim || (a->rot & 1) || (a->pairs != 0 && a->pairs != 1) || a->angles < 0 ||
+        !types_pair(a->type, c->type))
+        return DETFOLD_EINVAL;
+    if (a->tokens == 0)
+        return DETFOLD_OK;
+    if (!a->k || !a->v || !a->slots || (a->q_heads > 0) != (a->q != nullptr) || (a->q != nullptr) != (a->q_out != nullptr))
+        return DETFOLD_EINVAL;
+    if (a->rot > 0 && (!a->positions || !a->cos || !a->sin || a->angles < 1 || a->angles > kMaxElems / 128))
+        return DETFOLD_EINVAL;
+    const int size = elem_size(a->type);
+    const int64_t nq = a->q_heads > 0 ? a->q_heads : 1;
+    const int64_t ks = span2(a->tokens, a->k_token, c->heads, a->k_head, c->dim);
+    const int64_t vs = span2(a->tokens, a->v_token, c->heads, a->v_head, c->v_dim);
+    const int64_t qs = a->q ? span2(a->tokens, a->q_token, nq, a->q_head, c->dim) : 0;
+    const int64_t os = a->q ? span2(a->tokens, a->out_token, nq, a->out_head, c->dim) : 0;
+    if (ks < 0 || vs < 0 || qs < 0 || os < 0)
+        return DETFOLD_EINVAL;
+    for (const void *p : {a->k, a->v, a->q, (const void *)a->q_out})
+        if (!aligned(p, (uintptr_t)size))
+            return DETFOLD_EINVAL;
+    if (!aligned(a->slots, 8) || !aligned(a->positions, 8) || !aligned(a->cos, 4) || !aligned(a->sin, 4))
+        return DETFOLD_EINVAL;
+    if (a->q_out && !distinct(a->tokens, a->out_token, nq, a->out_head, c->dim))
+        return DETFOLD_EOVERLAP;
+    // What is written (q_out, the cache) against what is read and against each other.
+    const Range k = cache_range(*c, false), v = cache_range(*c, true);
+    const Range in[] = {range(a->k, ks, size), range(a->v, vs, size), range(a->q, qs, size),
+                        range(a->slots, a->tokens, 8),
+                        range(a->rot ? a->positions : nullptr, a->tokens, 8),
+                        range(a->rot ? a->cos : nullptr, a->angles * (a->rot / 2), 4),
+                        range(a->rot ? a->sin : nullptr, a->angles * (a->rot / 2), 4),
+                        range(c->k_scale, c->heads, 4), range(c->v_scale, c->heads, 4)};
+    const Range out = range(a->q_out, os, size);
+    // In place, a query view among its neighbours of one projection: the
+    // spans of k and v interleave with it, its elements do not.
+    const bool in_place = a->q_out && a->q_out == a->q && a->out_token == a->q_token && a->out_head == a->q_head;
+    for (int i = 0; i < (int)(sizeof(in) / sizeof(in[0])); ++i) {
+        if (meet(k, in[i]) || meet(v, in[i]))
+            return DETFOLD_EOVERLAP;
+        if (!(in_place && i < 3) && meet(out, in[i]))
+            return DETFOLD_EOVERLAP;
+    }
+    if (meet(out, k) || meet(out, v))
+        return DETFOLD_EOVERLAP;
+    return DETFOLD_OK;
+}
+
+int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
+                int64_t window, int32_t split, int32_t cu_count, detfold_attend_plan *p)
+{
+    if (batch < 0 || batch >= kMaxCount || max_len < 0 || max_len >= kMaxCount || window < 0 || q_heads < 1 ||
+        q_heads > kMaxHeads || q_heads % c.heads != 0 || split < 0 || split % DETFOLD_ATTEND_STEP != 0 || cu_count < 1)
+        return DETFOLD_EINVAL;
+    p->units = batch * q_heads;
+    p->splits = 1;
+    p->split = max_len;
+    p->workspace_bytes = p->workspace_upto = 0;
+    return DETFOLD_OK;
+}
+
+int check_attend(const detfold_paged_cache *c, const detfold_attend *a)
+{
+    int rc = check_cache(c);
+    if (rc != DETFOLD_OK)
+        return rc;
+    if (!a || a->reserved != 0 || !types_pair(a->type, c->type) || (a->out_type != a->type && a->out_type != DETFOLD_F32))
+        return DETFOLD_EINVAL;
+    detfold_attend_plan p;  // checks the counts; the device's own plan follows
+    if ((rc = plan_attend(*c, a->batch, a->q_heads, a->max_len, a->window, a->split, 1, &p)) != DETFOLD_OK)
+        return rc;
+    if (!std::isfinite(a->scale) || a->table_width < 0 || a->table_row < 0 || a->workspace_bytes < 0)
+        return DETFOLD_EINVAL;
+    if (a->batch == 0)
+        return DETFOLD_OK;
+    if (!a->out || !a->q || !a->lens || (a->table_width > 0 && !a->table))
+        return DETFOLD_EINVAL;
+    const int size = elem_size(a->type), out_size = elem_size(a->out_type);
+    const int64_t qs = span2(a->batch, a->q_row, a->q_heads, a->q_head, c->dim);
+    const int64_t os = span2(a->batch, a->out_row, a->q_heads, a->out_head, c->v_dim);
+    const int64_t ts = a->table_width > 0 ? span2(a->batch, a->table_row, 1, 0, a->table_width) : 0;
+    if (qs < 0 || os < 0 || ts < 0)
+        return DETFOLD_EINVAL;
+    if (!aligned(a->q, (uintptr_t)size) || !aligned(a->out, (uintptr_t)out_size) || !aligned(a->lse, 4) ||
+        !aligned(a->table, 4) || !aligned(a->lens, 4) || !aligned(a->workspace, 16))
+        return DETFOLD_EINVAL;
+    if (!distinct(a->batch, a->out_row, a->q_heads, a->out_head, c->v_dim))
+        return DETFOLD_EOVERLAP;
+    const Range out = range(a->out, os, out_size), lse = range(a->lse, a->batch * a->q_heads, 4);
+    const Range work = range(a->workspace, a->workspace_bytes, 1);
+    const Range in[] = {range(a->q, qs, size), range(a->table, ts, 4), range(a->lens, a->batch, 4),
+                        cache_range(*c, false), cache_range(*c, true),
+                        range(c->k_scale, c->heads, 4), range(c->v_scale, c->heads, 4)};
+    for (const Range &r : in)
+        if (meet(out, r) || meet(lse, r) || meet(work, r))
+            return DETFOLD_EOVERLAP;
+    if (meet(out, lse) || meet(out, work) || meet(lse, work))
+        return DETFOLD_EOVERLAP;
+    return DETFOLD_OK;
+}
+
+int check_softmax(const SoftmaxArgs &s)
+{
+    if (s.w < 1 || s.rows < 0 || s.dim < 1 || s.type < DETFOLD_F32 || s.type > DETFOLD_F16)
+        return DETFOLD_EINVAL;
+    if (s.rows == 0)
+        return DETFOLD_OK;
+    if (s.dim > kMaxElems / s.rows || s.outs_pitch < s.rows * s.dim || s.lses_pitch < s.rows)
+        return DETFOLD_EINVAL;
+    const int64_t os = span2(s.w, s.outs_pitch, 1, 0, s.rows * s.dim);
+    const int64_t ls = span2(s.w, s.lses_pitch, 1, 0, s.rows);
+    const int size = elem_size(s.type);
+    if (os < 0 || ls < 0 || !s.out || !s.outs || !s.lses)
+        return DETFOLD_EINVAL;
+    if (!aligned(s.out, (uintptr_t)size) || !aligned(s.outs, (uintptr_t)size) || !aligned(s.lses, 4) || !aligned(s.lse, 4))
+        return DETFOLD_EINVAL;
+    const Range out = range(s.out, s.rows * s.dim, size), lse = range(s.lse, s.rows, 4);
+    const Range outs = range(s.outs, os, size), lses = range(s.lses, ls, 4);
+    if (meet(out, outs) || meet(out, lses) || meet(lse, outs) || meet(lse, lses) || meet(out, lse))
+        return DETFOLD_EOVERLAP;
+    return DETFOLD_OK;
+}
+
+}  // namespace detfold_impl
+
+using namespace detfold_impl;
+
+// ---------------------------------------------------------------------------
+// C ABI
+
+extern "C" {
+
+int detfold_cache_append(const detfold_paged_cache *cache, const detfold_append *args, void *stream)
+{
+    int rc = check_append(cache, args);
+    if (rc != DETFOLD_OK || args->tokens == 0)
+        return rc;
+    return launch_append({*cache, *args, divider((uint32_t)cache->page)}, stream);
+}
+
+int detfold_plan_attend(const detfold_paged_cache *cache, int64_t batch, int32_t q_heads, int64_t max_len,
+                        int64_t window, int32_t split, int32_t cu_count, detfold_attend_plan *plan)
+{
+    if (!plan)
+        return DETFOLD_EINVAL;
+    const int rc = check_cache(cache);
+    return rc != DETFOLD_OK ? rc : plan_attend(*cache, batch, q_heads, max_len, window, split, cu_count, plan);
+}
+
+int detfold_attend_workspace(const detfold_paged_cache *cache, int64_t batch, int32_t q_heads, int64_t max_len,
+                             int32_t split, int64_t *bytes)
+{
+    if (!bytes)
+        return DETFOLD_EINVAL;
+    detfold_attend_plan p;
+    int rc = detfold_plan_attend(cache, batch, q_heads, max_len, 0, split, 1, &p);
+    if (rc != DETFOLD_OK)
+        return rc;
+    int32_t cu = 0;
+    if ((rc = current_cu_count(&cu)) != DETFOLD_OK)
+        return rc;
+    rc = detfold_plan_attend(cache, batch, q_heads, max_len, 0, split, cu, &p);
+    *bytes = p.workspace_upto;
+    return rc;
+}
+
+int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend *args, void *stream)
+{
+    int rc = check_attend(cache, args);
+    if (rc != DETFOLD_OK || args->batch == 0)
+        return rc;
+    int32_t cu = 0;
+    if ((rc = current_cu_count(&cu)) != DETFOLD_OK)
+        return rc;
+    detfold_attend_plan p;
+    if ((rc = plan_attend(*cache, args->batch, args->q_heads, args->max_len, args->window, args->split, cu, &p)) != DETFOLD_OK)
+        return rc;
+    if (p.workspace_bytes > 0 && (!args->workspace || args->workspace_bytes < p.workspace_bytes))
+        return DETFOLD_ESIZE;
+    return launch_attend({*cache, *args, divider((uint32_t)cache->page), p.splits, p.split, args->q_heads / cache->heads}, stream);
+}
+
+int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *lse, int32_t type, int32_t W,
+                         int64_t rows, int64_t dim, int64_t outs_pitch, int64_t lses_pitch, void *stream)
+{
+    const SoftmaxArgs s = {out, outs, lses, lse, rows, dim, outs_pitch, lses_pitch, type, W};
+    const int rc = check_softmax(s);
+    if (rc != DETFOLD_OK || rows == 0)
+        return rc;
+    return launch_softmax(s, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,78 @@
+// decode.h -- declarations shared by the decode-step operators: decode.cpp
+// (host-only checks and planning, and their C ABI), cache_kernels.hip (the
+// append and the softmax fold) and attend_kernels.hip (the paged attention).
+// Not installed; the public interface is include/detfold.h.
+#ifndef DETFOLD_DECODE_H
+#define DETFOLD_DECODE_H
+
+#include <cstdint>
+
+#include "detfold.h"
+
+namespace detfold_impl {
+
+constexpr int elem_size(int type)
+{
+    return type == DETFOLD_F32 ? 4 : type == DETFOLD_E4M3 ? 1 : 2;
+}
+
+constexpr float kE4m3Max = 448.0f;
+
+// x / d for 0 <= x < 2^31 and 1 <= d < 2^31 as a multiply and a shift: with
+// s = ceil(log2 d) and m = ceil(2^(31+s) / d) (below 2^32), x * m >> (31 + s)
+// is exact, since m * d exceeds 2^(31+s) by less than d <= 2^s.
+struct Divider {
+    uint32_t magic, shift, d;
+};
+
+inline Divider divider(uint32_t d)
+{
+    uint32_t s = 0;
+    while (((uint64_t)1 << s) < d)
+        ++s;
+    const uint64_t m = (((uint64_t)1 << (31 + s)) + d - 1) / d;
+    return {(uint32_t)m, 31 + s, d};
+}
+
+// Kernel arguments of the append: the two public structs, and what the host
+// derives from them.
+struct AppendArgs {
+    detfold_paged_cache c;
+    detfold_append a;
+    Divider page;
+};
+
+struct AttendArgs {
+    detfold_paged_cache c;
+    detfold_attend a;
+    Divider page;
+    int64_t splits, split;  // parts of a row and tokens of one
+    int32_t group;          // query heads of a key-value head
+};
+
+struct SoftmaxArgs {
+    void *out;
+    const void *outs;
+    const float *lses;
+    float *lse;
+    int64_t rows, dim, outs_pitch, lses_pitch;
+    int32_t type, w;
+};
+
+// --- decode.cpp: host only, no device access ---------------------------------
+bool types_pair(int32_t type, int32_t cache_type);
+int check_cache(const detfold_paged_cache *c);
+int check_append(const detfold_paged_cache *c, const detfold_append *a);
+int check_attend(const detfold_paged_cache *c, const detfold_attend *a);
+int check_softmax(const SoftmaxArgs &s);
+int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
+                int64_t window, int32_t split, int32_t cu_count, detfold_attend_plan *p);
+
+// --- cache_kernels.hip, attend_kernels.hip: launches --------------------------
+int launch_append(const AppendArgs &a, void *stream);
+int launch_softmax(const SoftmaxArgs &s, void *stream);
+int launch_attend(const AttendArgs &a, void *stream);
+
+}  // namespace detfold_impl
+
+#endif  // DETFOLD_DECODE_H

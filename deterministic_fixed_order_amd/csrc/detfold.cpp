@@ -21,6 +21,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_cu_count[kMaxDevices];
 
+}  // namespace
+
 int current_cu_count(int32_t *cu)
 {
     int dev = -1;
@@ -41,6 +43,8 @@ int current_cu_count(int32_t *cu)
     *cu = c;
     return DETFOLD_OK;
 }
+
+namespace {
 
 int run_ranks(float *out, const float *stacked, int32_t W, int64_t len, bool scaled, float inv_w,
               const detfold_launch *ovr, void *stream, void *begin = nullptr, void *done = nullptr)
@@ -385,7 +389,7 @@ const char *detfold_strerror(int rc)
     case DETFOLD_ELAUNCH: return "HIP kernel launch failed";
     case DETFOLD_EDEVICE: return "no usable current HIP device";
     case DETFOLD_ESIZE: return "request exceeds the library's static stage "
-                               "(DETFOLD_STATIC_STAGE_FLOATS floats)";
+                               "(DETFOLD_STATIC_STAGE_FLOATS floats) or the caller's workspace";
     case DETFOLD_ECAPTURE: return "the pair link's streams are being captured into a graph, "
                                   "which the pair link does not support";
     default: return "unknown detfold return code";

@@ -309,6 +309,10 @@ int launch_one_shot(const OneShotArgs &a, int nranks, void *stream);
 int static_stage(float **stage);
 int launch_zero_words(uint32_t *p, int64_t n, void *stream);
 
+// --- detfold.cpp -------------------------------------------------------------
+// The current device's compute units (cached per device), or DETFOLD_EDEVICE.
+int current_cu_count(int32_t *cu);
+
 }  // namespace detfold_impl
 
 #endif  // DETFOLD_INTERNAL_H

@@ -52,7 +52,7 @@ extern "C" {
 #define DETFOLD_EOVERLAP 2 /* output range overlaps an input range it must not alias     */
 #define DETFOLD_ELAUNCH 3  /* the HIP launch was refused                                 */
 #define DETFOLD_EDEVICE 4  /* no current HIP device, or its properties could not be read */
-#define DETFOLD_ESIZE 5    /* the request needs more than the library's static stage     */
+#define DETFOLD_ESIZE 5    /* the request needs more than the static stage or workspace  */
 #define DETFOLD_ECAPTURE 6 /* a pair-link stream is being captured into a graph         */
 
 /*
@@ -363,6 +363,175 @@ int detfold_one_shot_all_reduce(const detfold_one_shot_link *link, float *x0, fl
  */
 int detfold_one_shot_rank(const detfold_one_shot_link *link, int32_t rank, float *x, int64_t n,
                           void *stream);
+
+/* ------------------------------------------------------------------------
+ * The decode step around the fold: a paged key-value cache, the append that
+ * fills it, the attention of one new token over it, and the fixed-order join
+ * of attention partials.
+ *
+ * Types of the buffers these calls take (DETFOLD_E4M3: 8-bit floats of 4
+ * exponent and 3 mantissa bits, no infinity, largest value 448).
+ */
+#define DETFOLD_F32 0
+#define DETFOLD_BF16 1
+#define DETFOLD_F16 2
+#define DETFOLD_E4M3 3 /* caches only */
+
+/* Head sizes the paged cache takes. */
+#define DETFOLD_MIN_HEAD 16
+#define DETFOLD_MAX_HEAD 256
+
+/*
+ * A paged cache: `pages` pages of `page` token slots each; slot s of the cache
+ * is token s % page of page s / page, and holds `heads` key heads of `dim`
+ * values and value heads of `v_dim`.  Strides are in elements; a head's values
+ * are contiguous, so a page may lie token-major ([page][heads][dim]) or
+ * head-major ([heads][page][dim]).  A plain host struct: the calls read it and
+ * keep no pointer to it.
+ *   type      F32, BF16, F16 or E4M3, of keys and values alike
+ *   k_scale,  device, `heads` floats each, E4M3 only (NULL = 1): a stored
+ *   v_scale   value v of head h stands for v * scale[h]
+ * A query or appended key/value may be of the cache's own type; an E4M3 cache
+ * takes F32, BF16 and F16, a BF16 cache F32 too.
+ */
+typedef struct detfold_paged_cache {
+    void *k, *v;                     /* device */
+    const float *k_scale, *v_scale;  /* device or NULL */
+    int64_t pages;                   /* >= 1; pages * page below 2^31 */
+    int64_t k_page, k_token, k_head; /* elements from one page, token, head to the next */
+    int64_t v_page, v_token, v_head;
+    int32_t page;       /* token slots of a page, >= 1 */
+    int32_t heads;      /* key-value heads, >= 1 */
+    int32_t dim, v_dim; /* DETFOLD_MIN_HEAD .. DETFOLD_MAX_HEAD */
+    int32_t type;
+    int32_t reserved;   /* 0 */
+} detfold_paged_cache;
+
+/*
+ * detfold_cache_append -- write the keys and values of `tokens` new tokens into
+ * their cache slots, the position rotation applied to the keys and, where q is
+ * given, to the queries on the way.
+ *
+ * With rot > 0 the first `rot` values of a key or query head turn by the
+ * angles of the token's position p: value i and its partner j (i + rot/2, or,
+ * with pairs, 2i and 2i + 1) become
+ *     x_i * cos[p][i] - x_j * sin[p][i]   and   x_j * cos[p][i] + x_i * sin[p][i],
+ * each product and sum one binary32 rounding, rounded once to the type they are
+ * stored in; the values beyond rot are copied.  An E4M3 cache stores
+ * x / scale[h], one binary32 division, clamped to +-448 (a NaN stays one).
+ *   slots      device, int64: each token's slot.  A token whose slot is
+ *              negative or past the cache is not stored (padding of a batch);
+ *              its query still turns.  Two tokens of one call must not share
+ *              a slot
+ *   positions  device, int64; needed with rot > 0.  A position outside the
+ *              table of angles turns its token into NaN
+ *   cos, sin   device, [angles][rot / 2] floats; needed with rot > 0
+ *   q, q_out   device, [tokens][q_heads][dim]; both NULL when q_heads = 0.
+ *              q_out may be q itself (same strides) and else overlaps nothing
+ *   type       of k, v, q and q_out
+ * Strides are in elements; values of a head are contiguous.
+ * Errors: DETFOLD_EINVAL (also for types that do not go together), DETFOLD_EOVERLAP,
+ * DETFOLD_EDEVICE, DETFOLD_ELAUNCH.
+ */
+typedef struct detfold_append {
+    const void *k, *v, *q;
+    void *q_out;
+    const int64_t *slots, *positions;
+    const float *cos, *sin;
+    int64_t tokens, angles;
+    int64_t k_token, k_head, v_token, v_head, q_token, q_head, out_token, out_head;
+    int32_t type, q_heads, rot;
+    int32_t pairs; /* 0: value i turns with i + rot/2; 1: 2i with 2i + 1 */
+} detfold_append;
+int detfold_cache_append(const detfold_paged_cache *cache, const detfold_append *args, void *stream);
+
+/*
+ * detfold_attend_paged -- attention of one new token per row over the cache:
+ * query head g of row b attends over the row's tokens t through key-value head
+ * h = g / (q_heads / heads):
+ *     s_t = scale * (q . k_t),  lse = log(sum_t exp(s_t)),
+ *     out = sum_t exp(s_t - lse) v_t.
+ * A row sees its tokens [0, lens[b]), or with window > 0 the last `window` of
+ * them; token t lies in slot t % page of page table[b][t / page].  A row
+ * without a token gives out = 0 and lse = -infinity.  Slots that a row does
+ * not see are never part of its result, whatever they hold, and table entries
+ * past the row's last page are not read.
+ *
+ * Scores, the running maximum, the sum and the output are held in binary32.
+ * Two calls with equal arguments give equal bits: the cache's length is split
+ * over workgroups by a rule on the arguments and the device alone, and the
+ * parts are joined in ascending order of their tokens.  With `split` set the
+ * rule is the caller's, and a row's bits do not depend on the other rows, the
+ * batch or max_len.
+ *   lens      device, int32.  A negative length counts as 0; a length beyond
+ *             max_len or the table, or a page outside the cache, gives NaN in
+ *             that row's out and lse (nothing outside the cache is read)
+ *   max_len   an upper bound of lens, known on the host
+ *   lse       device, [batch][q_heads] floats, or NULL
+ *   q_heads   a multiple of the cache's heads
+ *   out_type  the type of q, or F32
+ *   split     tokens of one part: 0 = the plan's choice, else a multiple of
+ *             DETFOLD_ATTEND_STEP
+ *   workspace device memory of at least the plan's bytes, 16-byte
+ *             aligned, not shared by calls that overlap in time; its contents
+ *             before and after a call mean nothing
+ * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP (out or lse with another buffer),
+ * DETFOLD_ESIZE (workspace too small), DETFOLD_EDEVICE, DETFOLD_ELAUNCH.
+ */
+#define DETFOLD_ATTEND_STEP 32
+typedef struct detfold_attend {
+    void *out;
+    const void *q;
+    float *lse;
+    const int32_t *table, *lens;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t batch, max_len, window;
+    int64_t table_row, table_width; /* entries from one row to the next, and of a row */
+    int64_t q_row, q_head, out_row, out_head;
+    float scale;
+    int32_t type, out_type, q_heads;
+    int32_t split;
+    int32_t reserved; /* 0 */
+} detfold_attend;
+int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend *args, void *stream);
+
+/* How a call is split (host only; nothing is dereferenced). */
+typedef struct detfold_attend_plan {
+    int64_t units;           /* rows times groups of query heads that share the cache reads */
+    int64_t splits;          /* parts of a row's length */
+    int64_t split;           /* tokens of a part */
+    int64_t workspace_bytes; /* what this call needs: 0 where every row is one part */
+    int64_t workspace_upto;  /* what every call of this split needs whose batch and max_len are
+                                at most these, with any window */
+} detfold_attend_plan;
+int detfold_plan_attend(const detfold_paged_cache *cache, int64_t batch, int32_t q_heads,
+                        int64_t max_len, int64_t window, int32_t split, int32_t cu_count,
+                        detfold_attend_plan *plan);
+
+/* workspace_upto of that plan on the current device. */
+int detfold_attend_workspace(const detfold_paged_cache *cache, int64_t batch, int32_t q_heads,
+                             int64_t max_len, int32_t split, int64_t *bytes);
+
+/*
+ * detfold_fold_softmax -- the fixed-order join of W attention partials, each
+ * the softmax-weighted mean outs_w of its own tokens with lse_w the logarithm
+ * of its sum of exponentials (the ranks of a cache split over its length):
+ *     top = max_w lse_w,  a_w = exp(lse_w - top),  l = a_0 + a_1 + ... ,
+ *     out[i] = ((a_0 * outs_0[i] + a_1 * outs_1[i]) + ...) / l,  lse = top + log(l),
+ * strictly ascending in w and held in binary32, so the bits do not depend on
+ * the launch.  A partial with lse_w = -infinity had no token: it adds nothing,
+ * whatever its outs hold.  Where no partial had one, out = 0 and lse = -infinity.
+ *   outs   device, partial w at outs + w * outs_pitch, [rows][dim] contiguous
+ *   lses   device, partial w at lses + w * lses_pitch, [rows]
+ *   out    device, [rows][dim], of the type of outs;  lse  device, [rows] or NULL
+ *   type   DETFOLD_F32, _BF16 or _F16
+ *   W >= 1; pitches in elements, at least rows * dim and rows
+ * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP, DETFOLD_EDEVICE, DETFOLD_ELAUNCH.
+ */
+int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *lse, int32_t type,
+                         int32_t W, int64_t rows, int64_t dim, int64_t outs_pitch,
+                         int64_t lses_pitch, void *stream);
 
 /* Static, NUL-terminated description of a return code (never NULL). */
 const char *detfold_strerror(int rc);
