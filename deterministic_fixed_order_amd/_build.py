@@ -45,8 +45,9 @@ KERNELS = os.path.join(CSRC, "fold_kernels.hip")
 HOST_SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "detfold.cpp")]
 SOURCES = [KERNELS] + HOST_SOURCES
 INTERNAL_HEADER = os.path.join(CSRC, "internal.h")
-DECODE_KERNELS = [os.path.join(CSRC, f) for f in ("cache_kernels.hip", "attend_kernels.hip")]
-DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_device.h")]
+DECODE_KERNELS = [os.path.join(CSRC, f) for f in ("cache_kernels.hip", "attend_kernels.hip", "attend_f32.hip",
+                                                     "attend_f16.hip", "attend_bf16.hip")]
+DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_device.h", "attend_kernel.h")]
 EXPORTS_MAP = os.path.join(CSRC, "exports.map")
 HEADER = os.path.join(ROOT, "include", "detfold.h")
 LIB = os.path.join(PKG, "libdetfold.so")

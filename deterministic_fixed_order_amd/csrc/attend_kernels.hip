@@ -1,95 +1,69 @@
-// attend_kernels.hip -- attention of one new token per row over a paged
-// key-value cache, for gfx950.
+// attend_kernels.hip -- the launch of the paged attention and the join of the
+// parts of long rows, for gfx950.
 
 #include <hip/hip_runtime.h>
 
-#include "decode_device.h"
+#include "attend_kernel.h"
 
 namespace detfold_impl {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds at most 2^32 threads
 
-// One workgroup per row and query head, tiles of 256 tokens: a thread scores
-// one token of the tile, then sums one value of the output over the tile.
-template <typename Q, typename C, typename O>
-__global__ __launch_bounds__(kBlock) void k_attend(AttendArgs p)
+// One workgroup per row and query head.  A wave takes every fourth part, a
+// lane four dims (heads are at most 256), and the waves' sums are added in
+// order: parts that are empty add zeros, so a row's bits do not depend on how
+// many follow its last one.
+__global__ __launch_bounds__(kBlock) void k_join_parts(AttendArgs p)
 {
     const detfold_attend &a = p.a;
-    const detfold_paged_cache &c = p.c;
-    const int64_t b = blockIdx.x / a.q_heads;
-    const int g = (int)(blockIdx.x % a.q_heads), h = g / p.group, tid = threadIdx.x;
-    __shared__ float q[DETFOLD_MAX_HEAD], w[kBlock], part[kBlock];
-    __shared__ int64_t place[kBlock];
-    for (int i = tid; i < c.dim; i += kBlock)
-        q[i] = to_f32(((const Q *)a.q)[b * a.q_row + g * a.q_head + i]);
-    const int64_t len = a.lens[b] > 0 ? a.lens[b] : 0;
-    bool bad = len > a.max_len || len > a.table_width * c.page;
-    const int64_t end = bad ? 0 : len, begin = a.window > 0 && end > a.window ? end - a.window : 0;
-    const float by = a.scale * (c.k_scale ? c.k_scale[h] : 1.0f);
-    float m = -INFINITY, l = 0.0f, acc = 0.0f;
-    for (int64_t t0 = begin; t0 < end; t0 += kBlock) {
-        const int64_t t = t0 + tid;
-        float s = -INFINITY;
-        __syncthreads();
-        if (t < end) {
-            const uint32_t at = divide((uint32_t)t, p.page);
-            const int64_t pg = a.table[b * a.table_row + at], off = t - (int64_t)at * c.page;
-            if (pg < 0 || pg >= c.pages) {
-                s = __builtin_nanf("");
-                place[tid] = 0;
-            } else {
-                const C *k = (const C *)c.k + pg * c.k_page + off * c.k_token + h * c.k_head;
-                s = 0.0f;
-                for (int i = 0; i < c.dim; ++i)
-                    s += q[i] * to_f32(k[i]);
-                s *= by;
-                place[tid] = pg * c.v_page + off * c.v_token + h * c.v_head;
-            }
-        }
-        part[tid] = s;
-        __syncthreads();
-        for (int n = kBlock / 2; n > 0; n >>= 1) {
-            if (tid < n)
-                part[tid] = fmaxf(part[tid], part[tid + n]);
-            __syncthreads();
-        }
-        const float top = fmaxf(m, part[0]), base = top == -INFINITY ? 0.0f : top;
-        const float turn = expf(m - base);
-        w[tid] = expf(s - base);
-        __syncthreads();
-        part[tid] = w[tid];
-        __syncthreads();
-        for (int n = kBlock / 2; n > 0; n >>= 1) {
-            if (tid < n)
-                part[tid] += part[tid + n];
-            __syncthreads();
-        }
-        l = l * turn + part[0];
-        m = top;
-        acc *= turn;
-        const int64_t count = end - t0 < kBlock ? end - t0 : kBlock;
-        if (tid < c.v_dim)
-            for (int i = 0; i < count; ++i)
-                acc += w[i] * to_f32(((const C *)c.v + place[i])[tid]);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t b = p.row0 + blockIdx.x / a.q_heads;
+    const int head = blockIdx.x % a.q_heads, n = (int)p.parts.d;
+    const int64_t g = b * a.q_heads + head;
+    const float2 *ml = p.ml + g * n;
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 64)
+        m = fmaxf(m, ml[i].x);
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1)
+        m = fmaxf(m, __shfl_xor(m, i));
+    const float base = m == -INFINITY ? 0.0f : m;
+    const int d0 = 4 * lane, d = min(d0, p.c.v_dim - 4);
+    const float *o = p.acc + g * n * p.c.v_dim + d;
+    f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+#pragma unroll 8
+    for (int i = wave; i < n; i += kBlock / 64) {
+        const float2 s = ml[i];
+        f4 x;
+        __builtin_memcpy(&x, o + (int64_t)i * p.c.v_dim, sizeof(x));
+        const float w = __builtin_amdgcn_exp2f(s.x - base);
+        l += s.y * w;
+        if (s.y == 0.0f)  // no token: its sums were not written
+            x = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        acc += x * w;
     }
-    if (bad)
-        l = __builtin_nanf("");
-    if (tid < c.v_dim) {
-        const float o = l == 0.0f ? 0.0f : acc * (c.v_scale ? c.v_scale[h] : 1.0f) / l;
-        ((O *)a.out)[b * a.out_row + g * a.out_head + tid] = from_f32<O>(o);
+    __shared__ f4 accs[kBlock / 64][64];
+    __shared__ float ls[kBlock / 64];
+    accs[wave][lane] = acc;
+    if (lane == 0)
+        ls[wave] = l;
+    __syncthreads();
+    if (wave > 0)
+        return;
+#pragma unroll
+    for (int i = 1; i < kBlock / 64; ++i) {
+        acc += accs[i][lane];
+        l += ls[i];
     }
-    if (a.lse && tid == 0)
-        a.lse[b * a.q_heads + g] = (m == -INFINITY ? 0.0f : m) + logf(l);
-}
-
-template <typename Q, typename O> const void *pick(int cache)
-{
-    if (cache == DETFOLD_E4M3)
-        return (const void *)k_attend<Q, e4m3, O>;
-    if (sizeof(Q) == 4 && cache == DETFOLD_BF16)
-        return (const void *)k_attend<Q, bf16, O>;
-    return (const void *)k_attend<Q, Q, O>;
+    const float vs = p.c.v_scale ? p.c.v_scale[head / p.group] : 1.0f;
+    const float out[4] = {attended(acc.x, vs, l), attended(acc.y, vs, l), attended(acc.z, vs, l), attended(acc.w, vs, l)};
+    if (d0 < p.c.v_dim)
+        put_out<4>(a, b * a.out_row + (int64_t)head * a.out_head + d, out);
+    if (a.lse && lane == 0)
+        a.lse[g] = log_sum(m, l);
 }
 
 }  // namespace
@@ -97,15 +71,28 @@ template <typename Q, typename O> const void *pick(int cache)
 int launch_attend(const AttendArgs &a, void *stream)
 {
     const bool wide = a.a.out_type == DETFOLD_F32;
-    const void *k = a.a.type == DETFOLD_F32    ? pick<float, float>(a.c.type)
-                    : a.a.type == DETFOLD_BF16 ? (wide ? pick<bf16, float>(a.c.type) : pick<bf16, bf16>(a.c.type))
-                                               : (wide ? pick<f16, float>(a.c.type) : pick<f16, f16>(a.c.type));
+    const int dim = a.c.dim > a.c.v_dim ? a.c.dim : a.c.v_dim;
+    const AttendKernel k = a.a.type == DETFOLD_F32    ? attend_f32(a.c.type, dim, a.tiled)
+                           : a.a.type == DETFOLD_BF16 ? attend_bf16(a.c.type, wide, dim, a.tiled)
+                                                      : attend_f16(a.c.type, wide, dim, a.tiled);
     AttendArgs copy = a;
     void *args[] = {&copy};
-    return hipLaunchKernel(k, dim3((unsigned)(a.a.batch * a.a.q_heads)), dim3(kBlock), args, 0,
-                           static_cast<hipStream_t>(stream)) == hipSuccess
-               ? DETFOLD_OK
-               : DETFOLD_ELAUNCH;
+    // Rows to a launch, whatever a row's workgroups.
+    auto rows = [&](int64_t each, const void *f, int threads, int lds) {
+        const int64_t some = each < kMaxBlocks ? kMaxBlocks / each : 1;
+        for (copy.row0 = 0; copy.row0 < a.a.batch; copy.row0 += some) {
+            const int64_t now = a.a.batch - copy.row0 < some ? a.a.batch - copy.row0 : some;
+            if (hipLaunchKernel(f, dim3((unsigned)(now * each)), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) != hipSuccess)
+                return false;
+        }
+        return true;
+    };
+    const int threads = 64 * a.waves, lds = k.q_bytes + a.waves / 2 * k.save_bytes;
+    if (!rows((int64_t)a.units.d * a.parts.d, k.f, threads, lds))
+        return DETFOLD_ELAUNCH;
+    if (a.parts.d > 1 && !rows(a.a.q_heads, (const void *)k_join_parts, kBlock, 0))
+        return DETFOLD_ELAUNCH;
+    return DETFOLD_OK;
 }
 
 }  // namespace detfold_impl

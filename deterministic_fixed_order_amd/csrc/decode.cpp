@@ -15,6 +15,8 @@ namespace {
 constexpr int64_t kMaxCount = (int64_t)1 << 31;   // counts that the kernels hold in 32 bits
 constexpr int64_t kMaxElems = (int64_t)1 << 46;   // extent of one buffer, in elements
 constexpr int32_t kMaxHeads = 1 << 16;
+constexpr int64_t kGroupsPerCu = 4;               // workgroups of the attention per compute unit
+constexpr int64_t kMinPart = 256;                 // tokens that are worth a workgroup
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
@@ -157,11 +159,42 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
     if (batch < 0 || batch >= kMaxCount || max_len < 0 || max_len >= kMaxCount || window < 0 || q_heads < 1 ||
         q_heads > kMaxHeads || q_heads % c.heads != 0 || split < 0 || split % DETFOLD_ATTEND_STEP != 0 || cu_count < 1)
         return DETFOLD_EINVAL;
-    p->units = batch * q_heads;
-    p->splits = 1;
-    p->split = max_len;
-    p->workspace_bytes = p->workspace_upto = 0;
+    const int64_t group = q_heads / c.heads, tiles = (group + 15) / 16;
+    p->units = batch * c.heads * tiles;
+    const int64_t seen = window > 0 && window < max_len ? window : max_len;
+    const int64_t full = (int64_t)cu_count * kGroupsPerCu;  // workgroups that fill the device
+    int64_t part = split > 0 ? split : kMinPart;
+    if (split == 0 && p->units > 0) {
+        const int64_t parts = (full + p->units - 1) / p->units, even = (seen + parts - 1) / parts;
+        if (even > part)
+            part = (even + DETFOLD_ATTEND_STEP - 1) / DETFOLD_ATTEND_STEP * DETFOLD_ATTEND_STEP;
+    }
+    p->splits = seen > part ? (seen + part - 1) / part : 1;
+    p->split = p->splits > 1 ? part : seen;
+    // A part leaves v_dim sums, its maximum and its sum of weights per query
+    // head; the sums come first, 16-byte aligned.
+    const int64_t rows = batch * q_heads, each = ((int64_t)c.v_dim + 2) * 4;
+    p->workspace_bytes = p->splits > 1 ? rows * p->splits * each : 0;
+    // Smaller calls: units * splits < full + units where the plan chooses, and
+    // no part but a row's last is shorter than the least.
+    const int64_t least = split > 0 ? split : kMinPart, most = (max_len + least - 1) / least;
+    const int64_t upto = rows * most, fill = p->units > 0 ? rows / p->units * (full + p->units) : 0;
+    p->workspace_upto = most > 1 ? (split > 0 || upto < fill ? upto : fill) * each : 0;
     return DETFOLD_OK;
+}
+
+// Waves of a workgroup.  With a split of the caller's always the same, since
+// the waves' sums are joined too.
+int attend_waves(const detfold_attend_plan &p, int32_t split, int32_t cu_count)
+{
+    return 4;
+}
+
+// 16 tokens from a multiple of 16 on lie in one page, and within 2^31 bytes of it.
+bool attend_tiled(const detfold_paged_cache &c)
+{
+    const int64_t far = ((int64_t)1 << 31) / 16 / elem_size(c.type) - DETFOLD_MAX_HEAD;
+    return c.page % 16 == 0 && c.k_token < far && c.v_token < far;
 }
 
 int check_attend(const detfold_paged_cache *c, const detfold_attend *a)
@@ -282,7 +315,20 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
         return rc;
     if (p.workspace_bytes > 0 && (!args->workspace || args->workspace_bytes < p.workspace_bytes))
         return DETFOLD_ESIZE;
-    return launch_attend({*cache, *args, divider((uint32_t)cache->page), p.splits, p.split, args->q_heads / cache->heads}, stream);
+    AttendArgs k = {};
+    k.c = *cache;
+    k.a = *args;
+    k.group = args->q_heads / cache->heads;
+    k.page = divider((uint32_t)cache->page);
+    k.tiles = divider((uint32_t)(k.group + 15) / 16);
+    k.units = divider((uint32_t)cache->heads * k.tiles.d);
+    k.parts = divider((uint32_t)p.splits);
+    k.split = p.split;
+    k.tiled = attend_tiled(*cache);
+    k.waves = attend_waves(p, args->split, cu);
+    k.acc = (float *)args->workspace;
+    k.ml = (float2 *)(k.acc + args->batch * args->q_heads * p.splits * cache->v_dim);
+    return launch_attend(k, stream);
 }
 
 int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *lse, int32_t type, int32_t W,

@@ -5,6 +5,8 @@
 #ifndef DETFOLD_DECODE_H
 #define DETFOLD_DECODE_H
 
+#include <hip/hip_vector_types.h>
+
 #include <cstdint>
 
 #include "detfold.h"
@@ -46,9 +48,27 @@ struct AttendArgs {
     detfold_paged_cache c;
     detfold_attend a;
     Divider page;
-    int64_t splits, split;  // parts of a row and tokens of one
-    int32_t group;          // query heads of a key-value head
+    Divider units;  // a row's workgroups per part: key-value heads times tiles of 16 query heads
+    Divider tiles;  // the latter
+    Divider parts;  // of a row's length
+    int64_t split;  // tokens of a part
+    int64_t row0;   // first row of the launch
+    int32_t group;  // query heads of a key-value head
+    int32_t tiled;  // 16 tokens from a multiple of 16 on lie in one page
+    int32_t waves;  // of a workgroup
+    float *acc;     // the parts' sums [batch][q_heads][parts][v_dim], where there are several
+    float2 *ml;     // and their maxima and sums of weights [batch][q_heads][parts]
 };
+
+// A kernel of the attention and the LDS it takes: for the queries, and for
+// each pair of waves.
+struct AttendKernel {
+    const void *f;
+    int q_bytes, save_bytes;
+};
+AttendKernel attend_bf16(int cache, bool wide, int dim, bool tiled);
+AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled);
+AttendKernel attend_f32(int cache, int dim, bool tiled);
 
 struct SoftmaxArgs {
     void *out;
@@ -67,6 +87,8 @@ int check_attend(const detfold_paged_cache *c, const detfold_attend *a);
 int check_softmax(const SoftmaxArgs &s);
 int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
                 int64_t window, int32_t split, int32_t cu_count, detfold_attend_plan *p);
+int attend_waves(const detfold_attend_plan &p, int32_t split, int32_t cu_count);
+bool attend_tiled(const detfold_paged_cache &c);
 
 // --- cache_kernels.hip, attend_kernels.hip: launches --------------------------
 int launch_append(const AppendArgs &a, void *stream);
