@@ -88,11 +88,46 @@ template <typename F> __device__ __forceinline__ float over_groups(float x, F f)
     return f(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
 }
 
-template <typename T> __device__ __forceinline__ float read_q(const void *q, int64_t i) { return to_f32(((const T *)q)[i]); }
+// A uniform read of what no kernel writes meanwhile.  As a vector load it
+// would be counted with the loads of the cache, in order, and waiting for it
+// would wait for them.
+__device__ __forceinline__ int32_t scalar_load(const int32_t *p) { return *(const __attribute__((address_space(4))) int32_t *)p; }
 
-// The ends of a row: its output from the sums, the logarithm of its weights'
-// sum (m is in units of log 2), and the store of N values.
-__device__ __forceinline__ float attended(float acc, float v_scale, float l) { return l == 0.0f ? 0.0f : acc * v_scale / l; }
+__device__ __forceinline__ int64_t from_lane(int64_t x, int l)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)x), hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// The kernel's arguments, read anew: held across a loop they would fill the
+// scalar registers, and then vector ones.
+typedef const __attribute__((address_space(4))) AttendArgs *ArgsPtr;
+__device__ __forceinline__ const AttendArgs &arguments()
+{
+    uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const AttendArgs *)(ArgsPtr)p;
+}
+
+// The same value, of which the compiler knows nothing: what is computed from it
+// in a loop is not held in registers across it.
+template <typename T> __device__ __forceinline__ T anew(T x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// The bits of the j-th of some words that lie n bytes or more from the start.
+__device__ __forceinline__ uint32_t keep_from(int n, int j)
+{
+    const int bits = 8 * n - 32 * j;
+    return bits >= 32 ? 0u : bits > 0 ? ~0u << bits : ~0u;
+}
+
+// The ends of a row: what its sums are multiplied by (one division a row; a
+// row without a token gives 0), the logarithm of its weights' sum (m is in
+// units of log 2), and the store of N values.
+__device__ __forceinline__ float out_scale(float v_scale, float l) { return l == 0.0f ? 0.0f : v_scale / l; }
 __device__ __forceinline__ float log_sum(float m, float l) { return (m == -INFINITY ? 0.0f : m * kLn2) + logf(l); }
 template <int N> __device__ __forceinline__ void put_out(const detfold_attend &a, int64_t at, const float (&o)[N])
 {
@@ -117,77 +152,128 @@ template <int N> __device__ __forceinline__ void put_out(const detfold_attend &a
     }
 }
 
+// The tokens of a row that are seen, in units of kUnit from a0 on (a row without
+// any counts as one, so that someone writes its output).
+struct RowTokens {
+    uint32_t begin, end, a0, steps;
+    bool bad;  // longer than the call or the table allows
+};
+__device__ __forceinline__ RowTokens row_tokens(const detfold_attend &a, const detfold_paged_cache &c, int32_t len, bool tiled)
+{
+    const int64_t n = len > 0 ? len : 0;
+    RowTokens r;
+    r.bad = n > a.max_len || n > a.table_width * c.page;
+    r.end = r.bad ? 0 : (uint32_t)n;
+    r.begin = a.window > 0 && r.end > a.window ? (uint32_t)(r.end - a.window) : 0;
+    r.a0 = tiled ? r.begin & ~15u : r.begin;
+    r.steps = r.end > r.begin ? (r.end - r.a0 + kUnit - 1) / kUnit : 1;
+    return r;
+}
+
+// An even share of all rows' units, found by every wave from the lengths:
+// share y of p.shares has the units [y * each, (y + 1) * each) of the rows laid
+// end to end.
+struct Share {
+    uint32_t left, at, row_at, each;  // units left, the next one, its row's first one, those of a share
+    int64_t row;
+};
+__device__ __forceinline__ Share find_share(const AttendArgs &p, uint32_t y, bool tiled)
+{
+    const int lane = threadIdx.x & 63, batch = (int)p.a.batch;
+    auto units = [&](int i) { return i < batch ? row_tokens(p.a, p.c, p.a.lens[i], tiled).steps : 0u; };
+    uint32_t own = units(lane), total = own;
+    for (int i = lane + 64; i < batch; i += 64)
+        total += units(i);
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1)
+        total += __shfl_xor(total, i);
+    total = __builtin_amdgcn_readfirstlane(total);
+    Share w = {};
+    w.each = max((uint32_t)kMinShare, (total + p.shares - 1) / p.shares);
+    w.at = y * w.each;
+    if (w.at >= total)
+        return w;
+    w.left = min(w.each, total - w.at);
+    uint32_t before = 0;
+    for (int i = 0; i < batch; i += 64) {
+        uint32_t upto = own;
+#pragma unroll
+        for (int n = 1; n < 64; n <<= 1) {
+            const uint32_t other = __shfl_up(upto, n);
+            upto += lane >= n ? other : 0;
+        }
+        const uint64_t past = __ballot(before + upto > w.at);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            w.row = i + at;
+            w.row_at = before + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(own, at);
+            break;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+        own = units(i + 64 + lane);
+    }
+    return w;
+}
+
 template <typename C, int QK, int PV, int D, bool TILED> struct Attend {
     static constexpr int kSize = sizeof(C);
     static constexpr int kChunk = 16 / kSize;         // dims of one 16-byte load of a key
     static constexpr int kChunks = D / (4 * kChunk);  // of these per lane and key
-    static constexpr int kTiles = kSize == 4 && D == 256 ? 1 : 2;  // tiles of 16 tokens in a step
+    static constexpr int kFit = 1024 / (D * kSize);   // tiles of 16 tokens whose keys take 64 registers
+    static constexpr int kMost = D < 256 ? 4 : QK == kF32 ? 1 : 2;
+    static constexpr int kTiles = kFit < kMost ? kFit : kMost;  // of a step
     static constexpr int kStep = 16 * kTiles;
     static constexpr int kWide = D >= 128 ? 8 : 4;    // dims of a value that a lane holds together
     static constexpr int kParts = D / (16 * kWide);
     static constexpr int kTokens = 4 * kTiles;        // tokens whose values a lane loads
     static constexpr int kQ = (QK == kF32 ? 4 : 2) * D * 16;  // LDS bytes of the queries
-    static constexpr int kAcc = D / 16;               // f4 of the output a lane holds
-    static constexpr int kSave = kAcc * 1024 + 512;   // LDS bytes of one wave's state
-    static constexpr int lds(int waves) { return kQ + waves / 2 * kSave; }
+    static constexpr int kRow = D + 4;                // floats of a query head's sums in LDS: heads on other banks
 
-    static_assert(kTiles == 2 || PV == kF32, "the 16-bit products take 32 tokens");
+    static_assert(kTiles % 2 == 0 || PV == kF32, "the 16-bit products take 32 tokens");
 };
 
 template <typename C, int QK, int PV, int D, bool TILED>
-__global__ __launch_bounds__(512) void k_attend(AttendArgs p)
+__global__ __launch_bounds__(512) void k_attend(AttendArgs)
 {
     typedef Attend<C, QK, PV, D, TILED> S;
     constexpr int CS = S::kSize, E = S::kChunk, NC = S::kChunks, UT = S::kTiles, VW = S::kWide, NP = S::kParts, NT = S::kTokens;
     extern __shared__ __align__(16) char lds[];
-    const detfold_attend &a = p.a;
-    const detfold_paged_cache &c = p.c;
-    const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const uint32_t per_row = divide(blockIdx.x, p.units), unit = blockIdx.x - per_row * p.units.d;
-    const uint32_t row = divide(per_row, p.parts), part = per_row - row * p.parts.d;
-    const uint32_t h = divide(unit, p.tiles), tile = unit - h * p.tiles.d;
-    const int64_t b = p.row0 + row;
-    const int head0 = (int)(h * p.group + 16 * tile);
-    const int live = min(16, p.group - 16 * (int)tile);
+    const AttendArgs &p0 = arguments();
+    const uint32_t y = divide(blockIdx.x, p0.units);
+    // A wave takes one of the workgroup's units, or one of several turns at it.
+    const int beside = p0.beside, in = wave & (beside - 1), turn = wave / beside, turns = waves / beside;
+    const uint32_t unit = (blockIdx.x - y * p0.units.d) * beside + in;
 
-    // The tokens of this part.
-    const int32_t want = a.lens[b];
-    const int64_t len = want > 0 ? want : 0;
-    bool bad = len > a.max_len || len > a.table_width * c.page;
-    const int64_t all = bad ? 0 : len, first = a.window > 0 && all > a.window ? all - a.window : 0;
-    const uint32_t begin = (uint32_t)min(all, first + part * p.split), end = (uint32_t)min(all, first + (part + 1) * p.split);
-    const uint32_t a0 = TILED ? begin & ~15u : begin, last = end > 0 ? end - 1 : 0;
-    const uint32_t steps = end > begin ? (end - a0 + S::kStep - 1) / S::kStep : 0;
-
-    // The queries as the operand of the score products, one lane's 16 bytes
-    // after the other; a chunk that would pass the head's end starts earlier,
-    // and what it repeats counts as zero.
-    {
-        constexpr int per = QK == kF32 ? 4 : 8;
-        for (int i = threadIdx.x; i < D * 64 / (4 * per); i += blockDim.x) {
-            const int l = i & 63, f = i >> 6;
-            const int at = f * per / E, e0 = f * per % E, c0 = E * (4 * at + (l >> 4)), s = min(c0, c.dim - E);
-            const int64_t q0 = b * a.q_row + (int64_t)(head0 + min(l & 15, live - 1)) * a.q_head + s + e0;
-            float x[per];
-#pragma unroll
-            for (int e = 0; e < per; ++e) {
-                const float v = QK == kF32 ? read_q<float>(a.q, q0 + e) : QK == kBf16 ? read_q<bf16>(a.q, q0 + e) : read_q<f16>(a.q, q0 + e);
-                x[e] = s + e0 + e >= c0 && (l & 15) < live ? v : 0.0f;
-            }
-            if constexpr (QK == kF32)
-                ((f4 *)lds)[i] = f4{x[0], x[1], x[2], x[3]};
-            else if constexpr (QK == kBf16)
-                ((bf16x8 *)lds)[i] = bf16x8{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3], (bf16)x[4], (bf16)x[5], (bf16)x[6], (bf16)x[7]};
-            else
-                ((f16x8 *)lds)[i] = f16x8{(f16)x[0], (f16)x[1], (f16)x[2], (f16)x[3], (f16)x[4], (f16)x[5], (f16)x[6], (f16)x[7]};
-        }
+    // The work of this workgroup: one part of one row, or its even share of the
+    // steps of all rows, which may begin and end within one.
+    int64_t b;
+    uint32_t part = 0;
+    Share mine = {};
+    if (p0.shares) {
+        mine = find_share(p0, y, TILED);
+        if (mine.left == 0)
+            return;
+        b = mine.row;
+    } else {
+        const uint32_t row = divide(y, p0.parts);
+        part = y - row * p0.parts.d;
+        b = p0.row0 + row;
     }
 
-    const int32_t *table = a.table + b * a.table_row;
+    for (;;) {
+    const AttendArgs &p = arguments();
+    const detfold_attend &a = p.a;
+    const detfold_paged_cache &c = p.c;
+    const int lane = anew((int)threadIdx.x & 63), col = lane & 15, grp = lane >> 4;
+    const uint32_t h = divide(unit, p.tiles), tile = unit - h * p.tiles.d;
+    const int head0 = (int)(h * p.group + 16 * tile);
+    const int live = min(16, p.group - 16 * (int)tile);
     const char *k0 = (const char *)c.k + (int64_t)h * c.k_head * CS, *v0 = (const char *)c.v + (int64_t)h * c.v_head * CS;
     const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
     const uint32_t pages = (uint32_t)c.pages;
+    const float by = a.scale * (c.k_scale ? c.k_scale[h] : 1.0f) * kLog2e;
+    const bool ragged = c.dim % (4 * E) != 0;
 
     // Where a lane's loads lie within a key and a value.
     uint32_t k_at[NC], v_at[NP];
@@ -198,34 +284,61 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
     for (int i = 0; i < NP; ++i)
         v_at[i] = (uint32_t)min(VW * (16 * i + col), c.v_dim - VW) * CS + (TILED ? 4 * grp * (uint32_t)v_token : 0);
 
-    // The table's entries of a step: one per tile where tiles lie within a
-    // page, else one per token that this lane loads.  Tokens past the part are
-    // taken from its last ones, and masked.
-    int32_t id_k[UT], id_v[TILED ? 1 : NT];
-    uint32_t off_k[UT], off_v[TILED ? 1 : NT];
+    const RowTokens row = row_tokens(a, c, scalar_load(a.lens + b), TILED);
+    bool bad = row.bad;
+    uint32_t begin = row.begin, end = row.end, done = 0;
+    int64_t slot = -1;  // where the sums of this part go if the row has others
+    if (p.shares) {
+        const uint32_t x = mine.at - mine.row_at;
+        done = min(row.steps - x, mine.left);
+        if (done < row.steps)
+            slot = ((int64_t)y * (p.units.d * beside) + unit) * 2 + (x == 0);
+        if (x == 0 && unit == 0 && lane == 0 && turn == 0)
+            p.cut[b] = make_int2((int)y, (int)((mine.at + row.steps - 1) / mine.each));
+        end = x + done < row.steps ? row.a0 + kUnit * (x + done) : end;
+        begin = x ? row.a0 + kUnit * x : begin;
+    } else if (p.parts.d > 1) {
+        slot = (b * p.parts.d + part) * (p.units.d * beside) + unit;
+        const int64_t x = begin + part * p.split;
+        begin = (uint32_t)min(x, (int64_t)end), end = (uint32_t)min(x + p.split, (int64_t)end);
+    }
+    const uint32_t a0 = TILED ? begin & ~15u : begin, last = end > 0 ? end - 1 : 0;
+    const uint32_t steps = end > begin ? (end - a0 + S::kStep - 1) / S::kStep : 0;
+
+    // The queries as the operand of the score products, one lane's 16 bytes
+    // after the other; a chunk that would pass the head's end starts earlier,
+    // and what it repeats counts as zero.
+    char *const queries = lds + in * S::kQ;
+    constexpr int QS = QK == kF32 ? 4 : 2, PER = 16 / QS, NQ = D / (4 * PER);
+    const char *q = (const char *)a.q + (b * a.q_row + (int64_t)(head0 + min(col, live - 1)) * a.q_head) * QS;
+    auto query_chunk = [&](int i) { return E * (4 * (i * PER / E) + grp); };
+    Words<16> qw[NQ] = {};
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+        if ((i & (turns - 1)) == turn)
+            __builtin_memcpy(&qw[i], q + (min(query_chunk(i), c.dim - E) + i * PER % E) * QS, 16);
+
+    const int32_t *table = a.table + b * a.table_row;
+    // The pages of a step's tokens, looked up two steps ahead of the products:
+    // where tiles lie within a page one scalar each, else one per lane and
+    // token, handed to the lanes that load it when it is used.  Tokens past the
+    // part are taken from its last ones, and masked.
+    constexpr int IDS = TILED ? UT : 1;
+    const uint32_t own = lane & (S::kStep - 1);
+    struct Pages {
+        int32_t id[IDS];
+        uint32_t off[IDS];
+    };
     auto look_up = [&](uint32_t s) {
         const uint32_t t0 = a0 + s * S::kStep;
-        if constexpr (TILED) {
+        Pages g;
 #pragma unroll
-            for (int u = 0; u < UT; ++u) {
-                const uint32_t t = min(t0 + 16 * u, last & ~15u), n = divide(t, p.page);
-                id_k[u] = table[n];
-                off_k[u] = t - n * p.page.d;
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < UT; ++u) {
-                const uint32_t t = min(t0 + 16 * u + col, last), n = divide(t, p.page);
-                id_k[u] = table[n];
-                off_k[u] = t - n * p.page.d;
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint32_t t = min(t0 + 16 * (j / 4) + 4 * grp + j % 4, last), n = divide(t, p.page);
-                id_v[j] = table[n];
-                off_v[j] = t - n * p.page.d;
-            }
+        for (int u = 0; u < IDS; ++u) {
+            const uint32_t t = TILED ? min(t0 + 16 * u, last & ~15u) : min(t0 + own, last), n = divide(t, p.page);
+            g.id[u] = TILED ? scalar_load(table + n) : table[n];
+            g.off[u] = t - n * p.page.d;
         }
+        return g;
     };
     auto valid = [&](int32_t id) {  // the page, 0 for one that is none
         const bool no = (uint32_t)id >= pages;
@@ -235,28 +348,32 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
 
     Words<16> kw[UT][NC];
     Words<VW * CS> vw[NT][NP];
-    auto load_keys = [&] {
+    auto load_keys = [&](const Pages &g) {
+        int64_t at = 0;
+        if (!TILED)
+            at = valid(g.id[0]) * k_page + g.off[0] * k_token;
 #pragma unroll
         for (int u = 0; u < UT; ++u) {
-            const char *at = k0 + valid(id_k[u]) * k_page + off_k[u] * k_token;
+            const char *k = k0 + (TILED ? valid(g.id[u % IDS]) * k_page + g.off[u % IDS] * k_token : from_lane(at, 16 * u + col));
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                kw[u][i] = load_words<16>(at + k_at[i]);
+                kw[u][i] = load_words<16>(k + anew(k_at[i]));
         }
     };
-    auto load_values = [&] {
+    auto load_values = [&](const Pages &g) {
+        int64_t at = 0;
+        if (!TILED)
+            at = valid(g.id[0]) * v_page + g.off[0] * v_token;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const char *at = TILED ? v0 + valid(id_k[j / 4]) * v_page + (off_k[j / 4] + j % 4) * v_token
-                                   : v0 + valid(id_v[j]) * v_page + off_v[j] * v_token;
+            const char *v = v0 + (TILED ? valid(g.id[j / 4 % IDS]) * v_page + (g.off[j / 4 % IDS] + j % 4) * v_token
+                                        : from_lane(at, 16 * (j / 4) + 4 * grp + j % 4));
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                vw[j][i] = load_words<VW * CS>(at + v_at[i]);
+                vw[j][i] = load_words<VW * CS>(v + anew(v_at[i]));
         }
     };
 
-    const float by = a.scale * (c.k_scale ? c.k_scale[h] : 1.0f) * kLog2e;
-    const bool ragged = c.dim % (4 * E) != 0;
     // Weights of 16-bit floats are held 2^15 times larger, so that small ones
     // keep their digits; the sum is too, and both are put right at the end.
     constexpr float kLift = PV == kF16 ? 15.0f : 0.0f;
@@ -268,18 +385,44 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
         for (int j = 0; j < VW; ++j)
             acc[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    uint32_t s = wave;
+    uint32_t s = turn;
+    Pages now = {}, next = {};
+    if (s < steps)
+        now = look_up(s);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+        if ((i & (turns - 1)) == turn) {
+            const int drop = query_chunk(i) - min(query_chunk(i), c.dim - E) - i * PER % E;
+            u4 w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = col < live ? qw[i].w[j] & keep_from(drop * QS, j) : 0u;
+            *(u4 *)(queries + i * 1024 + lane * 16) = w;
+        }
+    __builtin_amdgcn_sched_barrier(0);  // else the queries' registers add to those of the loads below
     if (s < steps) {
-        look_up(s);
-        load_keys();
-        load_values();
-        if (s + waves < steps)
-            look_up(s + waves);
+        load_keys(now);
+        load_values(now);
+        now = look_up(min(s + turns, steps - 1));
     }
     __syncthreads();
-    for (; s < steps; s += waves) {
+    for (; s < steps; s += turns) {
         const uint32_t t0 = a0 + s * S::kStep;
-        const bool more = s + waves < steps;
+        const bool more = s + turns < steps;
+        const uint32_t q_at = anew(lane) * 16;
+        if (CS != 1 && ragged) {  // what a key's last chunk repeats: zero times infinity would be NaN
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int at = E * (4 * i + anew(grp)), drop = at - min(at, c.dim - E);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t keep = keep_from(CS * drop, j);
+#pragma unroll
+                    for (int u = 0; u < UT; ++u)
+                        kw[u][i].w[j] &= keep;
+                }
+            }
+        }
         // Scores: a row per token, a column per query head.
         f4 x[UT];
 #pragma unroll
@@ -287,18 +430,10 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
             x[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                if (CS != 1 && ragged) {  // what the last chunk repeats: zero times infinity would be NaN
-                    const int drop = E * (4 * i + grp) - min(E * (4 * i + grp), c.dim - E);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int bits = 8 * CS * drop - 32 * j;
-                        kw[u][i].w[j] &= bits >= 32 ? 0u : bits > 0 ? ~0u << bits : ~0u;
-                    }
-                }
                 if constexpr (QK == kF32) {
 #pragma unroll
                     for (int e = 0; e < E; e += 4) {
-                        const f4 q = ((const f4 *)lds)[(i * (E / 4) + e / 4) * 64 + lane];
+                        const f4 q = *(const f4 *)(queries + (i * (E / 4) + e / 4) * 1024 + q_at);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             x[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(kw[u][i].w, e + j), q[j], x[u], 0, 0, 0);
@@ -306,7 +441,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
                 } else {
 #pragma unroll
                     for (int e = 0; e < E; e += 8) {
-                        const u4 q = ((const u4 *)lds)[(i * (E / 8) + e / 8) * 64 + lane];
+                        const u4 q = *(const u4 *)(queries + (i * (E / 8) + e / 8) * 1024 + q_at);
                         const u4 k = {pair16<C, QK>(kw[u][i].w, e / 2), pair16<C, QK>(kw[u][i].w, e / 2 + 1),
                                       pair16<C, QK>(kw[u][i].w, e / 2 + 2), pair16<C, QK>(kw[u][i].w, e / 2 + 3)};
                         x[u] = mfma16<QK>(k, q, x[u]);
@@ -314,22 +449,33 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
                 }
             }
         }
-        if (more)
-            load_keys();
+        if (more) {
+            next = look_up(min(s + 2 * turns, steps - 1));
+            load_keys(now);
+        }
         // Weights, relative to the largest score so far.
         float top = -INFINITY;
         const bool edge = t0 < begin || t0 + S::kStep > end;
+        if (edge) {  // tokens of other parts, or none: their scores take no weight, and their values may be anything
 #pragma unroll
-        for (int u = 0; u < UT; ++u)
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t t = t0 + 16 * (j / 4) + 4 * grp + j % 4;
+                const bool out = t < begin || t >= end;
+                x[j / 4][j % 4] = out ? -INFINITY : x[j / 4][j % 4] * by;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[u][j] *= by;
-                if (edge) {
-                    const uint32_t t = t0 + 16 * u + 4 * grp + j;
-                    x[u][j] = t < begin || t >= end ? -INFINITY : x[u][j];
-                }
-                top = fmaxf(top, x[u][j]);
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int n = 0; n < VW * CS / 4; ++n)
+                        vw[j][i].w[n] = out ? 0u : vw[j][i].w[n];
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                x[j / 4][j % 4] *= by;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            top = fmaxf(top, x[j / 4][j % 4]);
         top = fmaxf(m, over_groups(top, [](float y, float z) { return fmaxf(y, z); }));
         const float base = top == -INFINITY ? 0.0f : top;
         if (__any(top > m)) {
@@ -350,18 +496,6 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
                 l += x[u][j];
             }
         // Values: the output's rows are its dims, its columns the query heads.
-        if (edge) {  // what lies beyond the row's tokens may be anything
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint32_t t = t0 + 16 * (j / 4) + 4 * grp + j % 4;
-                const bool out = t < begin || t >= end;
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int n = 0; n < VW * CS / 4; ++n)
-                        vw[j][i].w[n] = out ? 0u : vw[j][i].w[n];
-            }
-        }
         if constexpr (PV == kF32) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -371,34 +505,36 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
                     for (int n = 0; n < VW; ++n)
                         acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(vw[j][i].w, n), x[j / 4][j % 4], acc[i][n], 0, 0, 0);
         } else {
-            u4 w;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float y = x[j / 2][2 * (j % 2)], z = x[j / 2][2 * (j % 2) + 1];
-                if constexpr (PV == kBf16)
-                    w[j] = __builtin_bit_cast(uint32_t, bf16x2{(bf16)y, (bf16)z});
-                else
-                    w[j] = __builtin_bit_cast(uint32_t, f16x2{(f16)y, (f16)z});
-            }
+            for (int u = 0; u < UT; u += 2) {
+                u4 w;
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-#pragma unroll
-                for (int n = 0; n < VW; n += 2) {
-                    u4 lo, hi;  // dims n and n + 1 of the lane's eight tokens
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t y = pair16<C, PV>(vw[2 * j][i].w, n / 2), z = pair16<C, PV>(vw[2 * j + 1][i].w, n / 2);
-                        lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
-                        hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
-                    }
-                    acc[i][n] = mfma16<PV>(lo, w, acc[i][n]);
-                    acc[i][n + 1] = mfma16<PV>(hi, w, acc[i][n + 1]);
+                for (int j = 0; j < 4; ++j) {
+                    const float y = x[u + j / 2][2 * (j % 2)], z = x[u + j / 2][2 * (j % 2) + 1];
+                    if constexpr (PV == kBf16)
+                        w[j] = __builtin_bit_cast(uint32_t, bf16x2{(bf16)y, (bf16)z});
+                    else
+                        w[j] = __builtin_bit_cast(uint32_t, f16x2{(f16)y, (f16)z});
                 }
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int n = 0; n < VW; n += 2) {
+                        u4 lo, hi;  // dims n and n + 1 of the lane's eight tokens
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t y = pair16<C, PV>(vw[4 * u + 2 * j][i].w, n / 2), z = pair16<C, PV>(vw[4 * u + 2 * j + 1][i].w, n / 2);
+                            lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
+                            hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
+                        }
+                        acc[i][n] = mfma16<PV>(lo, w, acc[i][n]);
+                        acc[i][n + 1] = mfma16<PV>(hi, w, acc[i][n + 1]);
+                    }
+            }
         }
         if (more) {
-            load_values();
-            if (s + 2 * waves < steps)
-                look_up(s + 2 * waves);
+            load_values(now);
+            now = next;
         }
     }
 
@@ -414,72 +550,73 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs p)
     if (__any(bad))
         l = __builtin_nanf("");
 
-    // The waves' states, joined pairwise in a fixed order.
-    for (int n = waves / 2; n > 0; n >>= 1) {
-        char *save = lds + S::kQ + (wave < n ? wave : wave - n) * S::kSave;
-        if (wave >= n && wave < 2 * n) {
-#pragma unroll
-            for (int i = 0; i < S::kAcc; ++i)
-                ((f4 *)save)[i * 64 + lane] = acc[i / VW][i % VW];
-            ((f2 *)(save + S::kAcc * 1024))[lane] = f2{m, l};
-        }
-        __syncthreads();
-        if (wave < n) {
-            const f2 ml = ((const f2 *)(save + S::kAcc * 1024))[lane];
-            const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
-            const float mine = __builtin_amdgcn_exp2f(m - base), theirs = __builtin_amdgcn_exp2f(ml.x - base);
-            l = l * mine + ml.y * theirs;
-            m = top;
-#pragma unroll
-            for (int i = 0; i < S::kAcc; ++i)
-                acc[i / VW][i % VW] = acc[i / VW][i % VW] * mine + ((const f4 *)save)[i * 64 + lane] * theirs;
-        }
-        __syncthreads();
-    }
-    if (wave > 0 || col >= live)
-        return;
-    const int64_t g = b * a.q_heads + head0 + col;
-    if (p.parts.d > 1) {
-        const int64_t at = g * p.parts.d + part;
-        if (grp == 0)
-            p.ml[at] = make_float2(m, l);
-        if (steps == 0)
-            return;
-        float *o = p.acc + at * c.v_dim;
+    // The waves' states, joined in order: each leaves its heads' sums in LDS,
+    // over the queries, and a thread takes four dims of a head from every turn.
+    const int heads = min(16, p.group);
+    f2 *const state = (f2 *)lds;
+    float *const sums = (float *)(lds + waves * 16 * sizeof(f2));
+    __syncthreads();
+    if (col < live) {
+        float *mine = sums + (wave * heads + col) * S::kRow;
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int d0 = VW * (16 * i + 4 * grp + j), d = min(d0, c.v_dim - VW);
-                if (d0 < c.v_dim)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int n = 0; n < VW; ++n)
-                        o[d + n] = acc[i][n][j];
-            }
-        return;
+                for (int n = 0; n < VW; n += 4)
+                    *(f4 *)(mine + VW * (16 * i + 4 * grp + j) + n) = f4{acc[i][n][j], acc[i][n + 1][j], acc[i][n + 2][j], acc[i][n + 3][j]};
+        if (grp == 0)
+            state[wave * 16 + col] = f2{m, l};
     }
-    const float vs = c.v_scale ? c.v_scale[h] : 1.0f;
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int d0 = VW * (16 * i + 4 * grp + j), d = min(d0, c.v_dim - VW);
-            float o[VW];
-#pragma unroll
-            for (int n = 0; n < VW; ++n)
-                o[n] = attended(acc[i][n][j], vs, l);
-            if (d0 < c.v_dim)
-                put_out<VW>(a, b * a.out_row + (int64_t)(head0 + col) * a.out_head + d, o);
+    __syncthreads();
+    const AttendArgs &pe = arguments();
+    const float v_scale = pe.c.v_scale ? pe.c.v_scale[h] : 1.0f;
+    for (int i = 64 * turn + lane; i < live * (D / 4); i += 64 * turns) {
+        const AttendArgs &p = pe;
+        const detfold_attend &a = p.a;
+        const int head = i / (D / 4), at = i % (D / 4) * 4, at0 = at / VW * VW;
+        if (at0 >= p.c.v_dim)
+            continue;
+        float top = -INFINITY;
+        for (int w = in; w < waves; w += beside)
+            top = fmaxf(top, state[w * 16 + head].x);
+        const float base = top == -INFINITY ? 0.0f : top;
+        f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        float total = 0.0f;
+        for (int w = in; w < waves; w += beside) {
+            const f2 ml = state[w * 16 + head];
+            const float by = __builtin_amdgcn_exp2f(ml.x - base);
+            total += ml.y * by;
+            sum += *(const f4 *)(sums + (w * heads + head) * S::kRow + at) * by;
         }
-    if (a.lse && grp == 0)
-        a.lse[g] = log_sum(m, l);
+        const int64_t g = b * a.q_heads + head0 + head, from = slot * heads + head;
+        const int d = min(at0, p.c.v_dim - VW) + at - at0;
+        if (slot >= 0) {
+            __builtin_memcpy(p.acc + from * p.c.v_dim + d, &sum, sizeof(sum));
+            if (at == 0)
+                p.ml[from] = make_float2(top, total);
+        } else {
+            const float by = out_scale(v_scale, total);
+            const float o[4] = {sum.x * by, sum.y * by, sum.z * by, sum.w * by};
+            put_out<4>(a, b * a.out_row + (int64_t)(head0 + head) * a.out_head + d, o);
+            if (a.lse && at == 0)
+                a.lse[g] = log_sum(top, total);
+        }
+    }
+    mine.left -= done;
+    if (mine.left == 0)
+        return;
+    mine.at = mine.row_at = mine.at + done;
+    ++b;
+    __syncthreads();
+    }
 }
 
 // The kernel for a head size of at most D, if p says tiles lie within a page.
 template <typename C, int QK, int PV, int D> AttendKernel pick_tiled(bool tiled)
 {
     typedef Attend<C, QK, PV, D, true> S;
-    return {tiled ? (const void *)k_attend<C, QK, PV, D, true> : (const void *)k_attend<C, QK, PV, D, false>, S::kQ, S::kSave};
+    return {tiled ? (const void *)k_attend<C, QK, PV, D, true> : (const void *)k_attend<C, QK, PV, D, false>, S::kQ, S::kRow * 4};
 }
 template <typename C, int QK, int PV> AttendKernel pick_attend(int dim, bool tiled)
 {

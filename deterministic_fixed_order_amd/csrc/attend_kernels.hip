@@ -8,62 +8,89 @@
 namespace detfold_impl {
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kJoinWaves = 8;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds at most 2^32 threads
 
-// One workgroup per row and query head.  A wave takes every fourth part, a
-// lane four dims (heads are at most 256), and the waves' sums are added in
-// order: parts that are empty add zeros, so a row's bits do not depend on how
-// many follow its last one.
-__global__ __launch_bounds__(kBlock) void k_join_parts(AttendArgs p)
+// One workgroup per row and query head.  A lane takes four dims, LANES lanes a
+// part, and the groups of lanes every 512 / LANES-th part; their sums are added
+// in order.  Parts that are empty add zeros, so a row's bits do not depend on
+// how many follow its last one.
+template <int LANES> __global__ __launch_bounds__(64 * kJoinWaves) void k_join_parts(AttendArgs p)
 {
+    constexpr int GROUPS = 64 * kJoinWaves / LANES;
     const detfold_attend &a = p.a;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t b = p.row0 + blockIdx.x / a.q_heads;
-    const int head = blockIdx.x % a.q_heads, n = (int)p.parts.d;
-    const int64_t g = b * a.q_heads + head;
-    const float2 *ml = p.ml + g * n;
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 64)
-        m = fmaxf(m, ml[i].x);
-#pragma unroll
-    for (int i = 32; i > 0; i >>= 1)
-        m = fmaxf(m, __shfl_xor(m, i));
-    const float base = m == -INFINITY ? 0.0f : m;
+    const int head = blockIdx.x % a.q_heads, h = head / p.group, in = head - h * p.group;
+    const int64_t unit = h * (int64_t)p.tiles.d + in / 16, heads = min(16, p.group), units = (int64_t)p.units.d * p.beside;
+    int n = (int)p.parts.d;
+    int64_t first, next, step;  // slots
+    if (p.shares) {
+        const int2 cut = p.cut[b];
+        n = cut.y - cut.x + 1;
+        if (n == 1)
+            return;
+        step = 2 * units;
+        next = (cut.x * units + unit) * 2;
+        first = next + 1;
+    } else {
+        step = units;
+        first = next = b * n * step + unit;
+    }
+    auto slot = [&](int i) { return (i ? next + i * step : first) * heads + in % 16; };
     const int d0 = 4 * lane, d = min(d0, p.c.v_dim - 4);
-    const float *o = p.acc + g * n * p.c.v_dim + d;
     f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    float l = 0.0f;
-#pragma unroll 8
-    for (int i = wave; i < n; i += kBlock / 64) {
-        const float2 s = ml[i];
-        f4 x;
-        __builtin_memcpy(&x, o + (int64_t)i * p.c.v_dim, sizeof(x));
-        const float w = __builtin_amdgcn_exp2f(s.x - base);
-        l += s.y * w;
-        if (s.y == 0.0f)  // no token: its sums were not written
-            x = f4{0.0f, 0.0f, 0.0f, 0.0f};
-        acc += x * w;
-    }
-    __shared__ f4 accs[kBlock / 64][64];
-    __shared__ float ls[kBlock / 64];
-    accs[wave][lane] = acc;
-    if (lane == 0)
-        ls[wave] = l;
-    __syncthreads();
-    if (wave > 0)
-        return;
+    float m = -INFINITY, l = 0.0f;
+    for (int i0 = group; i0 < n; i0 += 8 * GROUPS) {  // eight parts' loads together
+        f4 x[8];
+        float2 s[8];
+        float top = m;
 #pragma unroll
-    for (int i = 1; i < kBlock / 64; ++i) {
-        acc += accs[i][lane];
-        l += ls[i];
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * GROUPS;
+            const int64_t at = slot(min(i, n - 1));
+            s[j] = p.ml[at];
+            __builtin_memcpy(&x[j], p.acc + at * p.c.v_dim + d, sizeof(f4));
+            if (i >= n)
+                s[j] = make_float2(-INFINITY, 0.0f), x[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            top = fmaxf(top, s[j].x);
+        const float base = top == -INFINITY ? 0.0f : top, turn = __builtin_amdgcn_exp2f(m - base);
+        l *= turn;
+        acc *= turn;
+        m = top;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w = __builtin_amdgcn_exp2f(s[j].x - base);
+            l += s[j].y * w;
+            acc += x[j] * w;
+        }
     }
-    const float vs = p.c.v_scale ? p.c.v_scale[head / p.group] : 1.0f;
-    const float out[4] = {attended(acc.x, vs, l), attended(acc.y, vs, l), attended(acc.z, vs, l), attended(acc.w, vs, l)};
+    __shared__ f4 accs[GROUPS][LANES];
+    __shared__ float2 mls[GROUPS];
+    accs[group][lane] = acc;
+    if (lane == 0)
+        mls[group] = make_float2(m, l);
+    __syncthreads();
+    if (group > 0)
+        return;
+    float top = -INFINITY;
+    for (int i = 0; i < GROUPS; ++i)
+        top = fmaxf(top, mls[i].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    acc = f4{0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
+    for (int i = 0; i < GROUPS; ++i) {
+        const float w = __builtin_amdgcn_exp2f(mls[i].x - base);
+        l += mls[i].y * w;
+        acc += accs[i][lane] * w;
+    }
+    const float by = out_scale(p.c.v_scale ? p.c.v_scale[h] : 1.0f, l), out[4] = {acc.x * by, acc.y * by, acc.z * by, acc.w * by};
     if (d0 < p.c.v_dim)
         put_out<4>(a, b * a.out_row + (int64_t)head * a.out_head + d, out);
     if (a.lse && lane == 0)
-        a.lse[g] = log_sum(m, l);
+        a.lse[b * a.q_heads + head] = log_sum(top, l);
 }
 
 }  // namespace
@@ -87,10 +114,16 @@ int launch_attend(const AttendArgs &a, void *stream)
         }
         return true;
     };
-    const int threads = 64 * a.waves, lds = k.q_bytes + a.waves / 2 * k.save_bytes;
-    if (!rows((int64_t)a.units.d * a.parts.d, k.f, threads, lds))
+    const int threads = 64 * a.waves, heads = a.group < 16 ? a.group : 16;
+    const int queries = a.beside * k.q_bytes, sums = a.waves * (128 + heads * k.head_bytes), lds = queries > sums ? queries : sums;
+    if (a.shares) {
+        if (hipLaunchKernel(k.f, dim3(a.shares * a.units.d), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) != hipSuccess)
+            return DETFOLD_ELAUNCH;
+    } else if (!rows((int64_t)a.units.d * a.parts.d, k.f, threads, lds)) {
         return DETFOLD_ELAUNCH;
-    if (a.parts.d > 1 && !rows(a.a.q_heads, (const void *)k_join_parts, kBlock, 0))
+    }
+    const void *join = a.c.v_dim <= 64 ? (const void *)k_join_parts<16> : a.c.v_dim <= 128 ? (const void *)k_join_parts<32> : (const void *)k_join_parts<64>;
+    if ((a.shares || a.parts.d > 1) && !rows(a.a.q_heads, join, 64 * kJoinWaves, 0))
         return DETFOLD_ELAUNCH;
     return DETFOLD_OK;
 }

@@ -15,8 +15,12 @@ namespace {
 constexpr int64_t kMaxCount = (int64_t)1 << 31;   // counts that the kernels hold in 32 bits
 constexpr int64_t kMaxElems = (int64_t)1 << 46;   // extent of one buffer, in elements
 constexpr int32_t kMaxHeads = 1 << 16;
-constexpr int64_t kGroupsPerCu = 4;               // workgroups of the attention per compute unit
-constexpr int64_t kMinPart = 256;                 // tokens that are worth a workgroup
+constexpr int64_t kGroupsPerCu = 1;               // workgroups of the attention per compute unit
+constexpr int64_t kShort = 256;                   // tokens that one workgroup takes by itself
+constexpr int64_t kStepBytes = 32768;              // of the cache that keep a wave's loads in flight
+constexpr int64_t kMaxEven = 4096;                // rows that every workgroup adds up the lengths of
+constexpr int64_t kLongPart = 8192;               // tokens of a part where there are more rows
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // workgroups of a launch, well below what a grid takes
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
@@ -154,40 +158,50 @@ int check_append(const detfold_paged_cache *c, const detfold_append *a)
 }
 
 int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
-                int64_t window, int32_t split, int32_t cu_count, detfold_attend_plan *p)
+                int64_t window, int32_t split, bool wide, int32_t cu_count, AttendPlan *p)
 {
     if (batch < 0 || batch >= kMaxCount || max_len < 0 || max_len >= kMaxCount || window < 0 || q_heads < 1 ||
         q_heads > kMaxHeads || q_heads % c.heads != 0 || split < 0 || split % DETFOLD_ATTEND_STEP != 0 || cu_count < 1)
         return DETFOLD_EINVAL;
-    const int64_t group = q_heads / c.heads, tiles = (group + 15) / 16;
-    p->units = batch * c.heads * tiles;
+    const int64_t group = q_heads / c.heads, tiles = (group + 15) / 16, units = c.heads * tiles;
     const int64_t seen = window > 0 && window < max_len ? window : max_len;
     const int64_t full = (int64_t)cu_count * kGroupsPerCu;  // workgroups that fill the device
-    int64_t part = split > 0 ? split : kMinPart;
-    if (split == 0 && p->units > 0) {
-        const int64_t parts = (full + p->units - 1) / p->units, even = (seen + parts - 1) / parts;
-        if (even > part)
-            part = (even + DETFOLD_ATTEND_STEP - 1) / DETFOLD_ATTEND_STEP * DETFOLD_ATTEND_STEP;
+    p->units = batch * units;
+    p->shares = 0;
+    p->waves = wide || 64 * (c.dim + c.v_dim) * elem_size(c.type) < kStepBytes ? 8 : 4;
+    p->beside = units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
+    const int64_t groups = units / p->beside;
+    int64_t part = split > 0 ? split : kLongPart;
+    if (split == 0) {
+        if (seen <= kShort) {
+            part = kShort;
+        } else if (batch > 0 && groups <= full / 2 && batch <= kMaxEven && batch * (seen / 32 + 2) < kMaxCount) {
+            p->shares = full / groups;
+            const int64_t even = (batch * seen + p->shares - 1) / p->shares, half = (seen + 1) / 2;
+            part = even < half ? even : half;
+        } else if (batch > 0 && seen > kMaxBlocks / p->units * part) {
+            part = (seen - 1) / (kMaxBlocks / p->units + 1) + 1;
+        }
+        part = (part + DETFOLD_ATTEND_STEP - 1) / DETFOLD_ATTEND_STEP * DETFOLD_ATTEND_STEP;
     }
     p->splits = seen > part ? (seen + part - 1) / part : 1;
     p->split = p->splits > 1 ? part : seen;
     // A part leaves v_dim sums, its maximum and its sum of weights per query
-    // head; the sums come first, 16-byte aligned.
-    const int64_t rows = batch * q_heads, each = ((int64_t)c.v_dim + 2) * 4;
-    p->workspace_bytes = p->splits > 1 ? rows * p->splits * each : 0;
-    // Smaller calls: units * splits < full + units where the plan chooses, and
-    // no part but a row's last is shorter than the least.
-    const int64_t least = split > 0 ? split : kMinPart, most = (max_len + least - 1) / least;
-    const int64_t upto = rows * most, fill = p->units > 0 ? rows / p->units * (full + p->units) : 0;
-    p->workspace_upto = most > 1 ? (split > 0 || upto < fill ? upto : fill) * each : 0;
+    // head.  Smaller calls take no more parts of their own, and the number of
+    // shares does not depend on them.
+    const int64_t each = (group < 16 ? group : 16) * ((int64_t)c.v_dim + 2) * 4;
+    const int64_t least = split > 0 ? split : kLongPart, most = (max_len + least - 1) / least;
+    const int64_t shared = split == 0 && groups <= full / 2 ? 2 * (full / groups) * units : 0;
+    if (p->units > kMaxElems / 16 || (split > 0 && p->units > 0 && most > kMaxElems / p->units))
+        return DETFOLD_EINVAL;
+    int64_t upto = most == 1 ? 0 : split > 0 || p->units < kMaxBlocks ? p->units * most : kMaxBlocks + 2 * p->units;
+    if (split == 0 && upto > kMaxBlocks + 2 * p->units)
+        upto = kMaxBlocks + 2 * p->units;
+    upto = upto > shared ? upto : shared;
+    p->slots = p->shares ? shared : p->splits > 1 ? p->units * p->splits : 0;
+    p->workspace_bytes = batch > 0 ? p->slots * each + (p->shares ? batch * 8 : 0) : 0;
+    p->workspace_upto = batch > 0 && max_len > (split > 0 ? split : kShort) ? upto * each + batch * 8 : 0;
     return DETFOLD_OK;
-}
-
-// Waves of a workgroup.  With a split of the caller's always the same, since
-// the waves' sums are joined too.
-int attend_waves(const detfold_attend_plan &p, int32_t split, int32_t cu_count)
-{
-    return 4;
 }
 
 // 16 tokens from a multiple of 16 on lie in one page, and within 2^31 bytes of it.
@@ -204,8 +218,8 @@ int check_attend(const detfold_paged_cache *c, const detfold_attend *a)
         return rc;
     if (!a || a->reserved != 0 || !types_pair(a->type, c->type) || (a->out_type != a->type && a->out_type != DETFOLD_F32))
         return DETFOLD_EINVAL;
-    detfold_attend_plan p;  // checks the counts; the device's own plan follows
-    if ((rc = plan_attend(*c, a->batch, a->q_heads, a->max_len, a->window, a->split, 1, &p)) != DETFOLD_OK)
+    AttendPlan p;  // checks the counts; the device's own plan follows
+    if ((rc = plan_attend(*c, a->batch, a->q_heads, a->max_len, a->window, a->split, false, 1, &p)) != DETFOLD_OK)
         return rc;
     if (!std::isfinite(a->scale) || a->table_width < 0 || a->table_row < 0 || a->workspace_bytes < 0)
         return DETFOLD_EINVAL;
@@ -281,8 +295,13 @@ int detfold_plan_attend(const detfold_paged_cache *cache, int64_t batch, int32_t
 {
     if (!plan)
         return DETFOLD_EINVAL;
-    const int rc = check_cache(cache);
-    return rc != DETFOLD_OK ? rc : plan_attend(*cache, batch, q_heads, max_len, window, split, cu_count, plan);
+    AttendPlan p;
+    int rc = check_cache(cache);
+    if (rc == DETFOLD_OK)
+        rc = plan_attend(*cache, batch, q_heads, max_len, window, split, false, cu_count, &p);
+    if (rc == DETFOLD_OK)
+        *plan = p;
+    return rc;
 }
 
 int detfold_attend_workspace(const detfold_paged_cache *cache, int64_t batch, int32_t q_heads, int64_t max_len,
@@ -310,9 +329,13 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
     int32_t cu = 0;
     if ((rc = current_cu_count(&cu)) != DETFOLD_OK)
         return rc;
-    detfold_attend_plan p;
-    if ((rc = plan_attend(*cache, args->batch, args->q_heads, args->max_len, args->window, args->split, cu, &p)) != DETFOLD_OK)
+    AttendPlan p;
+    if ((rc = plan_attend(*cache, args->batch, args->q_heads, args->max_len, args->window, args->split, args->out_type == DETFOLD_F32 && cache->type != DETFOLD_F32, cu,
+                          &p)) != DETFOLD_OK)
         return rc;
+    const int64_t groups = p.units / args->batch / p.beside;
+    if (groups * p.splits > kMaxBlocks)
+        return DETFOLD_EINVAL;
     if (p.workspace_bytes > 0 && (!args->workspace || args->workspace_bytes < p.workspace_bytes))
         return DETFOLD_ESIZE;
     AttendArgs k = {};
@@ -321,13 +344,17 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
     k.group = args->q_heads / cache->heads;
     k.page = divider((uint32_t)cache->page);
     k.tiles = divider((uint32_t)(k.group + 15) / 16);
-    k.units = divider((uint32_t)cache->heads * k.tiles.d);
-    k.parts = divider((uint32_t)p.splits);
+    k.beside = p.beside;
+    k.units = divider((uint32_t)cache->heads * k.tiles.d / p.beside);
+    k.parts = divider((uint32_t)(p.shares ? 1 : p.splits));
+    k.shares = (uint32_t)p.shares;
     k.split = p.split;
     k.tiled = attend_tiled(*cache);
-    k.waves = attend_waves(p, args->split, cu);
+    k.waves = p.waves;
+    const int64_t heads = p.slots * (k.group < 16 ? k.group : 16);
     k.acc = (float *)args->workspace;
-    k.ml = (float2 *)(k.acc + args->batch * args->q_heads * p.splits * cache->v_dim);
+    k.ml = (float2 *)(k.acc + heads * cache->v_dim);
+    k.cut = (int2 *)(k.ml + heads);
     return launch_attend(k, stream);
 }
 

@@ -48,23 +48,34 @@ struct AttendArgs {
     detfold_paged_cache c;
     detfold_attend a;
     Divider page;
-    Divider units;  // a row's workgroups per part: key-value heads times tiles of 16 query heads
-    Divider tiles;  // the latter
-    Divider parts;  // of a row's length
-    int64_t split;  // tokens of a part
-    int64_t row0;   // first row of the launch
+    Divider units;  // workgroups per row and part: the units (key-value heads times
+                    // tiles of 16 query heads) over those that lie beside each other in one
+    Divider tiles;  // of a key-value head's query heads
+    Divider parts;  // of every row's length, split tokens each, or
+    uint32_t shares;  // even shares of all rows' tokens (0: parts)
     int32_t group;  // query heads of a key-value head
+    int64_t split;
+    int64_t row0;   // first row of the launch
     int32_t tiled;  // 16 tokens from a multiple of 16 on lie in one page
     int32_t waves;  // of a workgroup
-    float *acc;     // the parts' sums [batch][q_heads][parts][v_dim], where there are several
-    float2 *ml;     // and their maxima and sums of weights [batch][q_heads][parts]
+    int32_t beside; // units of a workgroup, a power of two
+    // What the parts of a row leave, in slots of min(16, group) query heads:
+    // slot (row * parts + part) * units + unit, or slots (share * units + unit)
+    // * 2 + 0 and 1 for the row that a share begins within and the one that it
+    // ends within.
+    float *acc;     // sums [slot][head][v_dim]
+    float2 *ml;     // maxima and sums of weights [slot][head]
+    int2 *cut;      // first and last share of each row
 };
 
-// A kernel of the attention and the LDS it takes: for the queries, and for
-// each pair of waves.
+constexpr int kUnit = 64;     // tokens that shares are counted in
+constexpr int kMinShare = 1;  // of these, at least, in a share
+
+// A kernel of the attention and the LDS it takes: for the queries, and for the
+// sums of a wave's query head.
 struct AttendKernel {
     const void *f;
-    int q_bytes, save_bytes;
+    int q_bytes, head_bytes;
 };
 AttendKernel attend_bf16(int cache, bool wide, int dim, bool tiled);
 AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled);
@@ -85,9 +96,12 @@ int check_cache(const detfold_paged_cache *c);
 int check_append(const detfold_paged_cache *c, const detfold_append *a);
 int check_attend(const detfold_paged_cache *c, const detfold_attend *a);
 int check_softmax(const SoftmaxArgs &s);
+struct AttendPlan : detfold_attend_plan {
+    int64_t shares, slots;
+    int32_t waves, beside;
+};
 int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
-                int64_t window, int32_t split, int32_t cu_count, detfold_attend_plan *p);
-int attend_waves(const detfold_attend_plan &p, int32_t split, int32_t cu_count);
+                int64_t window, int32_t split, bool wide, int32_t cu_count, AttendPlan *p);
 bool attend_tiled(const detfold_paged_cache &c);
 
 // --- cache_kernels.hip, attend_kernels.hip: launches --------------------------

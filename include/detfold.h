@@ -458,11 +458,10 @@ int detfold_cache_append(const detfold_paged_cache *cache, const detfold_append 
  * past the row's last page are not read.
  *
  * Scores, the running maximum, the sum and the output are held in binary32.
- * Two calls with equal arguments give equal bits: the cache's length is split
- * over workgroups by a rule on the arguments and the device alone, and the
- * parts are joined in ascending order of their tokens.  With `split` set the
- * rule is the caller's, and a row's bits do not depend on the other rows, the
- * batch or max_len.
+ * Two calls with equal arguments and lengths give equal bits: the rows' tokens
+ * are split over workgroups by a rule on these and the device alone, and the
+ * parts are joined in a fixed order.  With `split` set a row's parts are its
+ * own, and its bits do not depend on the other rows, the batch or max_len.
  *   lens      device, int32.  A negative length counts as 0; a length beyond
  *             max_len or the table, or a page outside the cache, gives NaN in
  *             that row's out and lse (nothing outside the cache is read)
@@ -471,7 +470,7 @@ int detfold_cache_append(const detfold_paged_cache *cache, const detfold_append 
  *   q_heads   a multiple of the cache's heads
  *   out_type  the type of q, or F32
  *   split     tokens of one part: 0 = the plan's choice, else a multiple of
- *             DETFOLD_ATTEND_STEP
+ *             DETFOLD_ATTEND_STEP (a row's parts times heads at most 2^22)
  *   workspace device memory of at least the plan's bytes, 16-byte
  *             aligned, not shared by calls that overlap in time; its contents
  *             before and after a call mean nothing
@@ -499,8 +498,9 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
 /* How a call is split (host only; nothing is dereferenced). */
 typedef struct detfold_attend_plan {
     int64_t units;           /* rows times groups of query heads that share the cache reads */
-    int64_t splits;          /* parts of a row's length */
-    int64_t split;           /* tokens of a part */
+    int64_t splits;          /* parts of a row of max_len tokens */
+    int64_t split;           /* tokens of a part; with split = 0 rows may also share one, so that
+                                parts are even whatever the rows' lengths */
     int64_t workspace_bytes; /* what this call needs: 0 where every row is one part */
     int64_t workspace_upto;  /* what every call of this split needs whose batch and max_len are
                                 at most these, with any window */
