@@ -18,8 +18,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
 // N bytes of the cache, read once: at any alignment that a head's start may
 // have (one wide load all the same), and not kept in the caches.
 template <int N> struct Words {

@@ -253,7 +253,7 @@ int check_attend(const detfold_paged_cache *c, const detfold_attend *a)
 
 int check_softmax(const SoftmaxArgs &s)
 {
-    if (s.w < 1 || s.rows < 0 || s.dim < 1 || s.type < DETFOLD_F32 || s.type > DETFOLD_F16)
+    if (s.w < 1 || s.rows < 0 || s.dim < 1 || s.dim >= kMaxCount / 2 || s.type < DETFOLD_F32 || s.type > DETFOLD_F16)
         return DETFOLD_EINVAL;
     if (s.rows == 0)
         return DETFOLD_OK;
@@ -287,7 +287,11 @@ int detfold_cache_append(const detfold_paged_cache *cache, const detfold_append 
     int rc = check_append(cache, args);
     if (rc != DETFOLD_OK || args->tokens == 0)
         return rc;
-    return launch_append({*cache, *args, divider((uint32_t)cache->page)}, stream);
+    AppendArgs k = {};
+    k.c = *cache;
+    k.a = *args;
+    k.page = divider((uint32_t)cache->page);
+    return launch_append(k, stream);
 }
 
 int detfold_plan_attend(const detfold_paged_cache *cache, int64_t batch, int32_t q_heads, int64_t max_len,
@@ -361,7 +365,7 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
 int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *lse, int32_t type, int32_t W,
                          int64_t rows, int64_t dim, int64_t outs_pitch, int64_t lses_pitch, void *stream)
 {
-    const SoftmaxArgs s = {out, outs, lses, lse, rows, dim, outs_pitch, lses_pitch, type, W};
+    const SoftmaxArgs s = {out, outs, lses, lse, rows, dim, outs_pitch, lses_pitch, type, W, {}, 0, 0};
     const int rc = check_softmax(s);
     if (rc != DETFOLD_OK || rows == 0)
         return rc;

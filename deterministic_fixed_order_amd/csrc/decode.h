@@ -42,6 +42,13 @@ struct AppendArgs {
     detfold_paged_cache c;
     detfold_append a;
     Divider page;
+    // Of the launch: chunks of a key or query head and of a value head, groups
+    // of heads of a token (the queries' first) and of its values, the tokens,
+    // and the workgroups that turn (the others copy values).
+    Divider chunks, v_chunks, groups, v_groups;
+    int64_t token0;
+    uint32_t tokens, turn;
+    int32_t q_groups;
 };
 
 struct AttendArgs {
@@ -88,6 +95,9 @@ struct SoftmaxArgs {
     float *lse;
     int64_t rows, dim, outs_pitch, lses_pitch;
     int32_t type, w;
+    Divider chunks;  // of the launch: a row's, its first row and their count
+    int64_t row0;
+    uint32_t count;
 };
 
 // --- decode.cpp: host only, no device access ---------------------------------

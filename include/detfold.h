@@ -526,7 +526,7 @@ int detfold_attend_workspace(const detfold_paged_cache *cache, int64_t batch, in
  *   lses   device, partial w at lses + w * lses_pitch, [rows]
  *   out    device, [rows][dim], of the type of outs;  lse  device, [rows] or NULL
  *   type   DETFOLD_F32, _BF16 or _F16
- *   W >= 1; pitches in elements, at least rows * dim and rows
+ *   W >= 1, dim below 2^30; pitches in elements, at least rows * dim and rows
  * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP, DETFOLD_EDEVICE, DETFOLD_ELAUNCH.
  */
 int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *lse, int32_t type,
