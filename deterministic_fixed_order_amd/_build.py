@@ -4,7 +4,9 @@ Sources (``csrc/``): fold_kernels.hip (the fold's device code and launches),
 plan.cpp (host-only planning and argument checks), detfold.cpp (call sequences
 and the C ABI), internal.h (their shared declarations); of the decode-step
 operators cache_kernels.hip and attend_kernels.hip (device code and launches),
-decode.cpp (checks, planning and the C ABI), decode.h and decode_device.h.
+attend_f32.hip, attend_f16.hip and attend_bf16.hip (the instances of
+attend_kernel.h), decode.cpp (checks, planning and the C ABI), decode.h and
+decode_device.h; and bind.cpp, the C++ side of decode.py, a library of its own.
 exports.map limits the exported symbols to the C ABI of include/detfold.h.
 
 The .hip files are compiled in two passes, so that device-only flags reach
@@ -47,10 +49,13 @@ SOURCES = [KERNELS] + HOST_SOURCES
 INTERNAL_HEADER = os.path.join(CSRC, "internal.h")
 DECODE_KERNELS = [os.path.join(CSRC, f) for f in ("cache_kernels.hip", "attend_kernels.hip", "attend_f32.hip",
                                                      "attend_f16.hip", "attend_bf16.hip")]
-DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_device.h", "attend_kernel.h")]
+DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_device.h", "attend_kernel.h",
+                                                                 "bind.cpp")]
+BINDING = os.path.join(CSRC, "bind.cpp")
 EXPORTS_MAP = os.path.join(CSRC, "exports.map")
 HEADER = os.path.join(ROOT, "include", "detfold.h")
 LIB = os.path.join(PKG, "libdetfold.so")
+BINDING_LIB = os.path.join(PKG, "_bind.so")
 DIGEST = LIB + ".sha256"
 ARCH = "gfx950"
 
@@ -134,7 +139,7 @@ def _host_object(src: str, work: str, extra: list[str]) -> str:
 
 def _objects(work: str, extra: list[str]) -> list[str]:
     kernels = DECODE_KERNELS[::-1] + [KERNELS]
-    hosts = HOST_SOURCES + [s for s in DECODE_SOURCES if s.endswith(".cpp")]
+    hosts = HOST_SOURCES + [s for s in DECODE_SOURCES if s.endswith(".cpp") and s != BINDING]
     with ThreadPoolExecutor(max_workers=min(6, os.cpu_count() or 1)) as pool:
         jobs = [pool.submit(_kernel_object, s, work, extra) for s in kernels]
         jobs += [pool.submit(_host_object, s, work, extra) for s in hosts]
@@ -163,6 +168,27 @@ def build_library(out: str = LIB, extra: list[str] | None = None) -> str:
     return out
 
 
+def build_binding(out: str = BINDING_LIB) -> str:
+    """Compile bind.cpp, the C++ side of decode.py's calls (host code only),
+    against the installed torch.  It holds the digest of the sources, so that
+    it is never used beside a library of other ones."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = out + ".tmp%d" % os.getpid()
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+             '-DDETFOLD_BUILT_FROM="%s"' % source_digest(),
+             "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths():
+        flags += ["-isystem", path]
+    _run(["g++"] + flags + [BINDING, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+                            "-lc10", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, out)
+    return out
+
+
 def save_temps(outdir: str, src: str | None = None) -> None:
     """Keep the gfx950 assembly of a file's device pass (for reading our own
     ISA); the fold's unless another is named."""
@@ -172,3 +198,4 @@ def save_temps(outdir: str, src: str | None = None) -> None:
 
 if __name__ == "__main__":
     print(build_library())
+    print(build_binding())

@@ -1,0 +1,245 @@
+// bind.cpp -- the ordinary call of a decode-step operator from Python, without
+// the interpreter's share of it: reads the tensors, fills the public struct
+// and calls the library (a Python call costs 4 to 7 us of reading ten tensors'
+// types, shapes and strides, of which this needs less than 1).
+//
+// Only what it can take as it is: anything else (a wrong type, shape, device
+// or layout, a missing argument) returns -1, and decode.py, whose checks are
+// the same, says what is wrong.  The library's functions come as addresses, so
+// this links to neither the library nor HIP.
+
+#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "detfold.h"
+
+namespace {
+
+struct Arg {
+    const at::Tensor *t = nullptr;
+    bool none = false;
+    explicit Arg(PyObject *o)
+    {
+        none = o == Py_None;
+        if (!none && THPVariable_Check(o))
+            t = &THPVariable_Unpack(o);
+    }
+    // A tensor of this device, its last dimension contiguous.
+    bool on(int64_t dev) const
+    {
+        return t && t->layout() == c10::kStrided && t->get_device() == dev && t->dim() > 0 &&
+               (t->stride(-1) == 1 || t->size(-1) == 1);
+    }
+    // [n, heads, dim] (heads = 0: any)
+    bool heads(int64_t dev, c10::ScalarType type, int64_t n, int64_t heads, int64_t dim) const
+    {
+        return on(dev) && t->scalar_type() == type && t->dim() == 3 && t->size(0) == n && t->size(2) == dim &&
+               (heads == 0 || t->size(1) == heads);
+    }
+    // contiguous, of a shape
+    bool plain(int64_t dev, c10::ScalarType type, c10::IntArrayRef shape) const
+    {
+        return t && t->layout() == c10::kStrided && t->get_device() == dev && t->scalar_type() == type && t->sizes() == shape &&
+               t->is_contiguous();
+    }
+    template <typename T> T *at() const { return t ? static_cast<T *>(const_cast<void *>(t->const_data_ptr())) : nullptr; }
+    void *data() const { return t ? const_cast<void *>(t->const_data_ptr()) : nullptr; }
+};
+
+int type_of(c10::ScalarType t)
+{
+    return t == c10::kFloat ? DETFOLD_F32 : t == c10::kBFloat16 ? DETFOLD_BF16 : t == c10::kHalf ? DETFOLD_F16 : -1;
+}
+
+struct Numbers {
+    bool ok = true;
+    int64_t whole(PyObject *o)
+    {
+        const int64_t v = PyLong_Check(o) ? PyLong_AsLongLong(o) : (ok = false, 0);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            ok = false;
+        }
+        return v;
+    }
+    void *address(PyObject *o)
+    {
+        void *p = PyLong_Check(o) ? PyLong_AsVoidPtr(o) : (ok = false, nullptr);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            ok = false;
+        }
+        return p;
+    }
+};
+
+bool cache_of(PyObject *o, detfold_paged_cache *c)
+{
+    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof(*c))
+        return false;
+    std::memcpy(c, PyBytes_AS_STRING(o), sizeof(*c));
+    return true;
+}
+
+PyObject *not_taken() { return PyLong_FromLong(-1); }
+
+typedef int (*AppendFn)(const detfold_paged_cache *, const detfold_append *, void *);
+typedef int (*AttendFn)(const detfold_paged_cache *, const detfold_attend *, void *);
+typedef int (*FoldFn)(void *, const void *, const float *, float *, int32_t, int32_t, int64_t, int64_t, int64_t, int64_t, void *);
+
+// (function, cache, device, stream, k, v, slots, q, q_out, positions, cos, sin, pairs)
+PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    detfold_paged_cache c;
+    Numbers num;
+    if (n != 13 || !cache_of(args[1], &c))
+        return not_taken();
+    const AppendFn f = (AppendFn)num.address(args[0]);
+    const int64_t dev = num.whole(args[2]);
+    void *stream = num.address(args[3]);
+    const Arg k(args[4]), v(args[5]), slots(args[6]), q(args[7]), q_out(args[8]), positions(args[9]), cos(args[10]), sin(args[11]);
+    if (!num.ok || !k.t || k.t->dim() != 3)
+        return not_taken();
+    const c10::ScalarType type = k.t->scalar_type();
+    const int64_t tokens = k.t->size(0);
+    detfold_append a = {};
+    a.type = type_of(type);
+    if (a.type < 0 || !k.heads(dev, type, tokens, c.heads, c.dim) || !v.heads(dev, type, tokens, c.heads, c.v_dim) ||
+        !slots.plain(dev, c10::kLong, {tokens}))
+        return not_taken();
+    a.k = k.data(), a.k_token = k.t->stride(0), a.k_head = k.t->stride(1);
+    a.v = v.data(), a.v_token = v.t->stride(0), a.v_head = v.t->stride(1);
+    a.slots = slots.at<int64_t>();
+    a.tokens = tokens;
+    if (!q.none) {
+        if (!q.heads(dev, type, tokens, 0, c.dim) || q.t->size(1) > INT32_MAX || !q_out.heads(dev, type, tokens, q.t->size(1), c.dim))
+            return not_taken();
+        a.q = q.data(), a.q_token = q.t->stride(0), a.q_head = q.t->stride(1);
+        a.q_out = q_out.data(), a.out_token = q_out.t->stride(0), a.out_head = q_out.t->stride(1);
+        a.q_heads = (int32_t)q.t->size(1);
+    } else if (!q_out.none) {
+        return not_taken();
+    }
+    if (!cos.none) {
+        if (!cos.t || cos.t->dim() != 2 || cos.t->size(1) > INT32_MAX / 2 || !cos.plain(dev, c10::kFloat, cos.t->sizes()) ||
+            !sin.plain(dev, c10::kFloat, cos.t->sizes()) || !positions.plain(dev, c10::kLong, {tokens}))
+            return not_taken();
+        a.cos = cos.at<float>(), a.sin = sin.at<float>(), a.positions = positions.at<int64_t>();
+        a.angles = cos.t->size(0);
+        a.rot = (int32_t)(2 * cos.t->size(1));
+    } else if (!sin.none || !positions.none) {
+        return not_taken();
+    }
+    a.pairs = args[12] == Py_True ? 1 : 0;
+    if (args[12] != Py_True && args[12] != Py_False)
+        return not_taken();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = f(&c, &a, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+// (function, cache, device, stream, out, q, table, lens, scale, window, max_len, lse, workspace, split)
+PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    detfold_paged_cache c;
+    Numbers num;
+    if (n != 14 || !cache_of(args[1], &c))
+        return not_taken();
+    const AttendFn f = (AttendFn)num.address(args[0]);
+    const int64_t dev = num.whole(args[2]);
+    void *stream = num.address(args[3]);
+    const Arg out(args[4]), q(args[5]), table(args[6]), lens(args[7]), lse(args[11]), workspace(args[12]);
+    detfold_attend a = {};
+    a.window = num.whole(args[9]), a.max_len = num.whole(args[10]);
+    const int64_t split = num.whole(args[13]);
+    if (!num.ok || !PyFloat_Check(args[8]) || split < 0 || split > INT32_MAX || !q.t || q.t->dim() != 3 || !out.t)
+        return not_taken();
+    const double scale = PyFloat_AS_DOUBLE(args[8]);
+    a.scale = (float)scale;
+    if (std::isfinite(scale) != std::isfinite(a.scale))
+        return not_taken();
+    const int64_t batch = q.t->size(0), q_heads = q.t->size(1);
+    const c10::ScalarType type = q.t->scalar_type(), out_type = out.t->scalar_type();
+    a.type = type_of(type), a.out_type = type_of(out_type);
+    if (a.type < 0 || (out_type != type && out_type != c10::kFloat) || q_heads > INT32_MAX || !q.heads(dev, type, batch, 0, c.dim) ||
+        !out.heads(dev, out_type, batch, q_heads, c.v_dim) || !lens.plain(dev, c10::kInt, {batch}))
+        return not_taken();
+    if (!table.on(dev) || table.t->scalar_type() != c10::kInt || table.t->dim() != 2 || table.t->size(0) != batch)
+        return not_taken();
+    if (!lse.none && !lse.plain(dev, c10::kFloat, {batch, q_heads}))
+        return not_taken();
+    if (!workspace.t || workspace.t->get_device() != dev || !workspace.t->is_contiguous())
+        return not_taken();
+    a.out = out.data(), a.out_row = out.t->stride(0), a.out_head = out.t->stride(1);
+    a.q = q.data(), a.q_row = q.t->stride(0), a.q_head = q.t->stride(1);
+    a.lse = lse.at<float>();
+    a.table = table.at<int32_t>(), a.table_row = table.t->stride(0), a.table_width = table.t->size(1);
+    a.lens = lens.at<int32_t>();
+    a.workspace = workspace.data(), a.workspace_bytes = (int64_t)workspace.t->nbytes();
+    a.batch = batch, a.q_heads = (int32_t)q_heads, a.split = (int32_t)split;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = f(&c, &a, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+// (function, device, stream, out, outs, lses, lse)
+PyObject *fold(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    Numbers num;
+    if (n != 7)
+        return not_taken();
+    const FoldFn f = (FoldFn)num.address(args[0]);
+    const int64_t dev = num.whole(args[1]);
+    void *stream = num.address(args[2]);
+    const Arg out(args[3]), outs(args[4]), lses(args[5]), lse(args[6]);
+    if (!num.ok || dev < 0 || !outs.on(dev) || outs.t->dim() < 2 || outs.t->size(0) < 1 || outs.t->size(0) > INT32_MAX)
+        return not_taken();
+    const at::Tensor &o = *outs.t;
+    const c10::IntArrayRef shape = o.sizes(), one = shape.slice(1), rows_shape = one.slice(0, one.size() - 1);
+    const int type = type_of(o.scalar_type());
+    if (type < 0 || !out.plain(dev, o.scalar_type(), one) || !lses.t || lses.t->layout() != c10::kStrided || lses.t->get_device() != dev ||
+        lses.t->scalar_type() != c10::kFloat || lses.t->sizes() != shape.slice(0, shape.size() - 1))
+        return not_taken();
+    if (!lse.none && !lse.plain(dev, c10::kFloat, rows_shape))
+        return not_taken();
+    int64_t rows = 1;  // each partial contiguous
+    for (int64_t d = (int64_t)shape.size() - 2, step = shape.back(), lse_step = 1; d > 0; --d) {
+        if (shape[d] != 1 && (o.stride(d) != step || lses.t->stride(d) != lse_step))
+            return not_taken();
+        step *= shape[d], lse_step *= shape[d], rows *= shape[d];
+    }
+    const int64_t W = shape[0], dim = shape.back();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = f(out.data(), outs.data(), lses.at<float>(), lse.at<float>(), type, (int32_t)W, rows, dim, W > 1 ? o.stride(0) : rows * dim,
+           W > 1 ? lses.t->stride(0) : rows, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+PyMethodDef methods[] = {
+    {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
+    {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, nullptr},
+    {"fold", (PyCFunction)(void (*)(void))fold, METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__bind()
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_from", DETFOLD_BUILT_FROM) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -12,14 +12,20 @@ As in the rest of the package the functions only check and marshal: type,
 device, shape and strides here, sizes and overlaps in the library, before
 anything touches the device.  Work is enqueued on the caller's current stream
 (or ``stream``); nothing synchronizes, so a call may be captured into a graph.
+
+A call goes to ``_bind`` first, which reads the tensors in C++ and calls the
+library if all is as it should be (an append with its rotation: 9.9 us a call
+without it).  What it leaves comes back to the checks here, which say what is
+wrong, and make the call if nothing is.
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import os
 import struct
 
-from . import _check, _stream_handle as _stream, load as _load
+from . import LIB_PATH, _check, _stream_handle as _stream, load as _load
 
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 ATTEND_STEP = 32
@@ -77,6 +83,33 @@ def bind(lib) -> None:
     lib.detfold_plan_attend.argtypes = [ctypes.c_char_p, _q, _i, _q, _q, _i, _i, ctypes.POINTER(AttendPlan)]
     lib.detfold_attend_workspace.argtypes = [ctypes.c_char_p, _q, _i, _q, _i, i64p]
     lib.detfold_fold_softmax.argtypes = [_p, _p, _p, _p, _i, _i, _q, _q, _q, _q, _p]
+
+
+_native = None
+
+
+def _bound():
+    """``_bind``'s functions, each with the library's own, and torch's accessor
+    of the current stream; where there is none that was built with this
+    library, functions that take no call."""
+    global _native
+    lib = _load()
+    try:
+        import torch
+        from . import _bind
+        with open(LIB_PATH + ".sha256") as f:
+            ok = f.read().strip() == _bind.built_from
+        raw = torch._C._cuda_getCurrentRawStream
+    except (ImportError, OSError, AttributeError):
+        ok = False
+    if ok:
+        _native = raw, *(x for call, of in ((_bind.append, lib.detfold_cache_append),
+                                            (_bind.attend, lib.detfold_attend_paged),
+                                            (_bind.fold, lib.detfold_fold_softmax))
+                         for x in (call, ctypes.cast(of, _p).value))
+    else:
+        _native = (lambda device: 0, *(lambda *args: -1, 0) * 3)
+    return _native
 
 
 _types = None
@@ -182,6 +215,11 @@ def cache_append(cache: PagedCache, k, v, slots, *, q=None, q_out=None, position
     be ``q``.  The tensors may be strided views of one projection; tokens of
     one call must not share a slot."""
     dev = cache.device_index
+    current, call, of = (_native or _bound())[:3]
+    rc = call(of, cache._c, dev, current(dev) if stream is None else int(stream.cuda_stream), k, v, slots, q, q_out,
+              positions, cos, sin, pairs)
+    if rc >= 0:
+        return _check(rc, "cache_append") if rc else None
     type_ = _type(k, "k")
     _same(v, "v", type_, "k")
     ks, vs = _heads(k, "k", dev, cache.heads, cache.dim), _heads(v, "v", dev, cache.heads, cache.v_dim)
@@ -247,6 +285,11 @@ def attend_paged(out, q, cache: PagedCache, table, lens, *, scale=None, window: 
     of one part (a multiple of 32), so that a row's bits do not depend on the
     batch around it."""
     dev = cache.device_index
+    current, _, _, call, of = (_native or _bound())[:5]
+    rc = call(of, cache._c, dev, current(dev) if stream is None else int(stream.cuda_stream), out, q, table, lens,
+              1.0 / math.sqrt(cache.dim) if scale is None else scale, window, max_len, lse, workspace, split)
+    if rc >= 0:
+        return _check(rc, "attend_paged") if rc else None
     type_, out_type = _type(q, "q"), _type(out, "out")
     if out_type != type_ and out_type != F32:
         _refuse_type(out, "out", "of q's type or float32")
@@ -294,8 +337,13 @@ def fold_softmax(out, outs, lses, *, lse=None, stream=None) -> None:
     A partial with ``lses`` = -infinity had no token and adds nothing, whatever
     its ``outs`` hold.  The partials may be padded apart; each is contiguous."""
     type_ = _type(outs, "outs")
-    _same(out, "out", type_, "outs")
     dev = outs.get_device()
+    native = _native or _bound()
+    if dev >= 0:
+        rc = native[5](native[6], dev, native[0](dev) if stream is None else int(stream.cuda_stream), out, outs, lses, lse)
+        if rc >= 0:
+            return _check(rc, "fold_softmax") if rc else None
+    _same(out, "out", type_, "outs")
     if dev < 0:
         raise ValueError("outs must be a device tensor, got %s" % outs.device)
     if outs.dim() < 2 or outs.shape[0] < 1:
