@@ -9,9 +9,23 @@ namespace detfold_impl {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int64_t kOnceBytes = 8 << 20;          // of an output that is not kept in the caches
+constexpr int kHeads = 2;
+constexpr int64_t kFill = 1 << 18;               // threads that fill the device
 constexpr int64_t kMaxItems = (int64_t)1 << 30;  // threads of a launch: a grid holds at most 2^32
 
-// N values at any alignment that their type allows, as one wide load or store.
+// Workgroup b of n, of which each XCD takes runs of kRun neighbours (workgroups
+// go to the XCDs round-robin): an XCD's share of a stream is then contiguous.
+constexpr int kRun = 16;
+__device__ __forceinline__ uint32_t in_runs(uint32_t b, uint32_t n)
+{
+    constexpr uint32_t span = 8 * kRun;
+    const uint32_t r = b % span;
+    return b - r + span <= n ? b - r + r % 8 * kRun + r / 8 : b;
+}
+
+// N values at any alignment that their type allows, as one wide load or store;
+// once: not kept in the caches.
 template <typename T, int N> struct Vec {
     T x[N];
 };
@@ -28,7 +42,18 @@ template <typename T, int N, bool ONCE = false> __device__ __forceinline__ Vec<T
     }
     return v;
 }
-template <typename T, int N> __device__ __forceinline__ void store_vec(T *p, const Vec<T, N> &v) { __builtin_memcpy(p, &v, sizeof(v)); }
+template <typename T, int N, bool ONCE = false> __device__ __forceinline__ void store_vec(T *p, const Vec<T, N> &v)
+{
+    constexpr int B = N * sizeof(T);
+    if constexpr (ONCE && B % 4 == 0) {
+        typedef uint32_t w __attribute__((ext_vector_type(B / 4), aligned(1)));
+        w y;
+        __builtin_memcpy(&y, &v, B);
+        __builtin_nontemporal_store(y, (w *)p);
+    } else {
+        __builtin_memcpy(p, &v, B);
+    }
+}
 
 __device__ __forceinline__ void turn(float &x, float &y, float c, float s)
 {
@@ -37,15 +62,13 @@ __device__ __forceinline__ void turn(float &x, float &y, float c, float s)
     x = z;
 }
 
-// Heads that a thread turns by the same angles, and whose loads it issues
-// together.
-constexpr int kHeads = 4;
-
 // The append.  A thread takes V pairs that turn together (or V values that do
-// not turn) of kHeads heads of one token, so that the angles are read once for
-// these; the values' heads are copied by the workgroups after the first `turn`.
-template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) void k_append(AppendArgs p)
+// not turn) of HEADS heads of one token, so that the angles are read once for
+// these and their loads are in flight together; the values' heads are copied by
+// the workgroups after the first `turn`.
+template <typename T, typename C, int V, int HEADS> __global__ __launch_bounds__(kBlock) void k_append(AppendArgs p)
 {
+    constexpr bool ONCE = HEADS > 1;
     const detfold_append &a = p.a;
     const detfold_paged_cache &c = p.c;
     const bool values = blockIdx.x >= p.turn;
@@ -57,7 +80,7 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
         return;
     const int64_t t = p.token0 + in;
     const bool query = !values && g < (uint32_t)p.q_groups;
-    const int head0 = (int)(g - (query || values ? 0 : p.q_groups)) * kHeads, heads = query ? a.q_heads : c.heads;
+    const int head0 = (int)(g - (query || values ? 0 : p.q_groups)) * HEADS, heads = query ? a.q_heads : c.heads;
     const int64_t slot = a.slots[t];
     const bool stored = slot >= 0 && slot < c.pages * c.page;
     if (!query && !stored)
@@ -65,14 +88,15 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
     const uint32_t pg = stored ? divide((uint32_t)slot, p.page) : 0;
     const int64_t off = stored ? slot - (int64_t)pg * c.page : 0;
     if (values) {
-        const T *x = (const T *)a.v + t * a.v_token + u * V;
-        C *y = (C *)c.v + pg * c.v_page + off * c.v_token + u * V;
-        Vec<T, V> v[kHeads];
+        const int i0 = min((int)u * V, c.v_dim - V);
+        const T *x = (const T *)a.v + t * a.v_token + i0;
+        C *y = (C *)c.v + pg * c.v_page + off * c.v_token + i0;
+        Vec<T, V> v[HEADS];
 #pragma unroll
-        for (int j = 0; j < kHeads; ++j)
+        for (int j = 0; j < HEADS; ++j)
             v[j] = load_vec<T, V>(x + min(head0 + j, heads - 1) * a.v_head);
 #pragma unroll
-        for (int j = 0; j < kHeads; ++j) {
+        for (int j = 0; j < HEADS; ++j) {
             const int h = head0 + j;
             if (h >= heads)
                 break;
@@ -81,19 +105,21 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
 #pragma unroll
             for (int n = 0; n < V; ++n)
                 o.x[n] = from_f32<C>(c.v_scale ? to_f32(v[j].x[n]) / by : to_f32(v[j].x[n]));
-            store_vec(y + h * c.v_head, o);
+            store_vec<C, V, ONCE>(y + h * c.v_head, o);
         }
         return;
     }
-    const int half = a.rot / 2, turned = half / V;  // the chunks of a head that turn come first
+    // The chunks of a head that turn come first.  The last one of a run starts
+    // early enough to end with it.
+    const int half = a.rot / 2, turned = (half + V - 1) / V;
     const bool turns = u < (uint32_t)turned;
-    const int i0 = turns ? (int)u * (a.pairs ? 2 * V : V) : a.rot + ((int)u - turned) * V;
-    const int i1 = turns ? i0 + (a.pairs ? V : half) : i0;
+    const int at = turns ? min((int)u * V, half - V) : a.rot + min(((int)u - turned) * V, c.dim - a.rot - V);
+    const int i0 = turns && a.pairs ? 2 * at : at, i1 = !turns ? at : a.pairs ? 2 * at + V : half + at;
     const T *x = query ? (const T *)a.q + t * a.q_token : (const T *)a.k + t * a.k_token;
     const int64_t x_head = query ? a.q_head : a.k_head;
-    Vec<T, V> v0[kHeads], v1[kHeads];
+    Vec<T, V> v0[HEADS], v1[HEADS];
 #pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
+    for (int j = 0; j < HEADS; ++j) {
         const T *from = x + min(head0 + j, heads - 1) * x_head;
         v0[j] = load_vec<T, V>(from + i0);
         v1[j] = load_vec<T, V>(from + i1);
@@ -102,8 +128,8 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
     if (turns) {
         const int64_t pos = a.positions[t];
         if (pos >= 0 && pos < a.angles) {
-            cs = load_vec<float, V>(a.cos + pos * half + u * V);
-            sn = load_vec<float, V>(a.sin + pos * half + u * V);
+            cs = load_vec<float, V>(a.cos + pos * half + at);
+            sn = load_vec<float, V>(a.sin + pos * half + at);
         } else {
 #pragma unroll
             for (int n = 0; n < V; ++n)
@@ -111,7 +137,7 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
         }
     }
 #pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
+    for (int j = 0; j < HEADS; ++j) {
         const int h = head0 + j;
         if (h >= heads)
             break;
@@ -134,12 +160,12 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
 #pragma unroll
             for (int n = 0; n < V; ++n)
                 o.x[n] = from_f32<T>(x01[n]);
-            store_vec(to + i0, o);
+            store_vec<T, V, ONCE>(to + i0, o);
             if (turns) {
 #pragma unroll
                 for (int n = 0; n < V; ++n)
                     o.x[n] = from_f32<T>(x01[V + n]);
-                store_vec(to + i1, o);
+                store_vec<T, V, ONCE>(to + i1, o);
             }
         } else {
             C *to = (C *)c.k + pg * c.k_page + off * c.k_token + h * c.k_head;
@@ -148,12 +174,12 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
 #pragma unroll
             for (int n = 0; n < V; ++n)
                 o.x[n] = from_f32<C>(c.k_scale ? x01[n] / by : x01[n]);
-            store_vec(to + i0, o);
+            store_vec<C, V, ONCE>(to + i0, o);
             if (turns) {
 #pragma unroll
                 for (int n = 0; n < V; ++n)
                     o.x[n] = from_f32<C>(c.k_scale ? x01[V + n] / by : x01[V + n]);
-                store_vec(to + i1, o);
+                store_vec<C, V, ONCE>(to + i1, o);
             }
         }
     }
@@ -162,13 +188,13 @@ template <typename T, typename C, int V> __global__ __launch_bounds__(kBlock) vo
 // The softmax fold.  A thread takes V neighbouring values of a row, eight
 // partials' loads at a time, and forms the row's weights itself: eight
 // exponentials cost less than handing them round.
-template <typename T, int V> __global__ __launch_bounds__(kBlock) void k_fold_softmax(SoftmaxArgs s)
+template <typename T, int V, bool ONCE> __global__ __launch_bounds__(kBlock) void k_fold_softmax(SoftmaxArgs s)
 {
     constexpr int N = 8;
-    const uint32_t i = blockIdx.x * kBlock + threadIdx.x, in = divide(i, s.chunks), u = i - in * s.chunks.d;
+    const uint32_t i = in_runs(blockIdx.x, gridDim.x) * kBlock + threadIdx.x, in = divide(i, s.chunks), u = i - in * s.chunks.d;
     if (in >= s.count)
         return;
-    const int64_t row = s.row0 + in, at = row * s.dim + u * V;
+    const int64_t row = s.row0 + in, at = row * s.dim + min((int64_t)u * V, s.dim - V);
     const T *outs = (const T *)s.outs + at;
     const float *lses = s.lses + row;
     float top = -INFINITY, total = 0.0f, acc[V] = {};
@@ -205,43 +231,55 @@ template <typename T, int V> __global__ __launch_bounds__(kBlock) void k_fold_so
 #pragma unroll
     for (int n = 0; n < V; ++n)
         o.x[n] = from_f32<T>(acc[n] * by);
-    store_vec((T *)s.out + at, o);
+    store_vec<T, V, ONCE>((T *)s.out + at, o);
     if (s.lse && u == 0)
         s.lse[row] = (top == -INFINITY ? 0.0f : top) + logf(total);
 }
 
-template <typename T, typename C> const void *append_width(int v)
+template <typename T, typename C, int V> const void *append_heads(int heads)
+{
+    return heads == 1 ? (const void *)k_append<T, C, V, 1> : (const void *)k_append<T, C, V, kHeads>;
+}
+template <typename T, typename C> const void *append_width(int v, int heads)
 {
     if constexpr (sizeof(T) == 2)
         if (v == 8)
-            return (const void *)k_append<T, C, 8>;
-    return v == 4 ? (const void *)k_append<T, C, 4> : v == 2 ? (const void *)k_append<T, C, 2> : (const void *)k_append<T, C, 1>;
+            return append_heads<T, C, 8>(heads);
+    return v == 4 ? append_heads<T, C, 4>(heads) : v == 2 ? append_heads<T, C, 2>(heads) : append_heads<T, C, 1>(heads);
 }
-template <typename T> const void *pick_append(int cache, int v)
+template <typename T> const void *pick_append(int cache, int v, int heads)
 {
     if (cache == DETFOLD_E4M3)
-        return append_width<T, e4m3>(v);
+        return append_width<T, e4m3>(v, heads);
     if constexpr (sizeof(T) == 4)
         if (cache == DETFOLD_BF16)
-            return append_width<T, bf16>(v);
-    return append_width<T, T>(v);
+            return append_width<T, bf16>(v, heads);
+    return append_width<T, T>(v, heads);
 }
-template <typename T> const void *pick_softmax(int v)
+template <typename T, int V> const void *softmax_once(bool once)
+{
+    return once ? (const void *)k_fold_softmax<T, V, true> : (const void *)k_fold_softmax<T, V, false>;
+}
+template <typename T> const void *pick_softmax(int v, bool once)
 {
     if constexpr (sizeof(T) == 2)
         if (v == 8)
-            return (const void *)k_fold_softmax<T, 8>;
-    return v == 4 ? (const void *)k_fold_softmax<T, 4> : v == 2 ? (const void *)k_fold_softmax<T, 2> : (const void *)k_fold_softmax<T, 1>;
+            return softmax_once<T, 8>(once);
+    return v == 4 ? softmax_once<T, 4>(once) : v == 2 ? softmax_once<T, 2>(once) : softmax_once<T, 1>(once);
 }
 
-// The widest access of at most 16 bytes that divides every run of values.
-int width(int type, int64_t a, int64_t b, int64_t c)
+// The widest access of at most 16 bytes that each of these runs of values holds
+// at least once (the last one of a run may then overlap another, which writes
+// the same), or, where a write must not come before another's read, divides.
+int width(int type, bool overlap, int64_t a, int64_t b, int64_t c)
 {
     int v = 16 / elem_size(type);
-    while (a % v || b % v || c % v)
-        v /= 2;
+    for (int64_t n : {a, b, c})
+        while (overlap ? n > 0 && n < v : n % v != 0)
+            v /= 2;
     return v;
 }
+int chunks(int64_t n, int v) { return (int)((n + v - 1) / v); }
 
 bool launch(const void *k, int64_t blocks, void *args, void *stream)
 {
@@ -254,15 +292,18 @@ bool launch(const void *k, int64_t blocks, void *args, void *stream)
 int launch_append(const AppendArgs &a, void *stream)
 {
     AppendArgs p = a;
-    const int v = width(a.a.type, a.a.rot / 2, a.c.dim - a.a.rot, a.c.v_dim);
-    const void *k = a.a.type == DETFOLD_F32    ? pick_append<float>(a.c.type, v)
-                    : a.a.type == DETFOLD_BF16 ? pick_append<bf16>(a.c.type, v)
-                                               : pick_append<f16>(a.c.type, v);
-    p.q_groups = (a.a.q_heads + kHeads - 1) / kHeads;
-    p.groups = divider(p.q_groups + (a.c.heads + kHeads - 1) / kHeads);
-    p.v_groups = divider((a.c.heads + kHeads - 1) / kHeads);
-    p.chunks = divider((a.a.rot / 2 + a.c.dim - a.a.rot) / v);
-    p.v_chunks = divider(a.c.v_dim / v);
+    const int v = width(a.a.type, a.a.q != a.a.q_out, a.a.rot / 2, a.c.dim - a.a.rot, a.c.v_dim);
+    p.chunks = divider(chunks(a.a.rot / 2, v) + chunks(a.c.dim - a.a.rot, v));
+    p.v_chunks = divider(chunks(a.c.v_dim, v));
+    // One head a thread where there are not enough tokens to fill the device
+    // otherwise: the time is then one thread's.
+    const int heads = a.a.tokens * (a.a.q_heads + a.c.heads) * p.chunks.d / kHeads < kFill ? 1 : kHeads;
+    const void *k = a.a.type == DETFOLD_F32    ? pick_append<float>(a.c.type, v, heads)
+                    : a.a.type == DETFOLD_BF16 ? pick_append<bf16>(a.c.type, v, heads)
+                                               : pick_append<f16>(a.c.type, v, heads);
+    p.q_groups = (a.a.q_heads + heads - 1) / heads;
+    p.groups = divider(p.q_groups + (a.c.heads + heads - 1) / heads);
+    p.v_groups = divider((a.c.heads + heads - 1) / heads);
     const int64_t each = (int64_t)p.groups.d * p.chunks.d, v_each = (int64_t)p.v_groups.d * p.v_chunks.d;
     const int64_t some = kMaxItems / (each + v_each);
     for (p.token0 = 0; p.token0 < a.a.tokens; p.token0 += some) {
@@ -277,9 +318,10 @@ int launch_append(const AppendArgs &a, void *stream)
 int launch_softmax(const SoftmaxArgs &a, void *stream)
 {
     SoftmaxArgs p = a;
-    const int v = width(a.type, a.dim, 0, 0);
-    const void *k = a.type == DETFOLD_F32 ? pick_softmax<float>(v) : a.type == DETFOLD_BF16 ? pick_softmax<bf16>(v) : pick_softmax<f16>(v);
-    p.chunks = divider((uint32_t)(a.dim / v));
+    const int v = width(a.type, true, a.dim, 0, 0);
+    const bool once = a.rows * a.dim * elem_size(a.type) >= kOnceBytes;
+    const void *k = a.type == DETFOLD_F32 ? pick_softmax<float>(v, once) : a.type == DETFOLD_BF16 ? pick_softmax<bf16>(v, once) : pick_softmax<f16>(v, once);
+    p.chunks = divider((uint32_t)chunks(a.dim, v));
     const int64_t some = kMaxItems / p.chunks.d;
     for (p.row0 = 0; p.row0 < a.rows; p.row0 += some) {
         p.count = (uint32_t)(a.rows - p.row0 < some ? a.rows - p.row0 : some);
