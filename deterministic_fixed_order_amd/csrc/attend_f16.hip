@@ -6,11 +6,11 @@
 
 namespace detfold_impl {
 
-AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled)
+AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled, bool brief)
 {
     if (cache == DETFOLD_E4M3)
-        return wide ? pick_attend<e4m3, kF16, kF32>(dim, tiled) : pick_attend<e4m3, kF16, kF16>(dim, tiled);
-    return wide ? pick_attend<f16, kF16, kF32>(dim, tiled) : pick_attend<f16, kF16, kF16>(dim, tiled);
+        return wide ? pick_attend<e4m3, kF16, kF32>(dim, tiled, brief) : pick_attend<e4m3, kF16, kF16>(dim, tiled, brief);
+    return wide ? pick_attend<f16, kF16, kF32>(dim, tiled, brief) : pick_attend<f16, kF16, kF16>(dim, tiled, brief);
 }
 
 }  // namespace detfold_impl

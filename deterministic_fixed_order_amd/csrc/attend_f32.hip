@@ -6,11 +6,11 @@
 
 namespace detfold_impl {
 
-AttendKernel attend_f32(int cache, int dim, bool tiled)
+AttendKernel attend_f32(int cache, int dim, bool tiled, bool brief)
 {
     if (cache == DETFOLD_E4M3)
-        return pick_attend<e4m3, kF32, kF32>(dim, tiled);
-    return cache == DETFOLD_BF16 ? pick_attend<bf16, kF32, kF32>(dim, tiled) : pick_attend<float, kF32, kF32>(dim, tiled);
+        return pick_attend<e4m3, kF32, kF32>(dim, tiled, brief);
+    return cache == DETFOLD_BF16 ? pick_attend<bf16, kF32, kF32>(dim, tiled, brief) : pick_attend<float, kF32, kF32>(dim, tiled, brief);
 }
 
 }  // namespace detfold_impl

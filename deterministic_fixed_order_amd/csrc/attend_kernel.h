@@ -150,75 +150,83 @@ template <int N> __device__ __forceinline__ void put_out(const detfold_attend &a
     }
 }
 
-// The tokens of a row that are seen, in units of kUnit from a0 on (a row without
-// any counts as one, so that someone writes its output).
+// The tokens of a row that are seen, in units from a0 on (a row without any
+// counts as one, so that someone writes its output).
 struct RowTokens {
-    uint32_t begin, end, a0, steps;
+    uint32_t begin, end, a0, units;
     bool bad;  // longer than the call or the table allows
 };
-__device__ __forceinline__ RowTokens row_tokens(const detfold_attend &a, const detfold_paged_cache &c, int32_t len, bool tiled)
+__device__ __forceinline__ RowTokens row_tokens(const AttendArgs &p, int32_t len, bool tiled)
 {
     const int64_t n = len > 0 ? len : 0;
     RowTokens r;
-    r.bad = n > a.max_len || n > a.table_width * c.page;
+    r.bad = n > p.a.max_len || n > p.a.table_width * p.c.page;
     r.end = r.bad ? 0 : (uint32_t)n;
-    r.begin = a.window > 0 && r.end > a.window ? (uint32_t)(r.end - a.window) : 0;
+    r.begin = p.a.window > 0 && r.end > p.a.window ? (uint32_t)(r.end - p.a.window) : 0;
     r.a0 = tiled ? r.begin & ~15u : r.begin;
-    r.steps = r.end > r.begin ? (r.end - r.a0 + kUnit - 1) / kUnit : 1;
+    r.units = r.end > r.begin ? (r.end - r.a0 + (1u << p.unit) - 1) >> p.unit : 1;
     return r;
 }
 
 // An even share of all rows' units, found by every wave from the lengths:
-// share y of p.shares has the units [y * each, (y + 1) * each) of the rows laid
-// end to end.
+// share y has the units [y * each, (y + 1) * each) of the rows laid end to end.
 struct Share {
     uint32_t left, at, row_at, each;  // units left, the next one, its row's first one, those of a share
-    int64_t row;
+    int32_t row, len;                 // that row and its length
 };
 __device__ __forceinline__ Share find_share(const AttendArgs &p, uint32_t y, bool tiled)
 {
     const int lane = threadIdx.x & 63, batch = (int)p.a.batch;
-    auto units = [&](int i) { return i < batch ? row_tokens(p.a, p.c, p.a.lens[i], tiled).steps : 0u; };
-    uint32_t own = units(lane), total = own;
+    auto length = [&](int i) { return i < batch ? p.a.lens[i] : 0; };
+    auto units = [&](int i, int32_t len) { return i < batch ? row_tokens(p, len, tiled).units : 0u; };
+    int32_t len = length(lane);
+    uint32_t total = 0;
     for (int i = lane + 64; i < batch; i += 64)
-        total += units(i);
-#pragma unroll
-    for (int i = 32; i > 0; i >>= 1)
-        total += __shfl_xor(total, i);
-    total = __builtin_amdgcn_readfirstlane(total);
+        total += units(i, length(i));
     Share w = {};
-    w.each = max((uint32_t)kMinShare, (total + p.shares - 1) / p.shares);
-    w.at = y * w.each;
-    if (w.at >= total)
-        return w;
-    w.left = min(w.each, total - w.at);
     uint32_t before = 0;
     for (int i = 0; i < batch; i += 64) {
+        const uint32_t own = units(i + lane, len);
         uint32_t upto = own;
 #pragma unroll
         for (int n = 1; n < 64; n <<= 1) {
             const uint32_t other = __shfl_up(upto, n);
             upto += lane >= n ? other : 0;
         }
+        const uint32_t here = __builtin_amdgcn_readlane(upto, 63);
+        if (i == 0) {
+            if (batch > 64)
+#pragma unroll
+                for (int n = 32; n > 0; n >>= 1)
+                    total += __shfl_xor(total, n);
+            total = __builtin_amdgcn_readfirstlane(total) + here;
+            w.each = divide(total + p.shares.d - 1, p.shares);
+            w.at = y * w.each;
+            if (w.at >= total)
+                return w;
+            w.left = min(w.each, total - w.at);
+        }
         const uint64_t past = __ballot(before + upto > w.at);
         if (past) {
             const int at = __builtin_ctzll(past);
             w.row = i + at;
             w.row_at = before + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(own, at);
+            w.len = __builtin_amdgcn_readlane(len, at);
             break;
         }
-        before += __builtin_amdgcn_readlane(upto, 63);
-        own = units(i + 64 + lane);
+        before += here;
+        len = length(i + 64 + lane);
     }
     return w;
 }
 
-template <typename C, int QK, int PV, int D, bool TILED> struct Attend {
+// MOST: tiles of 16 tokens in a step, at most.
+template <typename C, int QK, int PV, int D, bool TILED, int MOST> struct Attend {
     static constexpr int kSize = sizeof(C);
     static constexpr int kChunk = 16 / kSize;         // dims of one 16-byte load of a key
     static constexpr int kChunks = D / (4 * kChunk);  // of these per lane and key
     static constexpr int kFit = 1024 / (D * kSize);   // tiles of 16 tokens whose keys take 64 registers
-    static constexpr int kMost = D < 256 ? 4 : QK == kF32 ? 1 : 2;
+    static constexpr int kMost = D < 256 ? MOST : QK == kF32 ? 1 : 2;
     static constexpr int kTiles = kFit < kMost ? kFit : kMost;  // of a step
     static constexpr int kStep = 16 * kTiles;
     static constexpr int kWide = D >= 128 ? 8 : 4;    // dims of a value that a lane holds together
@@ -230,10 +238,10 @@ template <typename C, int QK, int PV, int D, bool TILED> struct Attend {
     static_assert(kTiles % 2 == 0 || PV == kF32, "the 16-bit products take 32 tokens");
 };
 
-template <typename C, int QK, int PV, int D, bool TILED>
+template <typename C, int QK, int PV, int D, bool TILED, int MOST>
 __global__ __launch_bounds__(512) void k_attend(AttendArgs)
 {
-    typedef Attend<C, QK, PV, D, TILED> S;
+    typedef Attend<C, QK, PV, D, TILED, MOST> S;
     constexpr int CS = S::kSize, E = S::kChunk, NC = S::kChunks, UT = S::kTiles, VW = S::kWide, NP = S::kParts, NT = S::kTokens;
     extern __shared__ __align__(16) char lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -248,7 +256,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     int64_t b;
     uint32_t part = 0;
     Share mine = {};
-    if (p0.shares) {
+    if (p0.shares.d) {
         mine = find_share(p0, y, TILED);
         if (mine.left == 0)
             return;
@@ -257,6 +265,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         const uint32_t row = divide(y, p0.parts);
         part = y - row * p0.parts.d;
         b = p0.row0 + row;
+        mine.len = scalar_load(p0.a.lens + b);
     }
 
     for (;;) {
@@ -271,6 +280,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
     const uint32_t pages = (uint32_t)c.pages;
     const float by = a.scale * (c.k_scale ? c.k_scale[h] : 1.0f) * kLog2e;
+    const float v_scale = c.v_scale ? c.v_scale[h] : 1.0f;
     const bool ragged = c.dim % (4 * E) != 0;
 
     // Where a lane's loads lie within a key and a value.
@@ -282,19 +292,19 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     for (int i = 0; i < NP; ++i)
         v_at[i] = (uint32_t)min(VW * (16 * i + col), c.v_dim - VW) * CS + (TILED ? 4 * grp * (uint32_t)v_token : 0);
 
-    const RowTokens row = row_tokens(a, c, scalar_load(a.lens + b), TILED);
+    const RowTokens row = row_tokens(p, mine.len, TILED);
     bool bad = row.bad;
     uint32_t begin = row.begin, end = row.end, done = 0;
     int64_t slot = -1;  // where the sums of this part go if the row has others
-    if (p.shares) {
+    if (p.shares.d) {
         const uint32_t x = mine.at - mine.row_at;
-        done = min(row.steps - x, mine.left);
-        if (done < row.steps)
+        done = min(row.units - x, mine.left);
+        if (done < row.units)
             slot = ((int64_t)y * (p.units.d * beside) + unit) * 2 + (x == 0);
         if (x == 0 && unit == 0 && lane == 0 && turn == 0)
-            p.cut[b] = make_int2((int)y, (int)((mine.at + row.steps - 1) / mine.each));
-        end = x + done < row.steps ? row.a0 + kUnit * (x + done) : end;
-        begin = x ? row.a0 + kUnit * x : begin;
+            p.cut[b] = make_int2((int)y, (int)(done < row.units ? (mine.at + row.units - 1) / mine.each : y));
+        end = x + done < row.units ? row.a0 + ((x + done) << p.unit) : end;
+        begin = x ? row.a0 + (x << p.unit) : begin;
     } else if (p.parts.d > 1) {
         slot = (b * p.parts.d + part) * (p.units.d * beside) + unit;
         const int64_t x = begin + part * p.split;
@@ -397,7 +407,8 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
                 w[j] = col < live ? qw[i].w[j] & keep_from(drop * QS, j) : 0u;
             *(u4 *)(queries + i * 1024 + lane * 16) = w;
         }
-    __builtin_amdgcn_sched_barrier(0);  // else the queries' registers add to those of the loads below
+    if (D == 256)  // else the queries' registers add to those of the loads below
+        __builtin_amdgcn_sched_barrier(0);
     if (s < steps) {
         load_keys(now);
         load_values(now);
@@ -568,7 +579,6 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     }
     __syncthreads();
     const AttendArgs &pe = arguments();
-    const float v_scale = pe.c.v_scale ? pe.c.v_scale[h] : 1.0f;
     for (int i = 64 * turn + lane; i < live * (D / 4); i += 64 * turns) {
         const AttendArgs &p = pe;
         const detfold_attend &a = p.a;
@@ -606,19 +616,30 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         return;
     mine.at = mine.row_at = mine.at + done;
     ++b;
+    mine.len = scalar_load(arguments().a.lens + b);
     __syncthreads();
     }
 }
 
-// The kernel for a head size of at most D, if p says tiles lie within a page.
-template <typename C, int QK, int PV, int D> AttendKernel pick_tiled(bool tiled)
+// The kernel for a head size, for tiles within a page or anywhere, and for long
+// steps or short ones.
+template <typename C, int QK, int PV, int D, int MOST> AttendKernel pick_tiled(bool tiled)
 {
-    typedef Attend<C, QK, PV, D, true> S;
-    return {tiled ? (const void *)k_attend<C, QK, PV, D, true> : (const void *)k_attend<C, QK, PV, D, false>, S::kQ, S::kRow * 4};
+    typedef Attend<C, QK, PV, D, true, MOST> S;
+    return {tiled ? (const void *)k_attend<C, QK, PV, D, true, MOST> : (const void *)k_attend<C, QK, PV, D, false, MOST>, S::kQ, S::kRow * 4};
 }
-template <typename C, int QK, int PV> AttendKernel pick_attend(int dim, bool tiled)
+template <typename C, int QK, int PV, int D> AttendKernel pick_steps(bool tiled, bool brief)
 {
-    return dim <= 64 ? pick_tiled<C, QK, PV, 64>(tiled) : dim <= 128 ? pick_tiled<C, QK, PV, 128>(tiled) : pick_tiled<C, QK, PV, 256>(tiled);
+    if constexpr (Attend<C, QK, PV, D, true, 4>::kTiles > 2)
+        if (brief)
+            return pick_tiled<C, QK, PV, D, 2>(tiled);
+    return pick_tiled<C, QK, PV, D, 4>(tiled);
+}
+template <typename C, int QK, int PV> AttendKernel pick_attend(int dim, bool tiled, bool brief)
+{
+    return dim <= 64    ? pick_steps<C, QK, PV, 64>(tiled, brief)
+           : dim <= 128 ? pick_steps<C, QK, PV, 128>(tiled, brief)
+                        : pick_steps<C, QK, PV, 256>(tiled, brief);
 }
 
 }  // namespace detfold_impl

@@ -25,7 +25,7 @@ template <int LANES> __global__ __launch_bounds__(64 * kJoinWaves) void k_join_p
     const int64_t unit = h * (int64_t)p.tiles.d + in / 16, heads = min(16, p.group), units = (int64_t)p.units.d * p.beside;
     int n = (int)p.parts.d;
     int64_t first, next, step;  // slots
-    if (p.shares) {
+    if (p.shares.d) {
         const int2 cut = p.cut[b];
         n = cut.y - cut.x + 1;
         if (n == 1)
@@ -99,9 +99,9 @@ int launch_attend(const AttendArgs &a, void *stream)
 {
     const bool wide = a.a.out_type == DETFOLD_F32;
     const int dim = a.c.dim > a.c.v_dim ? a.c.dim : a.c.v_dim;
-    const AttendKernel k = a.a.type == DETFOLD_F32    ? attend_f32(a.c.type, dim, a.tiled)
-                           : a.a.type == DETFOLD_BF16 ? attend_bf16(a.c.type, wide, dim, a.tiled)
-                                                      : attend_f16(a.c.type, wide, dim, a.tiled);
+    const AttendKernel k = a.a.type == DETFOLD_F32    ? attend_f32(a.c.type, dim, a.tiled, a.brief)
+                           : a.a.type == DETFOLD_BF16 ? attend_bf16(a.c.type, wide, dim, a.tiled, a.brief)
+                                                      : attend_f16(a.c.type, wide, dim, a.tiled, a.brief);
     AttendArgs copy = a;
     void *args[] = {&copy};
     // Rows to a launch, whatever a row's workgroups.
@@ -116,14 +116,14 @@ int launch_attend(const AttendArgs &a, void *stream)
     };
     const int threads = 64 * a.waves, heads = a.group < 16 ? a.group : 16;
     const int queries = a.beside * k.q_bytes, sums = a.waves * (128 + heads * k.head_bytes), lds = queries > sums ? queries : sums;
-    if (a.shares) {
-        if (hipLaunchKernel(k.f, dim3(a.shares * a.units.d), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) != hipSuccess)
+    if (a.shares.d) {
+        if (hipLaunchKernel(k.f, dim3(a.shares.d * a.units.d), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) != hipSuccess)
             return DETFOLD_ELAUNCH;
     } else if (!rows((int64_t)a.units.d * a.parts.d, k.f, threads, lds)) {
         return DETFOLD_ELAUNCH;
     }
     const void *join = a.c.v_dim <= 64 ? (const void *)k_join_parts<16> : a.c.v_dim <= 128 ? (const void *)k_join_parts<32> : (const void *)k_join_parts<64>;
-    if ((a.shares || a.parts.d > 1) && !rows(a.a.q_heads, join, 64 * kJoinWaves, 0))
+    if ((a.shares.d || a.parts.d > 1) && !rows(a.a.q_heads, join, 64 * kJoinWaves, 0))
         return DETFOLD_ELAUNCH;
     return DETFOLD_OK;
 }

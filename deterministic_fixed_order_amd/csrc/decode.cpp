@@ -15,7 +15,7 @@ namespace {
 constexpr int64_t kMaxCount = (int64_t)1 << 31;   // counts that the kernels hold in 32 bits
 constexpr int64_t kMaxElems = (int64_t)1 << 46;   // extent of one buffer, in elements
 constexpr int32_t kMaxHeads = 1 << 16;
-constexpr int64_t kGroupsPerCu = 1;               // workgroups of the attention per compute unit
+constexpr int64_t kWavesPerCu = 8;                // of the attention, resident
 constexpr int64_t kShort = 256;                   // tokens that one workgroup takes by itself
 constexpr int64_t kStepBytes = 32768;              // of the cache that keep a wave's loads in flight
 constexpr int64_t kMaxEven = 4096;                // rows that every workgroup adds up the lengths of
@@ -165,18 +165,28 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
         return DETFOLD_EINVAL;
     const int64_t group = q_heads / c.heads, tiles = (group + 15) / 16, units = c.heads * tiles;
     const int64_t seen = window > 0 && window < max_len ? window : max_len;
-    const int64_t full = (int64_t)cu_count * kGroupsPerCu;  // workgroups that fill the device
+    const int64_t full = cu_count, waves = (int64_t)cu_count * kWavesPerCu;
     p->units = batch * units;
     p->shares = 0;
     p->waves = wide || 64 * (c.dim + c.v_dim) * elem_size(c.type) < kStepBytes ? 8 : 4;
     p->beside = units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
+    p->brief = seen <= 32;
     const int64_t groups = units / p->beside;
     int64_t part = split > 0 ? split : kLongPart;
     if (split == 0) {
         if (seen <= kShort) {
             part = kShort;
-        } else if (batch > 0 && groups <= full / 2 && batch <= kMaxEven && batch * (seen / 32 + 2) < kMaxCount) {
-            p->shares = full / groups;
+        } else if (batch > 0 && groups <= full / 2 && batch <= kMaxEven && batch * (seen / 32 + 2) < kMaxCount / 2) {
+            // Where one step for every wave that the device holds is enough, the
+            // least steps, and no more waves than heads; else a workgroup per
+            // compute unit.
+            if (batch * (seen / 32 + 2) <= waves / units) {
+                p->brief = true;
+                p->shares = waves / units;
+                p->waves = p->beside;
+            } else {
+                p->shares = full / groups;
+            }
             const int64_t even = (batch * seen + p->shares - 1) / p->shares, half = (seen + 1) / 2;
             part = even < half ? even : half;
         } else if (batch > 0 && seen > kMaxBlocks / p->units * part) {
@@ -191,14 +201,15 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
     // shares does not depend on them.
     const int64_t each = (group < 16 ? group : 16) * ((int64_t)c.v_dim + 2) * 4;
     const int64_t least = split > 0 ? split : kLongPart, most = (max_len + least - 1) / least;
-    const int64_t shared = split == 0 && groups <= full / 2 ? 2 * (full / groups) * units : 0;
+    const int64_t most_shares = waves / units > full / groups ? waves / units : full / groups;
+    const int64_t shared = split == 0 && groups <= full / 2 ? 2 * most_shares * units : 0;
     if (p->units > kMaxElems / 16 || (split > 0 && p->units > 0 && most > kMaxElems / p->units))
         return DETFOLD_EINVAL;
     int64_t upto = most == 1 ? 0 : split > 0 || p->units < kMaxBlocks ? p->units * most : kMaxBlocks + 2 * p->units;
     if (split == 0 && upto > kMaxBlocks + 2 * p->units)
         upto = kMaxBlocks + 2 * p->units;
     upto = upto > shared ? upto : shared;
-    p->slots = p->shares ? shared : p->splits > 1 ? p->units * p->splits : 0;
+    p->slots = p->shares ? 2 * p->shares * units : p->splits > 1 ? p->units * p->splits : 0;
     p->workspace_bytes = batch > 0 ? p->slots * each + (p->shares ? batch * 8 : 0) : 0;
     p->workspace_upto = batch > 0 && max_len > (split > 0 ? split : kShort) ? upto * each + batch * 8 : 0;
     return DETFOLD_OK;
@@ -351,7 +362,9 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
     k.beside = p.beside;
     k.units = divider((uint32_t)cache->heads * k.tiles.d / p.beside);
     k.parts = divider((uint32_t)(p.shares ? 1 : p.splits));
-    k.shares = (uint32_t)p.shares;
+    k.shares = p.shares ? divider((uint32_t)p.shares) : Divider{0, 0, 0};
+    k.unit = p.brief ? 5 : 6;
+    k.brief = p.brief;
     k.split = p.split;
     k.tiled = attend_tiled(*cache);
     k.waves = p.waves;

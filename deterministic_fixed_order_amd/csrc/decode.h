@@ -59,7 +59,9 @@ struct AttendArgs {
                     // tiles of 16 query heads) over those that lie beside each other in one
     Divider tiles;  // of a key-value head's query heads
     Divider parts;  // of every row's length, split tokens each, or
-    uint32_t shares;  // even shares of all rows' tokens (0: parts)
+    Divider shares; // even shares of all rows' tokens (0: parts),
+    int32_t unit;   // counted in 2^unit tokens
+    int32_t brief;  // steps of 32 tokens at most
     int32_t group;  // query heads of a key-value head
     int64_t split;
     int64_t row0;   // first row of the launch
@@ -75,18 +77,15 @@ struct AttendArgs {
     int2 *cut;      // first and last share of each row
 };
 
-constexpr int kUnit = 64;     // tokens that shares are counted in
-constexpr int kMinShare = 1;  // of these, at least, in a share
-
 // A kernel of the attention and the LDS it takes: for the queries, and for the
 // sums of a wave's query head.
 struct AttendKernel {
     const void *f;
     int q_bytes, head_bytes;
 };
-AttendKernel attend_bf16(int cache, bool wide, int dim, bool tiled);
-AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled);
-AttendKernel attend_f32(int cache, int dim, bool tiled);
+AttendKernel attend_bf16(int cache, bool wide, int dim, bool tiled, bool brief);
+AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled, bool brief);
+AttendKernel attend_f32(int cache, int dim, bool tiled, bool brief);
 
 struct SoftmaxArgs {
     void *out;
@@ -109,6 +108,7 @@ int check_softmax(const SoftmaxArgs &s);
 struct AttendPlan : detfold_attend_plan {
     int64_t shares, slots;
     int32_t waves, beside;
+    bool brief;
 };
 int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
                 int64_t window, int32_t split, bool wide, int32_t cu_count, AttendPlan *p);
