@@ -89,7 +89,7 @@ template <typename F> __device__ __forceinline__ float over_groups(float x, F f)
 // A uniform read of what no kernel writes meanwhile.  As a vector load it
 // would be counted with the loads of the cache, in order, and waiting for it
 // would wait for them.
-__device__ __forceinline__ int32_t scalar_load(const int32_t *p) { return *(const __attribute__((address_space(4))) int32_t *)p; }
+template <typename T> __device__ __forceinline__ T scalar_load(const T *p) { return *(const __attribute__((address_space(4))) T *)p; }
 
 __device__ __forceinline__ int64_t from_lane(int64_t x, int l)
 {
@@ -220,6 +220,10 @@ __device__ __forceinline__ Share find_share(const AttendArgs &p, uint32_t y, boo
     return w;
 }
 
+template <bool B> struct Last {
+    static constexpr bool value = B;
+};
+
 // MOST: tiles of 16 tokens in a step, at most.
 template <typename C, int QK, int PV, int D, bool TILED, int MOST> struct Attend {
     static constexpr int kSize = sizeof(C);
@@ -279,8 +283,8 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     const char *k0 = (const char *)c.k + (int64_t)h * c.k_head * CS, *v0 = (const char *)c.v + (int64_t)h * c.v_head * CS;
     const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
     const uint32_t pages = (uint32_t)c.pages;
-    const float by = a.scale * (c.k_scale ? c.k_scale[h] : 1.0f) * kLog2e;
-    const float v_scale = c.v_scale ? c.v_scale[h] : 1.0f;
+    const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f) * kLog2e;
+    const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
     const bool ragged = c.dim % (4 * E) != 0;
 
     // Where a lane's loads lie within a key and a value.
@@ -415,9 +419,12 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         now = look_up(min(s + turns, steps - 1));
     }
     __syncthreads();
-    for (; s < steps; s += turns) {
+    // One step; but for the last one it also issues the next one's loads, and
+    // is compiled for that alone: with a branch instead, the wait for the values
+    // would have to take the keys issued after them for values not yet there.
+    auto step = [&](auto last_one) {
+        constexpr bool more = !decltype(last_one)::value;
         const uint32_t t0 = a0 + s * S::kStep;
-        const bool more = s + turns < steps;
         const uint32_t q_at = anew(lane) * 16;
         if (CS != 1 && ragged) {  // what a key's last chunk repeats: zero times infinity would be NaN
 #pragma unroll
@@ -458,7 +465,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
                 }
             }
         }
-        if (more) {
+        if constexpr (more) {
             next = look_up(min(s + 2 * turns, steps - 1));
             load_keys(now);
         }
@@ -541,11 +548,15 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
                     }
             }
         }
-        if (more) {
+        if constexpr (more) {
             load_values(now);
             now = next;
         }
-    }
+    };
+    for (; s + turns < steps; s += turns)
+        step(Last<false>{});
+    if (s < steps)
+        step(Last<true>{});
 
     l = over_groups(l, [](float y, float z) { return y + z; });
     if (PV == kF16) {
