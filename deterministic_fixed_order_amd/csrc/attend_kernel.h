@@ -164,7 +164,7 @@ __device__ __forceinline__ RowTokens row_tokens(const AttendArgs &p, int32_t len
     r.end = r.bad ? 0 : (uint32_t)n;
     r.begin = p.a.window > 0 && r.end > p.a.window ? (uint32_t)(r.end - p.a.window) : 0;
     r.a0 = tiled ? r.begin & ~15u : r.begin;
-    r.units = r.end > r.begin ? (r.end - r.a0 + (1u << p.unit) - 1) >> p.unit : 1;
+    r.units = r.end > r.begin ? (r.end - r.a0 + kUnit - 1) / kUnit : 1;
     return r;
 }
 
@@ -233,7 +233,7 @@ template <typename C, int QK, int PV, int D, bool TILED, int MOST> struct Attend
     static constexpr int kMost = D < 256 ? MOST : QK == kF32 ? 1 : 2;
     static constexpr int kTiles = kFit < kMost ? kFit : kMost;  // of a step
     static constexpr int kStep = 16 * kTiles;
-    static constexpr int kWide = D >= 128 ? 8 : 4;    // dims of a value that a lane holds together
+    static constexpr int kWide = kChunk < D / 16 ? kChunk : D / 16;  // dims of a value that a lane loads together
     static constexpr int kParts = D / (16 * kWide);
     static constexpr int kTokens = 4 * kTiles;        // tokens whose values a lane loads
     static constexpr int kQ = (QK == kF32 ? 4 : 2) * D * 16;  // LDS bytes of the queries
@@ -307,8 +307,8 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
             slot = ((int64_t)y * (p.units.d * beside) + unit) * 2 + (x == 0);
         if (x == 0 && unit == 0 && lane == 0 && turn == 0)
             p.cut[b] = make_int2((int)y, (int)(done < row.units ? (mine.at + row.units - 1) / mine.each : y));
-        end = x + done < row.units ? row.a0 + ((x + done) << p.unit) : end;
-        begin = x ? row.a0 + (x << p.unit) : begin;
+        end = x + done < row.units ? row.a0 + kUnit * (x + done) : end;
+        begin = x ? row.a0 + kUnit * x : begin;
     } else if (p.parts.d > 1) {
         slot = (b * p.parts.d + part) * (p.units.d * beside) + unit;
         const int64_t x = begin + part * p.split;

@@ -176,17 +176,14 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
     if (split == 0) {
         if (seen <= kShort) {
             part = kShort;
+        } else if (batch > 0 && batch * ((seen + 31) / 32) <= waves / units) {
+            // One step for every wave that the device holds is enough: the
+            // least steps, and no more waves to a workgroup than heads.
+            part = DETFOLD_ATTEND_STEP;
+            p->brief = true;
+            p->waves = p->beside;
         } else if (batch > 0 && groups <= full / 2 && batch <= kMaxEven && batch * (seen / 32 + 2) < kMaxCount / 2) {
-            // Where one step for every wave that the device holds is enough, the
-            // least steps, and no more waves than heads; else a workgroup per
-            // compute unit.
-            if (batch * (seen / 32 + 2) <= waves / units) {
-                p->brief = true;
-                p->shares = waves / units;
-                p->waves = p->beside;
-            } else {
-                p->shares = full / groups;
-            }
+            p->shares = full / groups;
             const int64_t even = (batch * seen + p->shares - 1) / p->shares, half = (seen + 1) / 2;
             part = even < half ? even : half;
         } else if (batch > 0 && seen > kMaxBlocks / p->units * part) {
@@ -201,8 +198,7 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
     // shares does not depend on them.
     const int64_t each = (group < 16 ? group : 16) * ((int64_t)c.v_dim + 2) * 4;
     const int64_t least = split > 0 ? split : kLongPart, most = (max_len + least - 1) / least;
-    const int64_t most_shares = waves / units > full / groups ? waves / units : full / groups;
-    const int64_t shared = split == 0 && groups <= full / 2 ? 2 * most_shares * units : 0;
+    const int64_t shared = split > 0 ? 0 : groups <= full / 2 && 2 * (full / groups) * units > waves ? 2 * (full / groups) * units : waves;
     if (p->units > kMaxElems / 16 || (split > 0 && p->units > 0 && most > kMaxElems / p->units))
         return DETFOLD_EINVAL;
     int64_t upto = most == 1 ? 0 : split > 0 || p->units < kMaxBlocks ? p->units * most : kMaxBlocks + 2 * p->units;
@@ -363,7 +359,6 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
     k.units = divider((uint32_t)cache->heads * k.tiles.d / p.beside);
     k.parts = divider((uint32_t)(p.shares ? 1 : p.splits));
     k.shares = p.shares ? divider((uint32_t)p.shares) : Divider{0, 0, 0};
-    k.unit = p.brief ? 5 : 6;
     k.brief = p.brief;
     k.split = p.split;
     k.tiled = attend_tiled(*cache);

@@ -59,8 +59,7 @@ struct AttendArgs {
                     // tiles of 16 query heads) over those that lie beside each other in one
     Divider tiles;  // of a key-value head's query heads
     Divider parts;  // of every row's length, split tokens each, or
-    Divider shares; // even shares of all rows' tokens (0: parts),
-    int32_t unit;   // counted in 2^unit tokens
+    Divider shares; // even shares of all rows' tokens (0: parts)
     int32_t brief;  // steps of 32 tokens at most
     int32_t group;  // query heads of a key-value head
     int64_t split;
@@ -76,6 +75,8 @@ struct AttendArgs {
     float2 *ml;     // maxima and sums of weights [slot][head]
     int2 *cut;      // first and last share of each row
 };
+
+constexpr int kUnit = 64;  // tokens that shares are counted in
 
 // A kernel of the attention and the LDS it takes: for the queries, and for the
 // sums of a wave's query head.
