@@ -6,11 +6,12 @@
 
 namespace detfold_impl {
 
-AttendKernel attend_bf16(int cache, bool wide, int dim, bool tiled, bool brief)
+AttendKernel attend_bf16(const AttendArgs &a)
 {
-    if (cache == DETFOLD_E4M3)
-        return wide ? pick_attend<e4m3, kBf16, kF32>(dim, tiled, brief) : pick_attend<e4m3, kBf16, kBf16>(dim, tiled, brief);
-    return wide ? pick_attend<bf16, kBf16, kF32>(dim, tiled, brief) : pick_attend<bf16, kBf16, kBf16>(dim, tiled, brief);
+    const bool wide = a.a.out_type == DETFOLD_F32;
+    if (a.c.type == DETFOLD_E4M3)
+        return wide ? pick_attend<e4m3, kBf16, kF32>(a) : pick_attend<e4m3, kBf16, kBf16>(a);
+    return wide ? pick_attend<bf16, kBf16, kF32>(a) : pick_attend<bf16, kBf16, kBf16>(a);
 }
 
 }  // namespace detfold_impl

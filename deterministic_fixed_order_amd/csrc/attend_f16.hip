@@ -6,11 +6,12 @@
 
 namespace detfold_impl {
 
-AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled, bool brief)
+AttendKernel attend_f16(const AttendArgs &a)
 {
-    if (cache == DETFOLD_E4M3)
-        return wide ? pick_attend<e4m3, kF16, kF32>(dim, tiled, brief) : pick_attend<e4m3, kF16, kF16>(dim, tiled, brief);
-    return wide ? pick_attend<f16, kF16, kF32>(dim, tiled, brief) : pick_attend<f16, kF16, kF16>(dim, tiled, brief);
+    const bool wide = a.a.out_type == DETFOLD_F32;
+    if (a.c.type == DETFOLD_E4M3)
+        return wide ? pick_attend<e4m3, kF16, kF32>(a) : pick_attend<e4m3, kF16, kF16>(a);
+    return wide ? pick_attend<f16, kF16, kF32>(a) : pick_attend<f16, kF16, kF16>(a);
 }
 
 }  // namespace detfold_impl

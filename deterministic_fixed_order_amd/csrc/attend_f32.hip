@@ -6,11 +6,11 @@
 
 namespace detfold_impl {
 
-AttendKernel attend_f32(int cache, int dim, bool tiled, bool brief)
+AttendKernel attend_f32(const AttendArgs &a)
 {
-    if (cache == DETFOLD_E4M3)
-        return pick_attend<e4m3, kF32, kF32>(dim, tiled, brief);
-    return cache == DETFOLD_BF16 ? pick_attend<bf16, kF32, kF32>(dim, tiled, brief) : pick_attend<float, kF32, kF32>(dim, tiled, brief);
+    if (a.c.type == DETFOLD_E4M3)
+        return pick_attend<e4m3, kF32, kF32>(a);
+    return a.c.type == DETFOLD_BF16 ? pick_attend<bf16, kF32, kF32>(a) : pick_attend<float, kF32, kF32>(a);
 }
 
 }  // namespace detfold_impl

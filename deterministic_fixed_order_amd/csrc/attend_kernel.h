@@ -18,13 +18,18 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-// N bytes of the cache, read once: at any alignment that a head's start may
-// have (one wide load all the same), and not kept in the caches.
+// N bytes of the cache at any alignment that a head's start may have (one wide
+// load all the same); once: not kept in the caches.
 template <int N> struct Words {
     uint32_t w[N / 4];
 };
-template <int N> __device__ __forceinline__ Words<N> load_words(const char *p)
+template <int N, bool ONCE> __device__ __forceinline__ Words<N> load_words(const char *p)
 {
+    if constexpr (!ONCE) {
+        Words<N> r;
+        __builtin_memcpy(&r, p, N);
+        return r;
+    }
     typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
     typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
     typedef uint32_t v1 __attribute__((aligned(1)));
@@ -224,8 +229,8 @@ template <bool B> struct Last {
     static constexpr bool value = B;
 };
 
-// MOST: tiles of 16 tokens in a step, at most.
-template <typename C, int QK, int PV, int D, bool TILED, int MOST> struct Attend {
+// MOST: tiles of 16 tokens in a step, at most.  KEEP: what the caches keep.
+template <typename C, int QK, int PV, int D, bool TILED, int MOST, int KEEP> struct Attend {
     static constexpr int kSize = sizeof(C);
     static constexpr int kChunk = 16 / kSize;         // dims of one 16-byte load of a key
     static constexpr int kChunks = D / (4 * kChunk);  // of these per lane and key
@@ -242,10 +247,10 @@ template <typename C, int QK, int PV, int D, bool TILED, int MOST> struct Attend
     static_assert(kTiles % 2 == 0 || PV == kF32, "the 16-bit products take 32 tokens");
 };
 
-template <typename C, int QK, int PV, int D, bool TILED, int MOST>
+template <typename C, int QK, int PV, int D, bool TILED, int MOST, int KEEP>
 __global__ __launch_bounds__(512) void k_attend(AttendArgs)
 {
-    typedef Attend<C, QK, PV, D, TILED, MOST> S;
+    typedef Attend<C, QK, PV, D, TILED, MOST, KEEP> S;
     constexpr int CS = S::kSize, E = S::kChunk, NC = S::kChunks, UT = S::kTiles, VW = S::kWide, NP = S::kParts, NT = S::kTokens;
     extern __shared__ __align__(16) char lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -369,7 +374,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
             const char *k = k0 + (TILED ? valid(g.id[u % IDS]) * k_page + g.off[u % IDS] * k_token : from_lane(at, 16 * u + col));
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                kw[u][i] = load_words<16>(k + anew(k_at[i]));
+                kw[u][i] = load_words<16, KEEP == kNothing>(k + anew(k_at[i]));
         }
     };
     auto load_values = [&](const Pages &g) {
@@ -382,7 +387,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
                                         : from_lane(at, 16 * (j / 4) + 4 * grp + j % 4));
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                vw[j][i] = load_words<VW * CS>(v + anew(v_at[i]));
+                vw[j][i] = load_words<VW * CS, KEEP != kAll>(v + anew(v_at[i]));
         }
     };
 
@@ -632,25 +637,29 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     }
 }
 
-// The kernel for a head size, for tiles within a page or anywhere, and for long
-// steps or short ones.
-template <typename C, int QK, int PV, int D, int MOST> AttendKernel pick_tiled(bool tiled)
+// The kernel of a call, of those that one can need: short steps read little and
+// keep it, and only whole rows of 512 bytes or more keep nothing.
+template <typename C, int QK, int PV, int D, int MOST, int KEEP> AttendKernel pick_tiled(const AttendArgs &a)
 {
-    typedef Attend<C, QK, PV, D, true, MOST> S;
-    return {tiled ? (const void *)k_attend<C, QK, PV, D, true, MOST> : (const void *)k_attend<C, QK, PV, D, false, MOST>, S::kQ, S::kRow * 4};
+    typedef Attend<C, QK, PV, D, true, MOST, KEEP> S;
+    const void *f = a.tiled ? (const void *)k_attend<C, QK, PV, D, true, MOST, KEEP>
+                            : (const void *)k_attend<C, QK, PV, D, false, MOST, KEEP == kNothing ? kKeys : KEEP>;
+    return {f, S::kQ, S::kRow * 4};
 }
-template <typename C, int QK, int PV, int D> AttendKernel pick_steps(bool tiled, bool brief)
+template <typename C, int QK, int PV, int D> AttendKernel pick_steps(const AttendArgs &a)
 {
-    if constexpr (Attend<C, QK, PV, D, true, 4>::kTiles > 2)
-        if (brief)
-            return pick_tiled<C, QK, PV, D, 2>(tiled);
-    return pick_tiled<C, QK, PV, D, 4>(tiled);
+    if constexpr (Attend<C, QK, PV, D, true, 4, kAll>::kTiles > 2)
+        if (a.brief)
+            return pick_tiled<C, QK, PV, D, 2, kAll>(a);
+    if constexpr (D * sizeof(C) >= 512)
+        if (a.keep == kNothing)
+            return pick_tiled<C, QK, PV, D, 4, kNothing>(a);
+    return a.keep == kAll ? pick_tiled<C, QK, PV, D, 4, kAll>(a) : pick_tiled<C, QK, PV, D, 4, kKeys>(a);
 }
-template <typename C, int QK, int PV> AttendKernel pick_attend(int dim, bool tiled, bool brief)
+template <typename C, int QK, int PV> AttendKernel pick_attend(const AttendArgs &a)
 {
-    return dim <= 64    ? pick_steps<C, QK, PV, 64>(tiled, brief)
-           : dim <= 128 ? pick_steps<C, QK, PV, 128>(tiled, brief)
-                        : pick_steps<C, QK, PV, 256>(tiled, brief);
+    const int dim = a.c.dim > a.c.v_dim ? a.c.dim : a.c.v_dim;
+    return dim <= 64 ? pick_steps<C, QK, PV, 64>(a) : dim <= 128 ? pick_steps<C, QK, PV, 128>(a) : pick_steps<C, QK, PV, 256>(a);
 }
 
 }  // namespace detfold_impl

@@ -97,11 +97,7 @@ template <int LANES> __global__ __launch_bounds__(64 * kJoinWaves) void k_join_p
 
 int launch_attend(const AttendArgs &a, void *stream)
 {
-    const bool wide = a.a.out_type == DETFOLD_F32;
-    const int dim = a.c.dim > a.c.v_dim ? a.c.dim : a.c.v_dim;
-    const AttendKernel k = a.a.type == DETFOLD_F32    ? attend_f32(a.c.type, dim, a.tiled, a.brief)
-                           : a.a.type == DETFOLD_BF16 ? attend_bf16(a.c.type, wide, dim, a.tiled, a.brief)
-                                                      : attend_f16(a.c.type, wide, dim, a.tiled, a.brief);
+    const AttendKernel k = a.a.type == DETFOLD_F32 ? attend_f32(a) : a.a.type == DETFOLD_BF16 ? attend_bf16(a) : attend_f16(a);
     AttendArgs copy = a;
     void *args[] = {&copy};
     // Rows to a launch, whatever a row's workgroups.

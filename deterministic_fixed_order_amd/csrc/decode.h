@@ -61,6 +61,7 @@ struct AttendArgs {
     Divider parts;  // of every row's length, split tokens each, or
     Divider shares; // even shares of all rows' tokens (0: parts)
     int32_t brief;  // steps of 32 tokens at most
+    int32_t keep;   // what the caches keep of the keys and values
     int32_t group;  // query heads of a key-value head
     int64_t split;
     int64_t row0;   // first row of the launch
@@ -76,6 +77,7 @@ struct AttendArgs {
     int2 *cut;      // first and last share of each row
 };
 
+enum Keep { kAll, kKeys, kNothing };
 constexpr int kUnit = 64;  // tokens that shares are counted in
 
 // A kernel of the attention and the LDS it takes: for the queries, and for the
@@ -84,9 +86,9 @@ struct AttendKernel {
     const void *f;
     int q_bytes, head_bytes;
 };
-AttendKernel attend_bf16(int cache, bool wide, int dim, bool tiled, bool brief);
-AttendKernel attend_f16(int cache, bool wide, int dim, bool tiled, bool brief);
-AttendKernel attend_f32(int cache, int dim, bool tiled, bool brief);
+AttendKernel attend_bf16(const AttendArgs &a);
+AttendKernel attend_f16(const AttendArgs &a);
+AttendKernel attend_f32(const AttendArgs &a);
 
 struct SoftmaxArgs {
     void *out;
@@ -114,6 +116,7 @@ struct AttendPlan : detfold_attend_plan {
 int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
                 int64_t window, int32_t split, bool wide, int32_t cu_count, AttendPlan *p);
 bool attend_tiled(const detfold_paged_cache &c);
+int attend_keep(const detfold_paged_cache &c, int tiles, bool brief);
 
 // --- cache_kernels.hip, attend_kernels.hip: launches --------------------------
 int launch_append(const AppendArgs &a, void *stream);
