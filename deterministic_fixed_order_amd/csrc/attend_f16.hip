@@ -10,7 +10,7 @@ AttendKernel attend_f16(const AttendArgs &a)
 {
     const bool wide = a.a.out_type == DETFOLD_F32;
     if (a.c.type == DETFOLD_E4M3)
-        return wide ? pick_attend<e4m3, kF16, kF32>(a) : pick_attend<e4m3, kF16, kF16>(a);
+        return wide ? pick_attend<e4m3, kF16, kSplit>(a) : pick_attend<e4m3, kF16, kF16>(a);
     return wide ? pick_attend<f16, kF16, kF32>(a) : pick_attend<f16, kF16, kF16>(a);
 }
 
