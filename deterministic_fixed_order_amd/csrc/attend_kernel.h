@@ -29,11 +29,6 @@ template <int N> struct Words {
 };
 template <int N, bool ONCE> __device__ __forceinline__ Words<N> load_words(const char *p)
 {
-    if constexpr (!ONCE) {
-        Words<N> r;
-        __builtin_memcpy(&r, p, N);
-        return r;
-    }
     typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
     typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
     typedef uint32_t v1 __attribute__((aligned(1)));
@@ -41,14 +36,14 @@ template <int N, bool ONCE> __device__ __forceinline__ Words<N> load_words(const
     if constexpr (N >= 16) {
 #pragma unroll
         for (int i = 0; i < N / 16; ++i) {
-            const v4 x = __builtin_nontemporal_load((const v4 *)p + i);
+            const v4 x = ONCE ? __builtin_nontemporal_load((const v4 *)p + i) : ((const v4 *)p)[i];
             r.w[4 * i] = x.x, r.w[4 * i + 1] = x.y, r.w[4 * i + 2] = x.z, r.w[4 * i + 3] = x.w;
         }
     } else if constexpr (N == 8) {
-        const v2 x = __builtin_nontemporal_load((const v2 *)p);
+        const v2 x = ONCE ? __builtin_nontemporal_load((const v2 *)p) : *(const v2 *)p;
         r.w[0] = x.x, r.w[1] = x.y;
     } else {
-        r.w[0] = __builtin_nontemporal_load((const v1 *)p);
+        r.w[0] = ONCE ? __builtin_nontemporal_load((const v1 *)p) : *(const v1 *)p;
     }
     return r;
 }
@@ -239,7 +234,9 @@ template <typename C, int QK, int PV, int D, bool TILED, int MOST, int KEEP> str
     static constexpr int kChunk = 16 / kSize;         // dims of one 16-byte load of a key
     static constexpr int kChunks = D / (4 * kChunk);  // of these per lane and key
     static constexpr int kFit = 1024 / (D * kSize);   // tiles of 16 tokens whose keys take 64 registers
-    static constexpr int kMost = D < 256 ? MOST : PV == kF32 && QK == kF32 ? 1 : 2;
+    // Halves converted to float32 are held apart, in twice the registers.
+    static constexpr bool kTwice = __is_same(C, f16) && PV == kF32;
+    static constexpr int kMost = D < 256 ? (kTwice ? 2 : MOST) : PV == kF32 && (QK == kF32 || kTwice) ? 1 : 2;
     static constexpr int kTiles = kFit < kMost ? kFit : kMost;  // of a step
     static constexpr int kStep = 16 * kTiles;
     static constexpr int kWide = kChunk < D / 16 ? kChunk : D / 16;  // dims of a value that a lane loads together
@@ -523,12 +520,13 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         // Values: the output's rows are its dims, its columns the query heads.
         if constexpr (PV == kF32) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
 #pragma unroll
                     for (int n = 0; n < VW; ++n)
                         acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(vw[j][i].w, n), x[j / 4][j % 4], acc[i][n], 0, 0, 0);
+            }
         } else {
 #pragma unroll
             for (int u = 0; u < UT; u += 2) {

@@ -8,7 +8,8 @@
 namespace detfold_impl {
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 256;                      // threads of the append
+constexpr int kFold = 128;                       // and of the fold
 constexpr int64_t kOnceBytes = 8 << 20;          // of an output that is not kept in the caches
 constexpr int kHeads = 2;
 constexpr int64_t kFill = 1 << 18;               // threads that fill the device
@@ -16,7 +17,7 @@ constexpr int64_t kMaxItems = (int64_t)1 << 30;  // threads of a launch: a grid 
 
 // Workgroup b of n, of which each XCD takes runs of kRun neighbours (workgroups
 // go to the XCDs round-robin): an XCD's share of a stream is then contiguous.
-constexpr int kRun = 16;
+constexpr int kRun = 256;
 __device__ __forceinline__ uint32_t in_runs(uint32_t b, uint32_t n)
 {
     constexpr uint32_t span = 8 * kRun;
@@ -188,10 +189,10 @@ template <typename T, typename C, int V, int HEADS> __global__ __launch_bounds__
 // The softmax fold.  A thread takes V neighbouring values of a row, eight
 // partials' loads at a time, and forms the row's weights itself: eight
 // exponentials cost less than handing them round.
-template <typename T, int V, bool ONCE> __global__ __launch_bounds__(kBlock) void k_fold_softmax(SoftmaxArgs s)
+template <typename T, int V, bool ONCE> __global__ __launch_bounds__(kFold) void k_fold_softmax(SoftmaxArgs s)
 {
     constexpr int N = 8;
-    const uint32_t i = in_runs(blockIdx.x, gridDim.x) * kBlock + threadIdx.x, in = divide(i, s.chunks), u = i - in * s.chunks.d;
+    const uint32_t i = in_runs(blockIdx.x, gridDim.x) * kFold + threadIdx.x, in = divide(i, s.chunks), u = i - in * s.chunks.d;
     if (in >= s.count)
         return;
     const int64_t row = s.row0 + in, at = row * s.dim + min((int64_t)u * V, s.dim - V);
@@ -281,10 +282,10 @@ int width(int type, bool overlap, int64_t a, int64_t b, int64_t c)
 }
 int chunks(int64_t n, int v) { return (int)((n + v - 1) / v); }
 
-bool launch(const void *k, int64_t blocks, void *args, void *stream)
+bool launch(const void *k, int64_t blocks, int threads, void *args, void *stream)
 {
     void *list[] = {args};
-    return hipLaunchKernel(k, dim3((unsigned)blocks), dim3(kBlock), list, 0, static_cast<hipStream_t>(stream)) == hipSuccess;
+    return hipLaunchKernel(k, dim3((unsigned)blocks), dim3(threads), list, 0, static_cast<hipStream_t>(stream)) == hipSuccess;
 }
 
 }  // namespace
@@ -309,7 +310,7 @@ int launch_append(const AppendArgs &a, void *stream)
     for (p.token0 = 0; p.token0 < a.a.tokens; p.token0 += some) {
         p.tokens = (uint32_t)(a.a.tokens - p.token0 < some ? a.a.tokens - p.token0 : some);
         p.turn = (uint32_t)((p.tokens * each + kBlock - 1) / kBlock);
-        if (!launch(k, p.turn + (p.tokens * v_each + kBlock - 1) / kBlock, &p, stream))
+        if (!launch(k, p.turn + (p.tokens * v_each + kBlock - 1) / kBlock, kBlock, &p, stream))
             return DETFOLD_ELAUNCH;
     }
     return DETFOLD_OK;
@@ -325,7 +326,7 @@ int launch_softmax(const SoftmaxArgs &a, void *stream)
     const int64_t some = kMaxItems / p.chunks.d;
     for (p.row0 = 0; p.row0 < a.rows; p.row0 += some) {
         p.count = (uint32_t)(a.rows - p.row0 < some ? a.rows - p.row0 : some);
-        if (!launch(k, ((int64_t)p.count * p.chunks.d + kBlock - 1) / kBlock, &p, stream))
+        if (!launch(k, ((int64_t)p.count * p.chunks.d + kFold - 1) / kFold, kFold, &p, stream))
             return DETFOLD_ELAUNCH;
     }
     return DETFOLD_OK;
