@@ -268,8 +268,11 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     Share mine = {};
     if (p0.shares.d) {
         mine = find_share(p0, y, TILED);
-        if (mine.left == 0)
+        if (mine.left == 0) {
+            if (!p0.by_row && unit == 0 && threadIdx.x == 0)
+                p0.cut[y] = make_int3(-1, 0, 0);
             return;
+        }
         b = mine.row;
     } else {
         const uint32_t row = divide(y, p0.parts);
@@ -311,8 +314,10 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         done = min(row.units - x, mine.left);
         if (done < row.units)
             slot = ((int64_t)y * (p.units.d * beside) + unit) * 2 + (x == 0);
-        if (x == 0 && unit == 0 && lane == 0 && turn == 0)
-            p.cut[b] = make_int2((int)y, (int)(done < row.units ? (mine.at + row.units - 1) / mine.each : y));
+        if (unit == 0 && lane == 0 && turn == 0 && (p.by_row ? x == 0 : done == mine.left)) {
+            const bool cut = x == 0 && done < row.units;  // it begins here, and does not end here
+            p.cut[p.by_row ? b : y] = make_int3(cut ? (int)b : -1, (int)y, cut ? (int)((mine.at + row.units - 1) / mine.each) : 0);
+        }
         end = x + done < row.units ? row.a0 + kUnit * (x + done) : end;
         begin = x ? row.a0 + kUnit * x : begin;
     } else if (p.parts.d > 1) {

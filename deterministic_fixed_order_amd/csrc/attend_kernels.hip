@@ -8,30 +8,31 @@
 namespace detfold_impl {
 namespace {
 
-constexpr int kJoinWaves = 8;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds at most 2^32 threads
 
-// One workgroup per row and query head.  A lane takes four dims, LANES lanes a
-// part, and the groups of lanes every 512 / LANES-th part; their sums are added
-// in order.  Parts that are empty add zeros, so a row's bits do not depend on
-// how many follow its last one.
-template <int LANES> __global__ __launch_bounds__(64 * kJoinWaves) void k_join_parts(AttendArgs p)
+// One workgroup per query head and row, or share that a row may begin in without
+// ending there.  A lane takes four dims, LANES lanes a part, and the groups of
+// lanes every GROUPS-th part; their sums are added in order.  Parts that are
+// empty add zeros, so a row's bits do not depend on how many follow its last one.
+template <int LANES, int WAVES> __global__ __launch_bounds__(64 * WAVES) void k_join_parts(AttendArgs p)
 {
-    constexpr int GROUPS = 64 * kJoinWaves / LANES;
+    constexpr int GROUPS = 64 * WAVES / LANES;
     const detfold_attend &a = p.a;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    const int64_t b = p.row0 + blockIdx.x / a.q_heads;
-    const int head = blockIdx.x % a.q_heads, h = head / p.group, in = head - h * p.group;
+    const uint32_t y = blockIdx.x / a.q_heads;
+    const int head = blockIdx.x - y * a.q_heads, h = head / p.group, in = head - h * p.group;
     const int64_t unit = h * (int64_t)p.tiles.d + in / 16, heads = min(16, p.group), units = (int64_t)p.units.d * p.beside;
+    int64_t b = p.row0 + y;
     int n = (int)p.parts.d;
     int64_t first, next, step;  // slots
     if (p.shares.d) {
-        const int2 cut = p.cut[b];
-        n = cut.y - cut.x + 1;
-        if (n == 1)
+        const int3 cut = p.cut[y];
+        if (cut.x < 0)
             return;
+        b = cut.x;
+        n = cut.z - cut.y + 1;
         step = 2 * units;
-        next = (cut.x * units + unit) * 2;
+        next = (cut.y * units + unit) * 2;
         first = next + 1;
     } else {
         step = units;
@@ -93,6 +94,11 @@ template <int LANES> __global__ __launch_bounds__(64 * kJoinWaves) void k_join_p
         a.lse[b * a.q_heads + head] = log_sum(top, l);
 }
 
+template <int WAVES> const void *pick_join(int dim)
+{
+    return dim <= 64 ? (const void *)k_join_parts<16, WAVES> : dim <= 128 ? (const void *)k_join_parts<32, WAVES> : (const void *)k_join_parts<64, WAVES>;
+}
+
 }  // namespace
 
 int launch_attend(const AttendArgs &a, void *stream)
@@ -100,26 +106,33 @@ int launch_attend(const AttendArgs &a, void *stream)
     const AttendKernel k = a.a.type == DETFOLD_F32 ? attend_f32(a) : a.a.type == DETFOLD_BF16 ? attend_bf16(a) : attend_f16(a);
     AttendArgs copy = a;
     void *args[] = {&copy};
-    // Rows to a launch, whatever a row's workgroups.
+    auto launch = [&](const void *f, int64_t blocks, int threads, int lds) {
+        return hipLaunchKernel(f, dim3((unsigned)blocks), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) == hipSuccess;
+    };
+    // Some rows to a launch, whatever a row's workgroups.
     auto rows = [&](int64_t each, const void *f, int threads, int lds) {
         const int64_t some = each < kMaxBlocks ? kMaxBlocks / each : 1;
-        for (copy.row0 = 0; copy.row0 < a.a.batch; copy.row0 += some) {
-            const int64_t now = a.a.batch - copy.row0 < some ? a.a.batch - copy.row0 : some;
-            if (hipLaunchKernel(f, dim3((unsigned)(now * each)), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) != hipSuccess)
+        for (copy.row0 = 0; copy.row0 < a.a.batch; copy.row0 += some)
+            if (!launch(f, (a.a.batch - copy.row0 < some ? a.a.batch - copy.row0 : some) * each, threads, lds))
                 return false;
-        }
         return true;
     };
-    const int threads = 64 * a.waves, heads = a.group < 16 ? a.group : 16;
+    const int heads = a.group < 16 ? a.group : 16;
     const int queries = a.beside * k.q_bytes, sums = a.waves * (128 + heads * k.head_bytes), lds = queries > sums ? queries : sums;
     if (a.shares.d) {
-        if (hipLaunchKernel(k.f, dim3(a.shares.d * a.units.d), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) != hipSuccess)
-            return DETFOLD_ELAUNCH;
-    } else if (!rows((int64_t)a.units.d * a.parts.d, k.f, threads, lds)) {
-        return DETFOLD_ELAUNCH;
+        // Where rows have few parts, what counts is how many waves look for one:
+        // 64 ragged rows 5 us with two a workgroup, 12 with eight, which take 5
+        // us less than two where 16 rows have eight parts each.
+        const bool few = a.a.batch * 4 >= a.shares.d;
+        return launch(k.f, (int64_t)a.shares.d * a.units.d, 64 * a.waves, lds) &&
+                       launch(few ? pick_join<2>(a.c.v_dim) : pick_join<8>(a.c.v_dim), (a.by_row ? a.a.batch : a.shares.d) * a.a.q_heads,
+                              few ? 128 : 512, 0)
+                   ? DETFOLD_OK
+                   : DETFOLD_ELAUNCH;
     }
-    const void *join = a.c.v_dim <= 64 ? (const void *)k_join_parts<16> : a.c.v_dim <= 128 ? (const void *)k_join_parts<32> : (const void *)k_join_parts<64>;
-    if ((a.shares.d || a.parts.d > 1) && !rows(a.a.q_heads, join, 64 * kJoinWaves, 0))
+    if (!rows((int64_t)a.units.d * a.parts.d, k.f, 64 * a.waves, lds))
+        return DETFOLD_ELAUNCH;
+    if (a.parts.d > 1 && !rows(a.a.q_heads, pick_join<8>(a.c.v_dim), 512, 0))
         return DETFOLD_ELAUNCH;
     return DETFOLD_OK;
 }

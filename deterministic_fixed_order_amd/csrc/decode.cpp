@@ -206,8 +206,8 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
         upto = kMaxBlocks + 2 * p->units;
     upto = upto > shared ? upto : shared;
     p->slots = p->shares ? 2 * p->shares * units : p->splits > 1 ? p->units * p->splits : 0;
-    p->workspace_bytes = batch > 0 ? p->slots * each + (p->shares ? batch * 8 : 0) : 0;
-    p->workspace_upto = batch > 0 && max_len > (split > 0 ? split : kShort) ? upto * each + batch * 8 : 0;
+    p->workspace_bytes = batch > 0 ? p->slots * each + p->shares * 12 : 0;
+    p->workspace_upto = batch > 0 && max_len > (split > 0 ? split : kShort) ? upto * each + full * 12 : 0;
     return DETFOLD_OK;
 }
 
@@ -382,7 +382,8 @@ int detfold_attend_paged(const detfold_paged_cache *cache, const detfold_attend 
     const int64_t heads = p.slots * (k.group < 16 ? k.group : 16);
     k.acc = (float *)args->workspace;
     k.ml = (float2 *)(k.acc + heads * cache->v_dim);
-    k.cut = (int2 *)(k.ml + heads);
+    k.cut = (int3 *)(k.ml + heads);
+    k.by_row = args->batch <= p.shares;
     return launch_attend(k, stream);
 }
 

@@ -74,7 +74,11 @@ struct AttendArgs {
     // ends within.
     float *acc;     // sums [slot][head][v_dim]
     float2 *ml;     // maxima and sums of weights [slot][head]
-    int2 *cut;      // first and last share of each row
+    // Of each row, or where there are more rows than shares, of each share: the
+    // row that begins in it (-1: it also ends there), the first and the last
+    // share of that row.
+    int3 *cut;
+    int32_t by_row;
 };
 
 enum Keep { kAll, kKeys, kNothing };
