@@ -1,6 +1,42 @@
 // attend_kernel.h -- the kernel of the paged attention: one new token per row
 // over a paged key-value cache.  Included by the attend_*.hip files, each of
-// which instantiates the kernels of one compute type.
+// which instantiates the kernels of one query type.
+//
+// Mathematics.  With s_t = scale * (q . k_t) a wave keeps, per query head, the
+// largest score m so far, l = sum exp(s_t - m) and o = sum exp(s_t - m) v_t; a
+// larger m' turns l and o by exp(m - m').  Two such states join the same way, so
+// the tokens can be split over waves, workgroups and launches.  Scores are held
+// in units of log 2, and everything in binary32.
+//
+// What bounds it.  Every key and value is read once from HBM and used for at
+// most 16 query heads: 4 to 16 flop a byte, far below what the matrix units
+// give.  So the design is about keeping the reads in flight:
+// * Both products run on the matrix units with the cache as their first operand,
+//   in the layout in which it is loaded: 16 tokens by 4 chunks of 16 bytes for
+//   the scores.  The scores come out with a query head per lane column, which is
+//   what the second product takes as its second operand, so the weights never
+//   leave their lane; the values are transposed within a lane (two byte permutes
+//   per two words), and nothing of the cache goes through LDS.
+// * A wave's step is 64 tokens where the registers hold them (32 KiB of 128
+//   bfloat16).  The next step's keys are loaded when this one's scores are done,
+//   its values when this one's are used: 16 to 32 KiB in flight a wave, with 4
+//   waves a compute unit (8 where a step is 16 KiB).
+// * A workgroup's waves take different heads of the same tokens.  One head's 256
+//   bytes at the 2 KiB stride of a token-major page fall on 2 of 16 L2 channels:
+//   1 x 131072 bfloat16 took 101 us that way, 90 this way.
+// * Workgroups take even shares of all rows' tokens, found from the lengths on
+//   the device: 64 ragged rows took 281 us in parts of a fixed size, 160 so.
+//
+// Measured (MI355X, GPU time of the call with its join): 1 x 131072 bfloat16, 32
+// heads over 8 of 128: 90 us, 6.0 TB/s; 64 ragged rows of up to 8192: 160 us, 6.3
+// TB/s; 256 x 4096 e4m3: 326 us, 6.6 TB/s; 16 x 16384 float32: 316 us, 6.8 TB/s;
+// one row of 1000: 11.5 us, of which the loads' dependent latencies are 6 and the
+// join's launch 4.
+//
+// Weights are rounded to the cache's 16-bit type for the second product where
+// the output is of 16 bits too: half a step of what the output itself is rounded
+// to (0.0018 relative against the definition, 0.0017 with float32 weights).  A
+// float32 output takes them whole.
 #ifndef DETFOLD_ATTEND_KERNEL_H
 #define DETFOLD_ATTEND_KERNEL_H
 
@@ -228,7 +264,9 @@ template <bool B> struct Last {
     static constexpr bool value = B;
 };
 
-// MOST: tiles of 16 tokens in a step, at most.  KEEP: what the caches keep.
+// What follows from the types C of the cache, QK and PV of the two products, and
+// from the head class D.  TILED: 16 tokens lie within a page.  MOST: tiles of 16
+// tokens in a step, at most.  KEEP: what the caches keep.
 template <typename C, int QK, int PV, int D, bool TILED, int MOST, int KEEP> struct Attend {
     static constexpr int kSize = sizeof(C);
     static constexpr int kChunk = 16 / kSize;         // dims of one 16-byte load of a key
@@ -282,375 +320,375 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
     }
 
     for (;;) {
-    const AttendArgs &p = arguments();
-    const detfold_attend &a = p.a;
-    const detfold_paged_cache &c = p.c;
-    const int lane = anew((int)threadIdx.x & 63), col = lane & 15, grp = lane >> 4;
-    const uint32_t h = divide(unit, p.tiles), tile = unit - h * p.tiles.d;
-    const int head0 = (int)(h * p.group + 16 * tile);
-    const int live = min(16, p.group - 16 * (int)tile);
-    const char *k0 = (const char *)c.k + (int64_t)h * c.k_head * CS, *v0 = (const char *)c.v + (int64_t)h * c.v_head * CS;
-    const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
-    const uint32_t pages = (uint32_t)c.pages;
-    const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f) * kLog2e;
-    const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
-    const bool ragged = c.dim % (4 * E) != 0;
+        const AttendArgs &p = arguments();
+        const detfold_attend &a = p.a;
+        const detfold_paged_cache &c = p.c;
+        const int lane = anew((int)threadIdx.x & 63), col = lane & 15, grp = lane >> 4;
+        const uint32_t h = divide(unit, p.tiles), tile = unit - h * p.tiles.d;
+        const int head0 = (int)(h * p.group + 16 * tile);
+        const int live = min(16, p.group - 16 * (int)tile);
+        const char *k0 = (const char *)c.k + (int64_t)h * c.k_head * CS, *v0 = (const char *)c.v + (int64_t)h * c.v_head * CS;
+        const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
+        const uint32_t pages = (uint32_t)c.pages;
+        const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f) * kLog2e;
+        const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
+        const bool ragged = c.dim % (4 * E) != 0;
 
-    // Where a lane's loads lie within a key and a value.
-    uint32_t k_at[NC], v_at[NP];
+        // Where a lane's loads lie within a key and a value.
+        uint32_t k_at[NC], v_at[NP];
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-        k_at[i] = (uint32_t)min(E * (4 * i + grp), c.dim - E) * CS + (TILED ? col * (uint32_t)k_token : 0);
+        for (int i = 0; i < NC; ++i)
+            k_at[i] = (uint32_t)min(E * (4 * i + grp), c.dim - E) * CS + (TILED ? col * (uint32_t)k_token : 0);
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-        v_at[i] = (uint32_t)min(VW * (16 * i + col), c.v_dim - VW) * CS + (TILED ? 4 * grp * (uint32_t)v_token : 0);
+        for (int i = 0; i < NP; ++i)
+            v_at[i] = (uint32_t)min(VW * (16 * i + col), c.v_dim - VW) * CS + (TILED ? 4 * grp * (uint32_t)v_token : 0);
 
-    const RowTokens row = row_tokens(p, mine.len, TILED);
-    bool bad = row.bad;
-    uint32_t begin = row.begin, end = row.end, done = 0;
-    int64_t slot = -1;  // where the sums of this part go if the row has others
-    if (p.shares.d) {
-        const uint32_t x = mine.at - mine.row_at;
-        done = min(row.units - x, mine.left);
-        if (done < row.units)
-            slot = ((int64_t)y * (p.units.d * beside) + unit) * 2 + (x == 0);
-        if (unit == 0 && lane == 0 && turn == 0 && (p.by_row ? x == 0 : done == mine.left)) {
-            const bool cut = x == 0 && done < row.units;  // it begins here, and does not end here
-            p.cut[p.by_row ? b : y] = make_int3(cut ? (int)b : -1, (int)y, cut ? (int)((mine.at + row.units - 1) / mine.each) : 0);
-        }
-        end = x + done < row.units ? row.a0 + kUnit * (x + done) : end;
-        begin = x ? row.a0 + kUnit * x : begin;
-    } else if (p.parts.d > 1) {
-        slot = (b * p.parts.d + part) * (p.units.d * beside) + unit;
-        const int64_t x = begin + part * p.split;
-        begin = (uint32_t)min(x, (int64_t)end), end = (uint32_t)min(x + p.split, (int64_t)end);
-    }
-    const uint32_t a0 = TILED ? begin & ~15u : begin, last = end > 0 ? end - 1 : 0;
-    const uint32_t steps = end > begin ? (end - a0 + S::kStep - 1) / S::kStep : 0;
-
-    // The queries as the operand of the score products, one lane's 16 bytes
-    // after the other; a chunk that would pass the head's end starts earlier,
-    // and what it repeats counts as zero.
-    char *const queries = lds + in * S::kQ;
-    constexpr int QS = QK == kF32 ? 4 : 2, PER = 16 / QS, NQ = D / (4 * PER);
-    const char *q = (const char *)a.q + (b * a.q_row + (int64_t)(head0 + min(col, live - 1)) * a.q_head) * QS;
-    auto query_chunk = [&](int i) { return E * (4 * (i * PER / E) + grp); };
-    Words<16> qw[NQ] = {};
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-        if ((i & (turns - 1)) == turn)
-            __builtin_memcpy(&qw[i], q + (min(query_chunk(i), c.dim - E) + i * PER % E) * QS, 16);
-
-    const int32_t *table = a.table + b * a.table_row;
-    // The pages of a step's tokens, looked up two steps ahead of the products:
-    // where tiles lie within a page one scalar each, else one per lane and
-    // token, handed to the lanes that load it when it is used.  Tokens past the
-    // part are taken from its last ones, and masked.
-    constexpr int IDS = TILED ? UT : 1;
-    const uint32_t own = lane & (S::kStep - 1);
-    struct Pages {
-        int32_t id[IDS];
-        uint32_t off[IDS];
-    };
-    auto look_up = [&](uint32_t s) {
-        const uint32_t t0 = a0 + s * S::kStep;
-        Pages g;
-#pragma unroll
-        for (int u = 0; u < IDS; ++u) {
-            const uint32_t t = TILED ? min(t0 + 16 * u, last & ~15u) : min(t0 + own, last), n = divide(t, p.page);
-            g.id[u] = TILED ? scalar_load(table + n) : table[n];
-            g.off[u] = t - n * p.page.d;
-        }
-        return g;
-    };
-    auto valid = [&](int32_t id) {  // the page, 0 for one that is none
-        const bool no = (uint32_t)id >= pages;
-        bad |= no;
-        return (int64_t)(no ? 0 : id);
-    };
-
-    Words<16> kw[UT][NC];
-    Words<VW * CS> vw[NT][NP];
-    auto load_keys = [&](const Pages &g) {
-        int64_t at = 0;
-        if (!TILED)
-            at = valid(g.id[0]) * k_page + g.off[0] * k_token;
-#pragma unroll
-        for (int u = 0; u < UT; ++u) {
-            const char *k = k0 + (TILED ? valid(g.id[u % IDS]) * k_page + g.off[u % IDS] * k_token : from_lane(at, 16 * u + col));
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-                kw[u][i] = load_words<16, KEEP == kNothing>(k + anew(k_at[i]));
-        }
-    };
-    auto load_values = [&](const Pages &g) {
-        int64_t at = 0;
-        if (!TILED)
-            at = valid(g.id[0]) * v_page + g.off[0] * v_token;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const char *v = v0 + (TILED ? valid(g.id[j / 4 % IDS]) * v_page + (g.off[j / 4 % IDS] + j % 4) * v_token
-                                        : from_lane(at, 16 * (j / 4) + 4 * grp + j % 4));
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-                vw[j][i] = load_words<VW * CS, KEEP != kAll>(v + anew(v_at[i]));
-        }
-    };
-
-    // Weights of 16-bit floats are held 2^15 times larger, so that small ones
-    // keep their digits; the sum is too, and both are put right at the end.
-    constexpr float kLift = PV == kF16 ? 15.0f : 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    f4 acc[NP][VW];
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int j = 0; j < VW; ++j)
-            acc[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    uint32_t s = turn;
-    Pages now = {}, next = {};
-    if (s < steps)
-        now = look_up(s);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-        if ((i & (turns - 1)) == turn) {
-            const int drop = query_chunk(i) - min(query_chunk(i), c.dim - E) - i * PER % E;
-            u4 w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = col < live ? qw[i].w[j] & keep_from(drop * QS, j) : 0u;
-            *(u4 *)(queries + i * 1024 + lane * 16) = w;
-        }
-    if (D == 256)  // else the queries' registers add to those of the loads below
-        __builtin_amdgcn_sched_barrier(0);
-    if (s < steps) {
-        load_keys(now);
-        load_values(now);
-        now = look_up(min(s + turns, steps - 1));
-    }
-    __syncthreads();
-    // One step; but for the last one it also issues the next one's loads, and
-    // is compiled for that alone: with a branch instead, the wait for the values
-    // would have to take the keys issued after them for values not yet there.
-    auto step = [&](auto last_one) {
-        constexpr bool more = !decltype(last_one)::value;
-        const uint32_t t0 = a0 + s * S::kStep;
-        const uint32_t q_at = anew(lane) * 16;
-        if (CS != 1 && ragged) {  // what a key's last chunk repeats: zero times infinity would be NaN
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int at = E * (4 * i + anew(grp)), drop = at - min(at, c.dim - E);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t keep = keep_from(CS * drop, j);
-#pragma unroll
-                    for (int u = 0; u < UT; ++u)
-                        kw[u][i].w[j] &= keep;
-                }
+        const RowTokens row = row_tokens(p, mine.len, TILED);
+        bool bad = row.bad;
+        uint32_t begin = row.begin, end = row.end, done = 0;
+        int64_t slot = -1;  // where the sums of this part go if the row has others
+        if (p.shares.d) {
+            const uint32_t x = mine.at - mine.row_at;
+            done = min(row.units - x, mine.left);
+            if (done < row.units)
+                slot = ((int64_t)y * (p.units.d * beside) + unit) * 2 + (x == 0);
+            if (unit == 0 && lane == 0 && turn == 0 && (p.by_row ? x == 0 : done == mine.left)) {
+                const bool cut = x == 0 && done < row.units;  // it begins here, and does not end here
+                p.cut[p.by_row ? b : y] = make_int3(cut ? (int)b : -1, (int)y, cut ? (int)((mine.at + row.units - 1) / mine.each) : 0);
             }
+            end = x + done < row.units ? row.a0 + kUnit * (x + done) : end;
+            begin = x ? row.a0 + kUnit * x : begin;
+        } else if (p.parts.d > 1) {
+            slot = (b * p.parts.d + part) * (p.units.d * beside) + unit;
+            const int64_t x = begin + part * p.split;
+            begin = (uint32_t)min(x, (int64_t)end), end = (uint32_t)min(x + p.split, (int64_t)end);
         }
-        // Scores: a row per token, a column per query head.
-        f4 x[UT];
+        const uint32_t a0 = TILED ? begin & ~15u : begin, last = end > 0 ? end - 1 : 0;
+        const uint32_t steps = end > begin ? (end - a0 + S::kStep - 1) / S::kStep : 0;
+
+        // The queries as the operand of the score products, one lane's 16 bytes
+        // after the other; a chunk that would pass the head's end starts earlier,
+        // and what it repeats counts as zero.
+        char *const queries = lds + in * S::kQ;
+        constexpr int QS = QK == kF32 ? 4 : 2, PER = 16 / QS, NQ = D / (4 * PER);
+        const char *q = (const char *)a.q + (b * a.q_row + (int64_t)(head0 + min(col, live - 1)) * a.q_head) * QS;
+        auto query_chunk = [&](int i) { return E * (4 * (i * PER / E) + grp); };
+        Words<16> qw[NQ] = {};
 #pragma unroll
-        for (int u = 0; u < UT; ++u) {
-            x[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < NQ; ++i)
+            if ((i & (turns - 1)) == turn)
+                __builtin_memcpy(&qw[i], q + (min(query_chunk(i), c.dim - E) + i * PER % E) * QS, 16);
+
+        const int32_t *table = a.table + b * a.table_row;
+        // The pages of a step's tokens, looked up two steps ahead of the products:
+        // where tiles lie within a page one scalar each, else one per lane and
+        // token, handed to the lanes that load it when it is used.  Tokens past the
+        // part are taken from its last ones, and masked.
+        constexpr int IDS = TILED ? UT : 1;
+        const uint32_t own = lane & (S::kStep - 1);
+        struct Pages {
+            int32_t id[IDS];
+            uint32_t off[IDS];
+        };
+        auto look_up = [&](uint32_t s) {
+            const uint32_t t0 = a0 + s * S::kStep;
+            Pages g;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                if constexpr (QK == kF32) {
-#pragma unroll
-                    for (int e = 0; e < E; e += 4) {
-                        const f4 q = *(const f4 *)(queries + (i * (E / 4) + e / 4) * 1024 + q_at);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            x[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(kw[u][i].w, e + j), q[j], x[u], 0, 0, 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; e += 8) {
-                        const u4 q = *(const u4 *)(queries + (i * (E / 8) + e / 8) * 1024 + q_at);
-                        const u4 k = {pair16<C, QK>(kw[u][i].w, e / 2), pair16<C, QK>(kw[u][i].w, e / 2 + 1),
-                                      pair16<C, QK>(kw[u][i].w, e / 2 + 2), pair16<C, QK>(kw[u][i].w, e / 2 + 3)};
-                        x[u] = mfma16<QK>(k, q, x[u]);
-                    }
-                }
+            for (int u = 0; u < IDS; ++u) {
+                const uint32_t t = TILED ? min(t0 + 16 * u, last & ~15u) : min(t0 + own, last), n = divide(t, p.page);
+                g.id[u] = TILED ? scalar_load(table + n) : table[n];
+                g.off[u] = t - n * p.page.d;
             }
-        }
-        if constexpr (more) {
-            next = look_up(min(s + 2 * turns, steps - 1));
-            load_keys(now);
-        }
-        // Weights, relative to the largest score so far.
-        float top = -INFINITY;
-        const bool edge = t0 < begin || t0 + S::kStep > end;
-        if (edge) {  // tokens of other parts, or none: their scores take no weight, and their values may be anything
+            return g;
+        };
+        auto valid = [&](int32_t id) {  // the page, 0 for one that is none
+            const bool no = (uint32_t)id >= pages;
+            bad |= no;
+            return (int64_t)(no ? 0 : id);
+        };
+
+        Words<16> kw[UT][NC];
+        Words<VW * CS> vw[NT][NP];
+        auto load_keys = [&](const Pages &g) {
+            int64_t at = 0;
+            if (!TILED)
+                at = valid(g.id[0]) * k_page + g.off[0] * k_token;
+#pragma unroll
+            for (int u = 0; u < UT; ++u) {
+                const char *k = k0 + (TILED ? valid(g.id[u % IDS]) * k_page + g.off[u % IDS] * k_token : from_lane(at, 16 * u + col));
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    kw[u][i] = load_words<16, KEEP == kNothing>(k + anew(k_at[i]));
+            }
+        };
+        auto load_values = [&](const Pages &g) {
+            int64_t at = 0;
+            if (!TILED)
+                at = valid(g.id[0]) * v_page + g.off[0] * v_token;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const uint32_t t = t0 + 16 * (j / 4) + 4 * grp + j % 4;
-                const bool out = t < begin || t >= end;
-                x[j / 4][j % 4] = out ? -INFINITY : x[j / 4][j % 4] * by;
+                const char *v = v0 + (TILED ? valid(g.id[j / 4 % IDS]) * v_page + (g.off[j / 4 % IDS] + j % 4) * v_token
+                                            : from_lane(at, 16 * (j / 4) + 4 * grp + j % 4));
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int n = 0; n < VW * CS / 4; ++n)
-                        vw[j][i].w[n] = out ? 0u : vw[j][i].w[n];
+                    vw[j][i] = load_words<VW * CS, KEEP != kAll>(v + anew(v_at[i]));
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                x[j / 4][j % 4] *= by;
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            top = fmaxf(top, x[j / 4][j % 4]);
-        top = fmaxf(m, over_groups(top, [](float y, float z) { return fmaxf(y, z); }));
-        const float base = top == -INFINITY ? 0.0f : top;
-        if (__any(top > m)) {
-            const float turn = __builtin_amdgcn_exp2f(m - base);
-            l *= turn;
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-#pragma unroll
-                for (int j = 0; j < VW; ++j)
-                    acc[i][j] *= turn;
-            m = top;
-        }
-#pragma unroll
-        for (int u = 0; u < UT; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[u][j] = __builtin_amdgcn_exp2f((x[u][j] - base) + kLift);
-                l += x[u][j];
-            }
-        // Values: the output's rows are its dims, its columns the query heads.
-        if constexpr (PV == kF32) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int n = 0; n < VW; ++n)
-                        acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(vw[j][i].w, n), x[j / 4][j % 4], acc[i][n], 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < UT; u += 2) {
-                constexpr int TERMS = PV == kSplit ? 3 : 1;
-                u4 w[TERMS];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float y = x[u + j / 2][2 * (j % 2)], z = x[u + j / 2][2 * (j % 2) + 1];
-                    if constexpr (PV == kF16) {
-                        w[0][j] = __builtin_bit_cast(uint32_t, f16x2{(f16)y, (f16)z});
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < TERMS; ++n) {
-                            const bf16x2 part = {(bf16)y, (bf16)z};
-                            w[n][j] = __builtin_bit_cast(uint32_t, part);
-                            y -= (float)part.x, z -= (float)part.y;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int n = 0; n < VW; n += 2) {
-                        u4 lo, hi;  // dims n and n + 1 of the lane's eight tokens
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t y = pair16<C, PV>(vw[4 * u + 2 * j][i].w, n / 2), z = pair16<C, PV>(vw[4 * u + 2 * j + 1][i].w, n / 2);
-                            lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
-                            hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
-                        }
-#pragma unroll
-                        for (int e = 0; e < TERMS; ++e) {
-                            acc[i][n] = mfma16<PV>(lo, w[e], acc[i][n]);
-                            acc[i][n + 1] = mfma16<PV>(hi, w[e], acc[i][n + 1]);
-                        }
-                    }
-            }
-        }
-        if constexpr (more) {
-            load_values(now);
-            now = next;
-        }
-    };
-    for (; s + turns < steps; s += turns)
-        step(Last<false>{});
-    if (s < steps)
-        step(Last<true>{});
+        };
 
-    l = over_groups(l, [](float y, float z) { return y + z; });
-    if (PV == kF16) {
-        l *= 0x1p-15f;
+        // Weights of 16-bit floats are held 2^15 times larger, so that small ones
+        // keep their digits; the sum is too, and both are put right at the end.
+        constexpr float kLift = PV == kF16 ? 15.0f : 0.0f;
+        float m = -INFINITY, l = 0.0f;
+        f4 acc[NP][VW];
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
             for (int j = 0; j < VW; ++j)
-                acc[i][j] *= 0x1p-15f;
-    }
-    if (__any(bad))
-        l = __builtin_nanf("");
+                acc[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // The waves' states, joined in order: each leaves its heads' sums in LDS,
-    // over the queries, and a thread takes four dims of a head from every turn.
-    const int heads = min(16, p.group);
-    f2 *const state = (f2 *)lds;
-    float *const sums = (float *)(lds + waves * 16 * sizeof(f2));
-    __syncthreads();
-    if (col < live) {
-        float *mine = sums + (wave * heads + col) * S::kRow;
+        uint32_t s = turn;
+        Pages now = {}, next = {};
+        if (s < steps)
+            now = look_up(s);
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
+        for (int i = 0; i < NQ; ++i)
+            if ((i & (turns - 1)) == turn) {
+                const int drop = query_chunk(i) - min(query_chunk(i), c.dim - E) - i * PER % E;
+                u4 w;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int n = 0; n < VW; n += 4)
-                    *(f4 *)(mine + VW * (16 * i + 4 * grp + j) + n) = f4{acc[i][n][j], acc[i][n + 1][j], acc[i][n + 2][j], acc[i][n + 3][j]};
-        if (grp == 0)
-            state[wave * 16 + col] = f2{m, l};
-    }
-    __syncthreads();
-    const AttendArgs &pe = arguments();
-    for (int i = 64 * turn + lane; i < live * (D / 4); i += 64 * turns) {
-        const AttendArgs &p = pe;
-        const detfold_attend &a = p.a;
-        const int head = i / (D / 4), at = i % (D / 4) * 4, at0 = at / VW * VW;
-        if (at0 >= p.c.v_dim)
-            continue;
-        float top = -INFINITY;
-        for (int w = in; w < waves; w += beside)
-            top = fmaxf(top, state[w * 16 + head].x);
-        const float base = top == -INFINITY ? 0.0f : top;
-        f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-        float total = 0.0f;
-        for (int w = in; w < waves; w += beside) {
-            const f2 ml = state[w * 16 + head];
-            const float by = __builtin_amdgcn_exp2f(ml.x - base);
-            total += ml.y * by;
-            sum += *(const f4 *)(sums + (w * heads + head) * S::kRow + at) * by;
+                for (int j = 0; j < 4; ++j)
+                    w[j] = col < live ? qw[i].w[j] & keep_from(drop * QS, j) : 0u;
+                *(u4 *)(queries + i * 1024 + lane * 16) = w;
+            }
+        if (D == 256)  // else the queries' registers add to those of the loads below
+            __builtin_amdgcn_sched_barrier(0);
+        if (s < steps) {
+            load_keys(now);
+            load_values(now);
+            now = look_up(min(s + turns, steps - 1));
         }
-        const int64_t g = b * a.q_heads + head0 + head, from = slot * heads + head;
-        const int d = min(at0, p.c.v_dim - VW) + at - at0;
-        if (slot >= 0) {
-            __builtin_memcpy(p.acc + from * p.c.v_dim + d, &sum, sizeof(sum));
-            if (at == 0)
-                p.ml[from] = make_float2(top, total);
-        } else {
-            const float by = out_scale(v_scale, total);
-            const float o[4] = {sum.x * by, sum.y * by, sum.z * by, sum.w * by};
-            put_out<4>(a, b * a.out_row + (int64_t)(head0 + head) * a.out_head + d, o);
-            if (a.lse && at == 0)
-                a.lse[g] = log_sum(top, total);
+        __syncthreads();
+        // One step; but for the last one it also issues the next one's loads, and
+        // is compiled for that alone: with a branch instead, the wait for the values
+        // would have to take the keys issued after them for values not yet there.
+        auto step = [&](auto last_one) {
+            constexpr bool more = !decltype(last_one)::value;
+            const uint32_t t0 = a0 + s * S::kStep;
+            const uint32_t q_at = anew(lane) * 16;
+            if (CS != 1 && ragged) {  // what a key's last chunk repeats: zero times infinity would be NaN
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const int at = E * (4 * i + anew(grp)), drop = at - min(at, c.dim - E);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t keep = keep_from(CS * drop, j);
+#pragma unroll
+                        for (int u = 0; u < UT; ++u)
+                            kw[u][i].w[j] &= keep;
+                    }
+                }
+            }
+            // Scores: a row per token, a column per query head.
+            f4 x[UT];
+#pragma unroll
+            for (int u = 0; u < UT; ++u) {
+                x[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    if constexpr (QK == kF32) {
+#pragma unroll
+                        for (int e = 0; e < E; e += 4) {
+                            const f4 q = *(const f4 *)(queries + (i * (E / 4) + e / 4) * 1024 + q_at);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(kw[u][i].w, e + j), q[j], x[u], 0, 0, 0);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; e += 8) {
+                            const u4 q = *(const u4 *)(queries + (i * (E / 8) + e / 8) * 1024 + q_at);
+                            const u4 k = {pair16<C, QK>(kw[u][i].w, e / 2), pair16<C, QK>(kw[u][i].w, e / 2 + 1),
+                                          pair16<C, QK>(kw[u][i].w, e / 2 + 2), pair16<C, QK>(kw[u][i].w, e / 2 + 3)};
+                            x[u] = mfma16<QK>(k, q, x[u]);
+                        }
+                    }
+                }
+            }
+            if constexpr (more) {
+                next = look_up(min(s + 2 * turns, steps - 1));
+                load_keys(now);
+            }
+            // Weights, relative to the largest score so far.
+            float top = -INFINITY;
+            const bool edge = t0 < begin || t0 + S::kStep > end;
+            if (edge) {  // tokens of other parts, or none: their scores take no weight, and their values may be anything
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint32_t t = t0 + 16 * (j / 4) + 4 * grp + j % 4;
+                    const bool out = t < begin || t >= end;
+                    x[j / 4][j % 4] = out ? -INFINITY : x[j / 4][j % 4] * by;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int n = 0; n < VW * CS / 4; ++n)
+                            vw[j][i].w[n] = out ? 0u : vw[j][i].w[n];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    x[j / 4][j % 4] *= by;
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                top = fmaxf(top, x[j / 4][j % 4]);
+            top = fmaxf(m, over_groups(top, [](float y, float z) { return fmaxf(y, z); }));
+            const float base = top == -INFINITY ? 0.0f : top;
+            if (__any(top > m)) {
+                const float turn = __builtin_amdgcn_exp2f(m - base);
+                l *= turn;
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int j = 0; j < VW; ++j)
+                        acc[i][j] *= turn;
+                m = top;
+            }
+#pragma unroll
+            for (int u = 0; u < UT; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[u][j] = __builtin_amdgcn_exp2f((x[u][j] - base) + kLift);
+                    l += x[u][j];
+                }
+            // Values: the output's rows are its dims, its columns the query heads.
+            if constexpr (PV == kF32) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int n = 0; n < VW; ++n)
+                            acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(vw[j][i].w, n), x[j / 4][j % 4], acc[i][n], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < UT; u += 2) {
+                    constexpr int TERMS = PV == kSplit ? 3 : 1;
+                    u4 w[TERMS];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float y = x[u + j / 2][2 * (j % 2)], z = x[u + j / 2][2 * (j % 2) + 1];
+                        if constexpr (PV == kF16) {
+                            w[0][j] = __builtin_bit_cast(uint32_t, f16x2{(f16)y, (f16)z});
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < TERMS; ++n) {
+                                const bf16x2 part = {(bf16)y, (bf16)z};
+                                w[n][j] = __builtin_bit_cast(uint32_t, part);
+                                y -= (float)part.x, z -= (float)part.y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int n = 0; n < VW; n += 2) {
+                            u4 lo, hi;  // dims n and n + 1 of the lane's eight tokens
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t y = pair16<C, PV>(vw[4 * u + 2 * j][i].w, n / 2), z = pair16<C, PV>(vw[4 * u + 2 * j + 1][i].w, n / 2);
+                                lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
+                                hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
+                            }
+#pragma unroll
+                            for (int e = 0; e < TERMS; ++e) {
+                                acc[i][n] = mfma16<PV>(lo, w[e], acc[i][n]);
+                                acc[i][n + 1] = mfma16<PV>(hi, w[e], acc[i][n + 1]);
+                            }
+                        }
+                }
+            }
+            if constexpr (more) {
+                load_values(now);
+                now = next;
+            }
+        };
+        for (; s + turns < steps; s += turns)
+            step(Last<false>{});
+        if (s < steps)
+            step(Last<true>{});
+
+        l = over_groups(l, [](float y, float z) { return y + z; });
+        if (PV == kF16) {
+            l *= 0x1p-15f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int j = 0; j < VW; ++j)
+                    acc[i][j] *= 0x1p-15f;
         }
-    }
-    mine.left -= done;
-    if (mine.left == 0)
-        return;
-    mine.at = mine.row_at = mine.at + done;
-    ++b;
-    mine.len = scalar_load(arguments().a.lens + b);
-    __syncthreads();
+        if (__any(bad))
+            l = __builtin_nanf("");
+
+        // The waves' states, joined in order: each leaves its heads' sums in LDS,
+        // over the queries, and a thread takes four dims of a head from every turn.
+        const int heads = min(16, p.group);
+        f2 *const state = (f2 *)lds;
+        float *const sums = (float *)(lds + waves * 16 * sizeof(f2));
+        __syncthreads();
+        if (col < live) {
+            float *mine = sums + (wave * heads + col) * S::kRow;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int n = 0; n < VW; n += 4)
+                        *(f4 *)(mine + VW * (16 * i + 4 * grp + j) + n) = f4{acc[i][n][j], acc[i][n + 1][j], acc[i][n + 2][j], acc[i][n + 3][j]};
+            if (grp == 0)
+                state[wave * 16 + col] = f2{m, l};
+        }
+        __syncthreads();
+        const AttendArgs &pe = arguments();
+        for (int i = 64 * turn + lane; i < live * (D / 4); i += 64 * turns) {
+            const AttendArgs &p = pe;
+            const detfold_attend &a = p.a;
+            const int head = i / (D / 4), at = i % (D / 4) * 4, at0 = at / VW * VW;
+            if (at0 >= p.c.v_dim)
+                continue;
+            float top = -INFINITY;
+            for (int w = in; w < waves; w += beside)
+                top = fmaxf(top, state[w * 16 + head].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+            f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+            float total = 0.0f;
+            for (int w = in; w < waves; w += beside) {
+                const f2 ml = state[w * 16 + head];
+                const float by = __builtin_amdgcn_exp2f(ml.x - base);
+                total += ml.y * by;
+                sum += *(const f4 *)(sums + (w * heads + head) * S::kRow + at) * by;
+            }
+            const int64_t g = b * a.q_heads + head0 + head, from = slot * heads + head;
+            const int d = min(at0, p.c.v_dim - VW) + at - at0;
+            if (slot >= 0) {
+                __builtin_memcpy(p.acc + from * p.c.v_dim + d, &sum, sizeof(sum));
+                if (at == 0)
+                    p.ml[from] = make_float2(top, total);
+            } else {
+                const float by = out_scale(v_scale, total);
+                const float o[4] = {sum.x * by, sum.y * by, sum.z * by, sum.w * by};
+                put_out<4>(a, b * a.out_row + (int64_t)(head0 + head) * a.out_head + d, o);
+                if (a.lse && at == 0)
+                    a.lse[g] = log_sum(top, total);
+            }
+        }
+        mine.left -= done;
+        if (mine.left == 0)
+            return;
+        mine.at = mine.row_at = mine.at + done;
+        ++b;
+        mine.len = scalar_load(arguments().a.lens + b);
+        __syncthreads();
     }
 }
 
