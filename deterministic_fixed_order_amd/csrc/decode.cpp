@@ -16,7 +16,7 @@ constexpr int64_t kMaxCount = (int64_t)1 << 31;   // counts that the kernels hol
 constexpr int64_t kMaxElems = (int64_t)1 << 46;   // extent of one buffer, in elements
 constexpr int32_t kMaxHeads = 1 << 16;
 constexpr int64_t kWavesPerCu = 8;                // of the attention, resident
-constexpr int64_t kShort = 256;                   // tokens that one workgroup takes by itself
+constexpr int64_t kShortRow = 512;                // tokens that are not worth cutting where rows fill the device
 // Of the cache, read in a step of 64 tokens: with less, or with products in
 // float32 from narrower values, a compute unit takes 8 waves instead of 4 (heads
 // of 64 bfloat16 27.7 us instead of 28.3; bfloat16 to float32 194 instead of 230).
@@ -175,10 +175,15 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
     p->beside = units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
     p->brief = seen <= 32;
     const int64_t groups = units / p->beside;
+    // Three steps of a wave take less than a join (1 token 6.6 us, each step of 64
+    // bfloat16 tokens 1.2 more, one of 1000 in parts 11.5).
+    const int head = c.dim > c.v_dim ? c.dim : c.v_dim, wide_head = head <= 64 ? 64 : head <= 128 ? 128 : 256;
+    const int tiles_fit = 1024 / (wide_head * elem_size(c.type)), tiles_most = wide_head == 256 ? 2 : 4;
+    const int64_t few = 3 * 16 * (tiles_fit < tiles_most ? tiles_fit : tiles_most) * (4 / p->beside);
     int64_t part = split > 0 ? split : kLongPart;
     if (split == 0) {
-        if (seen <= kShort) {
-            part = kShort;
+        if (seen <= few || (batch * groups >= full && seen <= kShortRow)) {
+            part = seen;
         } else if (batch > 0 && batch * ((seen + 31) / 32) <= waves / units) {
             // One step for every wave that the device holds is enough: the
             // least steps, and no more waves to a workgroup than heads.
@@ -192,7 +197,7 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
         } else if (batch > 0 && seen > kMaxBlocks / p->units * part) {
             part = (seen - 1) / (kMaxBlocks / p->units + 1) + 1;
         }
-        part = (part + DETFOLD_ATTEND_STEP - 1) / DETFOLD_ATTEND_STEP * DETFOLD_ATTEND_STEP;
+        part = (part + DETFOLD_ATTEND_STEP - 1) / DETFOLD_ATTEND_STEP * DETFOLD_ATTEND_STEP + (part == 0) * DETFOLD_ATTEND_STEP;
     }
     p->splits = seen > part ? (seen + part - 1) / part : 1;
     p->split = p->splits > 1 ? part : seen;
@@ -210,7 +215,7 @@ int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, in
     upto = upto > shared ? upto : shared;
     p->slots = p->shares ? 2 * p->shares * units : p->splits > 1 ? p->units * p->splits : 0;
     p->workspace_bytes = batch > 0 ? p->slots * each + p->shares * 12 : 0;
-    p->workspace_upto = batch > 0 && max_len > (split > 0 ? split : kShort) ? upto * each + full * 12 : 0;
+    p->workspace_upto = batch > 0 && max_len > (split > 0 ? split : few) ? upto * each + full * 12 : 0;
     return DETFOLD_OK;
 }
 
