@@ -9,7 +9,7 @@ namespace detfold_impl {
 AttendKernel attend_f32(const AttendArgs &a)
 {
     if (a.c.type == DETFOLD_E4M3)
-        return pick_attend<e4m3, kF32, kSplit>(a);
+        return pick_attend<e4m3, kSplit, kSplit>(a);
     return a.c.type == DETFOLD_BF16 ? pick_attend<bf16, kF32, kF32>(a) : pick_attend<float, kF32, kF32>(a);
 }
 

@@ -44,10 +44,10 @@
 
 namespace detfold_impl {
 
-// What the matrix units multiply.  kSplit: float32 weights as the sum of three
-// bfloat16 ones (24 bits in all, so exact), with values of e4m3; three products of
-// those take 3/8 of the time of one in float32.  Only where no value is infinite:
-// a weight's third part may be zero.
+// What the matrix units multiply.  kSplit: float32 queries or weights as the sum
+// of three bfloat16 ones (24 bits in all, so exact), with keys or values of e4m3;
+// three products of those take 3/8 of the time of one in float32.  Only where no
+// key or value is infinite: a third part may be zero.
 enum Math { kBf16, kF16, kF32, kSplit };
 
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -115,6 +115,14 @@ template <int M> __device__ __forceinline__ f4 mfma16(u4 a, u4 b, f4 c)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// What a float32's upper half, a bfloat16, leaves of it: exact, and zero for an
+// infinity, whose upper half is all of it.
+__device__ __forceinline__ uint32_t below(uint32_t x)
+{
+    const float up = __builtin_bit_cast(float, x & 0xffff0000u), rest = __builtin_bit_cast(float, x) - up;
+    return up - up == 0.0f ? __builtin_bit_cast(uint32_t, rest) : 0u;
 }
 
 // Over the four groups of 16 lanes, the same on all of them.
@@ -280,7 +288,7 @@ template <typename C, int QK, int PV, int D, bool TILED, int MOST, int KEEP> str
     static constexpr int kWide = kChunk < D / 16 ? kChunk : D / 16;  // dims of a value that a lane loads together
     static constexpr int kParts = D / (16 * kWide);
     static constexpr int kTokens = 4 * kTiles;        // tokens whose values a lane loads
-    static constexpr int kQ = (QK == kF32 ? 4 : 2) * D * 16;  // LDS bytes of the queries
+    static constexpr int kQ = (QK == kF32 ? 4 : QK == kSplit ? 6 : 2) * D * 16;  // LDS bytes of the queries
     static constexpr int kRow = D + 4;                // floats of a query head's sums in LDS: heads on other banks
 
     static_assert(kTiles % 2 == 0 || PV == kF32, "the 16-bit products take 32 tokens");
@@ -370,14 +378,14 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         // after the other; a chunk that would pass the head's end starts earlier,
         // and what it repeats counts as zero.
         char *const queries = lds + in * S::kQ;
-        constexpr int QS = QK == kF32 ? 4 : 2, PER = 16 / QS, NQ = D / (4 * PER);
+        constexpr int QS = QK == kF32 || QK == kSplit ? 4 : 2, PER = QK == kF32 ? 4 : 8, NQ = D / (4 * PER);
         const char *q = (const char *)a.q + (b * a.q_row + (int64_t)(head0 + min(col, live - 1)) * a.q_head) * QS;
         auto query_chunk = [&](int i) { return E * (4 * (i * PER / E) + grp); };
-        Words<16> qw[NQ] = {};
+        Words<PER * QS> qw[NQ] = {};
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
             if ((i & (turns - 1)) == turn)
-                __builtin_memcpy(&qw[i], q + (min(query_chunk(i), c.dim - E) + i * PER % E) * QS, 16);
+                __builtin_memcpy(&qw[i], q + (min(query_chunk(i), c.dim - E) + i * PER % E) * QS, PER * QS);
 
         const int32_t *table = a.table + b * a.table_row;
         // The pages of a step's tokens, looked up two steps ahead of the products:
@@ -454,11 +462,23 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         for (int i = 0; i < NQ; ++i)
             if ((i & (turns - 1)) == turn) {
                 const int drop = query_chunk(i) - min(query_chunk(i), c.dim - E) - i * PER % E;
-                u4 w;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = col < live ? qw[i].w[j] & keep_from(drop * QS, j) : 0u;
-                *(u4 *)(queries + i * 1024 + lane * 16) = w;
+                for (int j = 0; j < PER * QS / 4; ++j)
+                    qw[i].w[j] = col < live ? qw[i].w[j] & keep_from(drop * QS, j) : 0u;
+                if constexpr (QK == kSplit) {
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {  // the highest bits, of which two values' are stored together
+                        u4 w;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            w[j] = __builtin_amdgcn_perm(qw[i].w[2 * j + 1], qw[i].w[2 * j], 0x07060302u);
+                            qw[i].w[2 * j] = below(qw[i].w[2 * j]), qw[i].w[2 * j + 1] = below(qw[i].w[2 * j + 1]);
+                        }
+                        *(u4 *)(queries + (part * NQ + i) * 1024 + lane * 16) = w;
+                    }
+                } else {
+                    *(u4 *)(queries + i * 1024 + lane * 16) = u4{qw[i].w[0], qw[i].w[1], qw[i].w[2], qw[i].w[3]};
+                }
             }
         if (D == 256)  // else the queries' registers add to those of the loads below
             __builtin_amdgcn_sched_barrier(0);
@@ -506,10 +526,13 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
                     } else {
 #pragma unroll
                         for (int e = 0; e < E; e += 8) {
-                            const u4 q = *(const u4 *)(queries + (i * (E / 8) + e / 8) * 1024 + q_at);
                             const u4 k = {pair16<C, QK>(kw[u][i].w, e / 2), pair16<C, QK>(kw[u][i].w, e / 2 + 1),
                                           pair16<C, QK>(kw[u][i].w, e / 2 + 2), pair16<C, QK>(kw[u][i].w, e / 2 + 3)};
-                            x[u] = mfma16<QK>(k, q, x[u]);
+#pragma unroll
+                            for (int part = 0; part < (QK == kSplit ? 3 : 1); ++part) {
+                                const u4 q = *(const u4 *)(queries + (part * NQ + i * (E / 8) + e / 8) * 1024 + q_at);
+                                x[u] = mfma16<QK>(k, q, x[u]);
+                            }
                         }
                     }
                 }

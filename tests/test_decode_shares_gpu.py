@@ -124,3 +124,29 @@ def test_lengths_change_between_replays(env):  # noqa: F811
         want, wl = torch.empty_like(q), torch.empty_like(lse)
         df.attend_paged(want, q, c, table, lens.clone(), max_len=3000, lse=wl)
         assert torch.equal(o, want) and torch.equal(l, wl), step
+
+
+@pytest.mark.parametrize("dtype,cache", PAIRS)
+@pytest.mark.parametrize("n", [40, 700])
+def test_queries_of_infinity_and_of_the_largest_values(env, dtype, cache, n):  # noqa: F811
+    """A score of -infinity everywhere leaves zeros; scores of the type's largest
+    values are finite, and alike here."""
+    df, torch, dev = env
+    gen = _gen(torch, 21, n)
+    (_, v), views = _cache(torch, gen, dev, cache, -(-n // 16), 16, 1, 32, 32)
+    k = torch.zeros(views[0].shape, device=dev)
+    k[..., 0] = 0.5
+    c = df.PagedCache(k.to(views[0].dtype), views[1])
+    big = torch.finfo(getattr(torch, {"f32": "float32", "bf16": "bfloat16", "f16": "float16"}[dtype])).max
+    q = torch.zeros((2, 1, 32), device=dev, dtype=views[0].dtype if dtype == cache else getattr(torch, {"f32": "float32", "bf16": "bfloat16", "f16": "float16"}[dtype]))
+    q[0, 0, 0], q[1, 0, 0] = -math.inf, big
+    table = torch.arange(-(-n // 16), dtype=torch.int32, device=dev).repeat(2, 1)
+    lens = torch.tensor([n, n], dtype=torch.int32, device=dev)
+    out, lse = torch.empty_like(q), torch.empty((2, 1), device=dev)
+    df.attend_paged(out, q, c, table, lens, lse=lse, scale=0.25)
+    assert bool((out[0] == 0).all()) and float(lse[0]) == -math.inf
+    # Equal weights of 1: exact but for the sum of n values, the division and the output's rounding.
+    seen = v.double().flatten(0, 1)[:n, 0]
+    tol = (2 * n * 2.0 ** -24 + 2.0 ** -21) * seen.abs().mean(0) + torch.finfo(q.dtype).eps / 2 * seen.mean(0).abs() + 2.0 ** -24
+    assert bool(((out[1, 0].double().cpu() - seen.mean(0)).abs() <= tol).all())
+    assert abs(float(lse[1]) / (0.25 * 0.5 * big) - 1) < 1e-3
