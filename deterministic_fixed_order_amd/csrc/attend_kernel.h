@@ -340,7 +340,6 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         const uint32_t pages = (uint32_t)c.pages;
         const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f) * kLog2e;
         const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
-        const bool ragged = c.dim % (4 * E) != 0;
 
         // Where a lane's loads lie within a key and a value.
         uint32_t k_at[NC], v_at[NP];
@@ -495,9 +494,19 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
             constexpr bool more = !decltype(last_one)::value;
             const uint32_t t0 = a0 + s * S::kStep;
             const uint32_t q_at = anew(lane) * 16;
-            if (CS != 1 && ragged) {  // what a key's last chunk repeats: zero times infinity would be NaN
+            // Scores: a row per token, a column per query head.
+            f4 x[UT];
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
+            for (int u = 0; u < UT; ++u)
+                x[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                // Chunks past the head's end are not multiplied, and what the one at
+                // its end repeats is cleared: there the queries are zero, but zero times
+                // an infinite key would be NaN (an e4m3 key is never infinite).
+                if (4 * E * i >= c.dim)
+                    break;
+                if (CS != 1 && 4 * E * (i + 1) > c.dim) {
                     const int at = E * (4 * i + anew(grp)), drop = at - min(at, c.dim - E);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -507,14 +516,8 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
                             kw[u][i].w[j] &= keep;
                     }
                 }
-            }
-            // Scores: a row per token, a column per query head.
-            f4 x[UT];
 #pragma unroll
-            for (int u = 0; u < UT; ++u) {
-                x[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < NC; ++i) {
+                for (int u = 0; u < UT; ++u) {
                     if constexpr (QK == kF32) {
 #pragma unroll
                         for (int e = 0; e < E; e += 4) {
