@@ -258,10 +258,20 @@ def cache_append(cache: PagedCache, k, v, slots, *, q=None, q_out=None, position
     _check(_load().detfold_cache_append(cache._c, args, _stream(k, stream)), "cache_append")
 
 
+def _within(stream, dev: int):
+    """The context in which torch allocates for `stream` (None: the current one)."""
+    import torch
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream.cuda_stream), device=dev))
+
+
 def attend_workspace(cache: PagedCache, batch: int, q_heads: int, max_len: int, *, split: int = 0):
     """The device memory that ``attend_paged`` joins the parts of long rows in,
     for calls whose batch and ``max_len`` are at most these (a uint8 tensor).
-    Calls that overlap in time must not share one."""
+    Calls that overlap in time must not share one.  It is allocated on torch's
+    current stream: for calls on another one, make it within that
+    (``torch.cuda.stream``), or keep it until they are done."""
     import torch
     n = ctypes.c_int64()
     _check(_load().detfold_attend_workspace(cache._c, batch, q_heads, max_len, split, ctypes.byref(n)),
@@ -309,7 +319,10 @@ def attend_paged(out, q, cache: PagedCache, table, lens, *, scale=None, window: 
     if max_len is None:
         max_len = min(width * cache.page, 2 ** 31 - 1)
     if workspace is None:
-        workspace = attend_workspace(cache, batch, q_heads, max_len, split=split)
+        # In the pool of the stream that uses it: what this call frees on return
+        # goes to no other stream before the parts are joined.
+        with _within(stream, dev):
+            workspace = attend_workspace(cache, batch, q_heads, max_len, split=split)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     args = _ATTEND.pack(out.data_ptr(), q.data_ptr(), lse_p, table.data_ptr(), lens_p, workspace.data_ptr(),
