@@ -5,8 +5,9 @@
 //
 // Only what it can take as it is: anything else (a wrong type, shape, device
 // or layout, a missing argument) returns -1, and decode.py, whose checks are
-// the same, says what is wrong.  The library's functions come as addresses, so
-// this links to neither the library nor HIP.
+// the same, says what is wrong.  So does whatever torch throws here (a tensor
+// within a function transform has no address to give).  The library's functions
+// come as addresses, so this links to neither the library nor HIP.
 
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -84,6 +85,16 @@ bool cache_of(PyObject *o, detfold_paged_cache *c)
     return true;
 }
 
+// The library's call, without the interpreter's lock (which the arguments,
+// evaluated before, still hold: what throws there needs it).
+template <typename F, typename... A> int unlocked(F f, A... args)
+{
+    PyThreadState *const state = PyEval_SaveThread();
+    const int rc = f(args...);
+    PyEval_RestoreThread(state);
+    return rc;
+}
+
 PyObject *not_taken() { return PyLong_FromLong(-1); }
 
 typedef int (*AppendFn)(const detfold_paged_cache *, const detfold_append *, void *);
@@ -136,11 +147,7 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
     a.pairs = args[12] == Py_True ? 1 : 0;
     if (args[12] != Py_True && args[12] != Py_False)
         return not_taken();
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = f(&c, &a, stream);
-    Py_END_ALLOW_THREADS
-    return PyLong_FromLong(rc);
+    return PyLong_FromLong(unlocked(f, &c, &a, stream));
 }
 
 // (function, cache, device, stream, out, q, table, lens, scale, window, max_len, lse, workspace, split)
@@ -182,11 +189,7 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n)
     a.lens = lens.at<int32_t>();
     a.workspace = workspace.data(), a.workspace_bytes = (int64_t)workspace.t->nbytes();
     a.batch = batch, a.q_heads = (int32_t)q_heads, a.split = (int32_t)split;
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = f(&c, &a, stream);
-    Py_END_ALLOW_THREADS
-    return PyLong_FromLong(rc);
+    return PyLong_FromLong(unlocked(f, &c, &a, stream));
 }
 
 // (function, device, stream, out, outs, lses, lse)
@@ -216,18 +219,27 @@ PyObject *fold(PyObject *, PyObject *const *args, Py_ssize_t n)
         step *= shape[d], lse_step *= shape[d], rows *= shape[d];
     }
     const int64_t W = shape[0], dim = shape.back();
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = f(out.data(), outs.data(), lses.at<float>(), lse.at<float>(), type, (int32_t)W, rows, dim, W > 1 ? o.stride(0) : rows * dim,
-           W > 1 ? lses.t->stride(0) : rows, stream);
-    Py_END_ALLOW_THREADS
-    return PyLong_FromLong(rc);
+    return PyLong_FromLong(unlocked(f, out.data(), outs.data(), lses.at<float>(), lse.at<float>(), type, (int32_t)W, rows, dim,
+                                    W > 1 ? o.stride(0) : rows * dim, W > 1 ? lses.t->stride(0) : rows, stream));
+}
+
+// A call that lets no C++ exception into the interpreter, which would end the
+// process.  The library's functions are C and throw none, so nothing was done yet.
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    try {
+        return F(self, args, n);
+    } catch (...) {
+        PyErr_Clear();
+        return not_taken();
+    }
 }
 
 PyMethodDef methods[] = {
-    {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
-    {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, nullptr},
-    {"fold", (PyCFunction)(void (*)(void))fold, METH_FASTCALL, nullptr},
+    {"append", (PyCFunction)(void (*)(void))guarded<append>, METH_FASTCALL, nullptr},
+    {"attend", (PyCFunction)(void (*)(void))guarded<attend>, METH_FASTCALL, nullptr},
+    {"fold", (PyCFunction)(void (*)(void))guarded<fold>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
