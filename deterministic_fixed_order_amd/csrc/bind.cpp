@@ -46,8 +46,9 @@ struct Arg {
         return t && t->layout() == c10::kStrided && t->get_device() == dev && t->scalar_type() == type && t->sizes() == shape &&
                t->is_contiguous();
     }
-    template <typename T> T *at() const { return t ? static_cast<T *>(const_cast<void *>(t->const_data_ptr())) : nullptr; }
-    void *data() const { return t ? const_cast<void *>(t->const_data_ptr()) : nullptr; }
+    template <typename T = void> const T *read() const { return t ? static_cast<const T *>(t->const_data_ptr()) : nullptr; }
+    // For what is written: memory that the tensor shares with a lazy copy becomes its own.
+    template <typename T = void> T *written() const { return t ? static_cast<T *>(t->mutable_data_ptr()) : nullptr; }
 };
 
 int type_of(c10::ScalarType t)
@@ -121,24 +122,25 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (a.type < 0 || !k.heads(dev, type, tokens, c.heads, c.dim) || !v.heads(dev, type, tokens, c.heads, c.v_dim) ||
         !slots.plain(dev, c10::kLong, {tokens}))
         return not_taken();
-    a.k = k.data(), a.k_token = k.t->stride(0), a.k_head = k.t->stride(1);
-    a.v = v.data(), a.v_token = v.t->stride(0), a.v_head = v.t->stride(1);
-    a.slots = slots.at<int64_t>();
+    a.slots = slots.read<int64_t>();
     a.tokens = tokens;
     if (!q.none) {
         if (!q.heads(dev, type, tokens, 0, c.dim) || q.t->size(1) > INT32_MAX || !q_out.heads(dev, type, tokens, q.t->size(1), c.dim))
             return not_taken();
-        a.q = q.data(), a.q_token = q.t->stride(0), a.q_head = q.t->stride(1);
-        a.q_out = q_out.data(), a.out_token = q_out.t->stride(0), a.out_head = q_out.t->stride(1);
+        a.q_out = q_out.written(), a.q = q.read();  // in this order: all may be one tensor's
+        a.q_token = q.t->stride(0), a.q_head = q.t->stride(1);
+        a.out_token = q_out.t->stride(0), a.out_head = q_out.t->stride(1);
         a.q_heads = (int32_t)q.t->size(1);
     } else if (!q_out.none) {
         return not_taken();
     }
+    a.k = k.read(), a.k_token = k.t->stride(0), a.k_head = k.t->stride(1);
+    a.v = v.read(), a.v_token = v.t->stride(0), a.v_head = v.t->stride(1);
     if (!cos.none) {
         if (!cos.t || cos.t->dim() != 2 || cos.t->size(1) > INT32_MAX / 2 || !cos.plain(dev, c10::kFloat, cos.t->sizes()) ||
             !sin.plain(dev, c10::kFloat, cos.t->sizes()) || !positions.plain(dev, c10::kLong, {tokens}))
             return not_taken();
-        a.cos = cos.at<float>(), a.sin = sin.at<float>(), a.positions = positions.at<int64_t>();
+        a.cos = cos.read<float>(), a.sin = sin.read<float>(), a.positions = positions.read<int64_t>();
         a.angles = cos.t->size(0);
         a.rot = (int32_t)(2 * cos.t->size(1));
     } else if (!sin.none || !positions.none) {
@@ -182,12 +184,12 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n)
         return not_taken();
     if (!workspace.t || workspace.t->get_device() != dev || !workspace.t->is_contiguous())
         return not_taken();
-    a.out = out.data(), a.out_row = out.t->stride(0), a.out_head = out.t->stride(1);
-    a.q = q.data(), a.q_row = q.t->stride(0), a.q_head = q.t->stride(1);
-    a.lse = lse.at<float>();
-    a.table = table.at<int32_t>(), a.table_row = table.t->stride(0), a.table_width = table.t->size(1);
-    a.lens = lens.at<int32_t>();
-    a.workspace = workspace.data(), a.workspace_bytes = (int64_t)workspace.t->nbytes();
+    a.out = out.written(), a.out_row = out.t->stride(0), a.out_head = out.t->stride(1);
+    a.q = q.read(), a.q_row = q.t->stride(0), a.q_head = q.t->stride(1);
+    a.lse = lse.written<float>();
+    a.table = table.read<int32_t>(), a.table_row = table.t->stride(0), a.table_width = table.t->size(1);
+    a.lens = lens.read<int32_t>();
+    a.workspace = workspace.written(), a.workspace_bytes = (int64_t)workspace.t->nbytes();
     a.batch = batch, a.q_heads = (int32_t)q_heads, a.split = (int32_t)split;
     return PyLong_FromLong(unlocked(f, &c, &a, stream));
 }
@@ -219,7 +221,7 @@ PyObject *fold(PyObject *, PyObject *const *args, Py_ssize_t n)
         step *= shape[d], lse_step *= shape[d], rows *= shape[d];
     }
     const int64_t W = shape[0], dim = shape.back();
-    return PyLong_FromLong(unlocked(f, out.data(), outs.data(), lses.at<float>(), lse.at<float>(), type, (int32_t)W, rows, dim,
+    return PyLong_FromLong(unlocked(f, out.written(), outs.read(), lses.read<float>(), lse.written<float>(), type, (int32_t)W, rows, dim,
                                     W > 1 ? o.stride(0) : rows * dim, W > 1 ? lses.t->stride(0) : rows, stream));
 }
 
