@@ -56,6 +56,8 @@ int type_of(c10::ScalarType t)
     return t == c10::kFloat ? DETFOLD_F32 : t == c10::kBFloat16 ? DETFOLD_BF16 : t == c10::kHalf ? DETFOLD_F16 : -1;
 }
 
+int cache_type_of(c10::ScalarType t) { return t == c10::kFloat8_e4m3fn ? DETFOLD_E4M3 : type_of(t); }
+
 struct Numbers {
     bool ok = true;
     int64_t whole(PyObject *o)
@@ -78,11 +80,45 @@ struct Numbers {
     }
 };
 
-bool cache_of(PyObject *o, detfold_paged_cache *c)
+PyObject *kDescribed, *kKeys, *kValues, *kKeyScale, *kValueScale;  // names of a PagedCache's attributes
+
+struct Attr {  // one of these, held
+    PyObject *o;
+    Attr(PyObject *of, PyObject *name) : o(PyObject_GetAttr(of, name))
+    {
+        if (!o) {
+            PyErr_Clear();
+            o = Py_NewRef(Py_None);
+        }
+    }
+    Attr(const Attr &) = delete;
+    ~Attr() { Py_DECREF(o); }
+};
+
+// A PagedCache as it was described when it was made, with the addresses and
+// strides that its tensors have now.
+bool cache_of(PyObject *o, int64_t dev, bool written, detfold_paged_cache *c)
 {
-    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof(*c))
+    const Attr described(o, kDescribed), ko(o, kKeys), vo(o, kValues);
+    if (!PyBytes_Check(described.o) || PyBytes_GET_SIZE(described.o) != (Py_ssize_t)sizeof(*c))
         return false;
-    std::memcpy(c, PyBytes_AS_STRING(o), sizeof(*c));
+    std::memcpy(c, PyBytes_AS_STRING(described.o), sizeof(*c));
+    const Arg k(ko.o), v(vo.o);
+    for (const Arg *x : {&k, &v})
+        if (!x->on(dev) || x->t->dim() != 4 || cache_type_of(x->t->scalar_type()) != c->type || x->t->size(0) != c->pages ||
+            x->t->size(1) != c->page || x->t->size(2) != c->heads || x->t->size(3) != (x == &k ? c->dim : c->v_dim))
+            return false;
+    c->k = written ? k.written() : const_cast<void *>(k.read()), c->v = written ? v.written() : const_cast<void *>(v.read());
+    c->k_page = k.t->stride(0), c->k_token = k.t->stride(1), c->k_head = k.t->stride(2);
+    c->v_page = v.t->stride(0), c->v_token = v.t->stride(1), c->v_head = v.t->stride(2);
+    for (const float **scale : {&c->k_scale, &c->v_scale})
+        if (*scale) {
+            const Attr so(o, scale == &c->k_scale ? kKeyScale : kValueScale);
+            const Arg x(so.o);
+            if (!x.plain(dev, c10::kFloat, {c->heads}))
+                return false;
+            *scale = x.read<float>();
+        }
     return true;
 }
 
@@ -107,10 +143,12 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     detfold_paged_cache c;
     Numbers num;
-    if (n != 13 || !cache_of(args[1], &c))
+    if (n != 13)
         return not_taken();
     const AppendFn f = (AppendFn)num.address(args[0]);
     const int64_t dev = num.whole(args[2]);
+    if (!cache_of(args[1], dev, true, &c))
+        return not_taken();
     void *stream = num.address(args[3]);
     const Arg k(args[4]), v(args[5]), slots(args[6]), q(args[7]), q_out(args[8]), positions(args[9]), cos(args[10]), sin(args[11]);
     if (!num.ok || !k.t || k.t->dim() != 3)
@@ -157,10 +195,12 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     detfold_paged_cache c;
     Numbers num;
-    if (n != 14 || !cache_of(args[1], &c))
+    if (n != 14)
         return not_taken();
     const AttendFn f = (AttendFn)num.address(args[0]);
     const int64_t dev = num.whole(args[2]);
+    if (!cache_of(args[1], dev, false, &c))
+        return not_taken();
     void *stream = num.address(args[3]);
     const Arg out(args[4]), q(args[5]), table(args[6]), lens(args[7]), lse(args[11]), workspace(args[12]);
     detfold_attend a = {};
@@ -250,6 +290,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, null
 
 PyMODINIT_FUNC PyInit__bind()
 {
+    const struct {
+        PyObject **at;
+        const char *name;
+    } names[] = {{&kDescribed, "_c"}, {&kKeys, "k"}, {&kValues, "v"}, {&kKeyScale, "k_scale"}, {&kValueScale, "v_scale"}};
+    for (const auto &n : names)
+        if (!(*n.at = PyUnicode_InternFromString(n.name)))
+            return nullptr;
     PyObject *m = PyModule_Create(&module);
     if (m && PyModule_AddStringConstant(m, "built_from", DETFOLD_BUILT_FROM) < 0) {
         Py_DECREF(m);

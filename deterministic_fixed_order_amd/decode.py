@@ -185,17 +185,25 @@ class PagedCache:
                              % (tuple(k.shape), tuple(v.shape)))
         pages, page, heads, dim = k.shape
         dev = k.get_device()
-        ks, vs = _place(k, "k", dev), _place(v, "v", dev)
-        scales = []
-        for s, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if s is not None and type_ != E4M3:
+        for x, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if x is not None and type_ != E4M3:
                 raise ValueError("%s is for float8_e4m3fn caches" % nm)
-            scales.append(0 if s is None else _plain(s, nm, dev, "float32", (heads,)))
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.page, self.heads, self.dim, self.v_dim = pages, page, heads, dim, v.shape[3]
         self.type, self.device_index = type_, dev
-        self._c = _CACHE.pack(k.data_ptr(), v.data_ptr(), scales[0], scales[1], pages, ks[0], ks[1], ks[2],
-                              vs[0], vs[1], vs[2], page, heads, dim, self.v_dim, type_, 0)
+        self._c = self._described()
+
+    def _described(self) -> bytes:
+        """The cache for the library, where its tensors lie now."""
+        k, v, dev = self.k, self.v, self.device_index
+        for x, nm, dim in ((k, "k", self.dim), (v, "v", self.v_dim)):
+            if tuple(x.shape) != (self.pages, self.page, self.heads, dim) or _type(x, nm) != self.type:
+                raise ValueError("the cache's %s has changed its shape or type, to %s of %s" % (nm, tuple(x.shape), x.dtype))
+        ks, vs = _place(k, "k", dev), _place(v, "v", dev)
+        scales = [0 if x is None else _plain(x, nm, dev, "float32", (self.heads,))
+                  for x, nm in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale"))]
+        return _CACHE.pack(k.data_ptr(), v.data_ptr(), scales[0], scales[1], self.pages, ks[0], ks[1], ks[2],
+                           vs[0], vs[1], vs[2], self.page, self.heads, self.dim, self.v_dim, self.type, 0)
 
 
 def _same(t, name: str, want: int, like) -> None:
@@ -216,7 +224,7 @@ def cache_append(cache: PagedCache, k, v, slots, *, q=None, q_out=None, position
     one call must not share a slot."""
     dev = cache.device_index
     current, call, of = (_native or _bound())[:3]
-    rc = call(of, cache._c, dev, current(dev) if stream is None else int(stream.cuda_stream), k, v, slots, q, q_out,
+    rc = call(of, cache, dev, current(dev) if stream is None else int(stream.cuda_stream), k, v, slots, q, q_out,
               positions, cos, sin, pairs)
     if rc >= 0:
         return _check(rc, "cache_append") if rc else None
@@ -255,7 +263,7 @@ def cache_append(cache: PagedCache, k, v, slots, *, q=None, q_out=None, position
     args = _APPEND.pack(k.data_ptr(), v.data_ptr(), qp, op, _plain(slots, "slots", dev, "int64", (tokens,)), pp,
                         cp, sp, tokens, angles, ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], os[0], os[1], type_,
                         q_heads, rot, 1 if pairs else 0)
-    _check(_load().detfold_cache_append(cache._c, args, _stream(k, stream)), "cache_append")
+    _check(_load().detfold_cache_append(cache._described(), args, _stream(k, stream)), "cache_append")
 
 
 def _within(stream, dev: int):
@@ -296,7 +304,7 @@ def attend_paged(out, q, cache: PagedCache, table, lens, *, scale=None, window: 
     batch around it."""
     dev = cache.device_index
     current, _, _, call, of = (_native or _bound())[:5]
-    rc = call(of, cache._c, dev, current(dev) if stream is None else int(stream.cuda_stream), out, q, table, lens,
+    rc = call(of, cache, dev, current(dev) if stream is None else int(stream.cuda_stream), out, q, table, lens,
               1.0 / math.sqrt(cache.dim) if scale is None else scale, window, max_len, lse, workspace, split)
     if rc >= 0:
         return _check(rc, "attend_paged") if rc else None
@@ -328,7 +336,7 @@ def attend_paged(out, q, cache: PagedCache, table, lens, *, scale=None, window: 
     args = _ATTEND.pack(out.data_ptr(), q.data_ptr(), lse_p, table.data_ptr(), lens_p, workspace.data_ptr(),
                         workspace.nbytes, batch, max_len, window, ts[0], width, qs[0], qs[1], os[0], os[1],
                         1.0 / math.sqrt(cache.dim) if scale is None else scale, type_, out_type, q_heads, split, 0)
-    _check(_load().detfold_attend_paged(cache._c, args, _stream(q, stream)), "attend_paged")
+    _check(_load().detfold_attend_paged(cache._described(), args, _stream(q, stream)), "attend_paged")
 
 
 def plan_attend(cache, batch: int, q_heads: int, max_len: int, cu_count: int, *, window: int = 0,

@@ -19,23 +19,31 @@ from deterministic_fixed_order_amd import _bind, decode as d
 
 seen = []
 P, I, Q = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-STRUCT = ctypes.CFUNCTYPE(ctypes.c_int, P, P, P)(lambda c, a, s: (seen.append(a), 7)[1])
+STRUCT = ctypes.CFUNCTYPE(ctypes.c_int, P, P, P)(lambda c, a, s: (seen.append(d.PagedCacheC.from_buffer_copy(
+    ctypes.string_at(c, ctypes.sizeof(d.PagedCacheC)))), 7)[1])
 FOLD = ctypes.CFUNCTYPE(ctypes.c_int, P, P, P, P, I, I, Q, Q, Q, Q, P)(lambda *a: (seen.append(a), 7)[1])
 at = lambda f: ctypes.cast(f, P).value
-CACHE = bytes(d.PagedCacheC(k=1 << 40, v=1 << 41, pages=4, k_page=2048, k_token=128, k_head=64, v_page=2048, v_token=128,
-                            v_head=64, page=16, heads=2, dim=64, v_dim=64, type=d.F32))
+
+
+class Cache:
+    # what the binding reads of a PagedCache
+    _c = bytes(d.PagedCacheC(k=1 << 40, v=1 << 41, pages=4, k_page=2048, k_token=128, k_head=64, v_page=2048, v_token=128,
+                             v_head=64, page=16, heads=2, dim=64, v_dim=64, type=d.F32))
+
+    def __init__(self, device):
+        self.k, self.v = (torch.zeros((4, 16, 2, 64), device=device) for _ in range(2))
 
 
 def append(x, q, dev):
     n = x.shape[0]
-    return _bind.append(at(STRUCT), CACHE, dev, 0, x, x, torch.zeros(n, dtype=torch.int64, device=x.device), q, q, None,
+    return _bind.append(at(STRUCT), Cache(q.device), dev, 0, x, x, torch.zeros(n, dtype=torch.int64, device=x.device), q, q, None,
                         None, None, False)
 
 
 def attend(x, q, dev):
     n = q.shape[0]
     table, lens = (torch.zeros(s, dtype=torch.int32, device=q.device) for s in ((n, 4), (n,)))
-    return _bind.attend(at(STRUCT), CACHE, dev, 0, torch.empty_like(q), q, table, lens, 0.125, 0, 64, None,
+    return _bind.attend(at(STRUCT), Cache(q.device), dev, 0, torch.empty_like(q), q, table, lens, 0.125, 0, 64, None,
                         torch.empty(64, device=q.device), 0)
 
 
@@ -110,3 +118,28 @@ with FakeTensorMode():
     except RuntimeError as e:
         print("refused")
 """, transform) == "refused"
+
+
+def test_the_caches_memory_is_read_at_each_call():
+    """Other memory, other strides, another shape; and a lazy copy of a cache that is appended to."""
+    assert _run("""
+x, q, c = torch.ones((3, 2, 64)), torch.ones((3, 4, 64)), Cache("cpu")
+Cache = lambda device: c
+for step in range(4):
+    for op in (append, attend):
+        got = op(x, q, -1)
+        assert got == (7 if step < 3 else -1), (step, op, got)
+        if got == 7:
+            s = seen.pop()
+            assert (s.k, s.v) == (c.k.data_ptr(), c.v.data_ptr())
+            assert (s.k_page, s.k_token, s.k_head) == c.k.stride()[:3] and (s.v_page, s.v_token, s.v_head) == c.v.stride()[:3]
+    if step == 0:
+        c.k.data, c.v.data = torch.zeros((4, 16, 2, 64)), torch.zeros((4, 2, 16, 64)).transpose(1, 2)
+    elif step == 1:
+        lazy = torch._lazy_clone(c.k)
+    elif step == 2:
+        c.v.data = torch.zeros((3, 16, 2, 64))
+lazy_address = torch._C._data_address(lazy)
+assert lazy_address != c.k.data_ptr()
+print("read")
+""") == "read"

@@ -43,7 +43,8 @@ def stood_in(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: types.SimpleNamespace(cuda_stream=h))
     cache = object.__new__(d.PagedCache)
     cache.k = cache.v = torch.zeros((4, 16, 2, 64))
-    cache.device_index, cache.heads, cache.dim, cache.v_dim, cache.page, cache._c = -1, 2, 64, 64, 16, b""
+    cache.k_scale = cache.v_scale = None
+    cache.device_index, cache.heads, cache.dim, cache.v_dim, cache.page, cache.pages, cache.type = -1, 2, 64, 64, 16, 4, d.F32
     q = torch.zeros((3, 4, 64))
 
     def call(**kw):
