@@ -5,8 +5,9 @@
 // Mathematics.  With s_t = scale * (q . k_t) a wave keeps, per query head, the
 // largest score m so far, l = sum exp(s_t - m) and o = sum exp(s_t - m) v_t; a
 // larger m' turns l and o by exp(m - m').  Two such states join the same way, so
-// the tokens can be split over waves, workgroups and launches.  Scores are held
-// in units of log 2, and everything in binary32.
+// the tokens can be split over waves, workgroups and launches.  All is held in
+// binary32; log2 e multiplies a score's distance from m, not the score, which
+// could overflow.
 //
 // What bounds it.  Every key and value is read once from HBM and used for at
 // most 16 query heads: 4 to 16 flop a byte, far below what the matrix units
@@ -170,11 +171,17 @@ __device__ __forceinline__ uint32_t keep_from(int n, int j)
     return bits >= 32 ? 0u : bits > 0 ? ~0u << bits : ~0u;
 }
 
+// exp of a score's distance from the largest one (-infinity: 0); times 2^lift.
+template <int LIFT = 0> __device__ __forceinline__ float weight_of(float s)
+{
+    return __builtin_amdgcn_exp2f(LIFT ? __builtin_fmaf(s, kLog2e, (float)LIFT) : s * kLog2e);
+}
+
 // The ends of a row: what its sums are multiplied by (one division a row; a
-// row without a token gives 0), the logarithm of its weights' sum (m is in
-// units of log 2), and the store of N values.
+// row without a token gives 0), the logarithm of its weights' sum, and the store
+// of N values.
 __device__ __forceinline__ float out_scale(float v_scale, float l) { return l == 0.0f ? 0.0f : v_scale / l; }
-__device__ __forceinline__ float log_sum(float m, float l) { return (m == -INFINITY ? 0.0f : m * kLn2) + logf(l); }
+__device__ __forceinline__ float log_sum(float m, float l) { return (m == -INFINITY ? 0.0f : m) + logf(l); }
 template <int N> __device__ __forceinline__ void put_out(const detfold_attend &a, int64_t at, const float (&o)[N])
 {
     if (a.out_type == DETFOLD_F32) {
@@ -338,7 +345,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
         const char *k0 = (const char *)c.k + (int64_t)h * c.k_head * CS, *v0 = (const char *)c.v + (int64_t)h * c.v_head * CS;
         const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
         const uint32_t pages = (uint32_t)c.pages;
-        const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f) * kLog2e;
+        const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f);
         const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
 
         // Where a lane's loads lie within a key and a value.
@@ -444,7 +451,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
 
         // Weights of 16-bit floats are held 2^15 times larger, so that small ones
         // keep their digits; the sum is too, and both are put right at the end.
-        constexpr float kLift = PV == kF16 ? 15.0f : 0.0f;
+        constexpr int kLift = PV == kF16 ? 15 : 0;
         float m = -INFINITY, l = 0.0f;
         f4 acc[NP][VW];
 #pragma unroll
@@ -570,7 +577,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
             top = fmaxf(m, over_groups(top, [](float y, float z) { return fmaxf(y, z); }));
             const float base = top == -INFINITY ? 0.0f : top;
             if (__any(top > m)) {
-                const float turn = __builtin_amdgcn_exp2f(m - base);
+                const float turn = weight_of(m - base);
                 l *= turn;
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
@@ -583,7 +590,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
             for (int u = 0; u < UT; ++u)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[u][j] = __builtin_amdgcn_exp2f((x[u][j] - base) + kLift);
+                    x[u][j] = weight_of<kLift>(x[u][j] - base);
                     l += x[u][j];
                 }
             // Values: the output's rows are its dims, its columns the query heads.
@@ -690,7 +697,7 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
             float total = 0.0f;
             for (int w = in; w < waves; w += beside) {
                 const f2 ml = state[w * 16 + head];
-                const float by = __builtin_amdgcn_exp2f(ml.x - base);
+                const float by = weight_of(ml.x - base);
                 total += ml.y * by;
                 sum += *(const f4 *)(sums + (w * heads + head) * S::kRow + at) * by;
             }

@@ -62,13 +62,13 @@ template <int LANES, int WAVES> __global__ __launch_bounds__(64 * WAVES) void k_
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             top = fmaxf(top, s[j].x);
-        const float base = top == -INFINITY ? 0.0f : top, turn = __builtin_amdgcn_exp2f(m - base);
+        const float base = top == -INFINITY ? 0.0f : top, turn = weight_of(m - base);
         l *= turn;
         acc *= turn;
         m = top;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float w = __builtin_amdgcn_exp2f(s[j].x - base);
+            const float w = weight_of(s[j].x - base);
             l += s[j].y * w;
             acc += x[j] * w;
         }
@@ -87,7 +87,7 @@ template <int LANES, int WAVES> __global__ __launch_bounds__(64 * WAVES) void k_
     const float base = top == -INFINITY ? 0.0f : top;
     acc = f4{0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
     for (int i = 0; i < GROUPS; ++i) {
-        const float w = __builtin_amdgcn_exp2f(mls[i].x - base);
+        const float w = weight_of(mls[i].x - base);
         l += mls[i].y * w;
         acc += accs[i][lane] * w;
     }

@@ -30,7 +30,7 @@ template <> __device__ __forceinline__ e4m3 from_f32<e4m3>(float x)
     return {(uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, x, 0, false)};
 }
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ uint32_t divide(uint32_t x, const Divider &d)
 {
