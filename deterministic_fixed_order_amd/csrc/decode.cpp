@@ -65,6 +65,41 @@ struct Range {
 Range range(const void *p, int64_t elems, int size) { return {(uintptr_t)p, p ? (uint64_t)elems * (uint64_t)size : 0}; }
 bool meet(const Range &a, const Range &b) { return ranges_overlap(a.p, a.bytes, b.p, b.bytes); }
 
+// A view [tokens][heads][dim], in elements.
+struct Heads {
+    const void *p;
+    int64_t token, head, heads, dim;
+};
+
+// Whether x + t * step lies within (-b, a) for some |t| < tokens.
+bool reaches(int64_t x, int64_t step, int64_t tokens, int64_t a, int64_t b)
+{
+    if (tokens == 1 || step == 0)
+        return x > -b && x < a;
+    const int64_t y = -b - x;  // the first t with t * step > y
+    const int64_t t = (y >= 0 ? y / step : -((-y + step - 1) / step)) + 1;
+    return t < tokens && x + (t > -tokens ? t : 1 - tokens) * step < a;
+}
+
+// Whether two such views, whose spans meet, share an element.  Of tokens that are
+// not equally far apart, and of more than 2^20 pairs of heads that interleave, it
+// is taken as given.
+bool share_elements(const Heads &q, const Heads &k, int64_t tokens, int size)
+{
+    if (tokens > 1 && q.token != k.token)
+        return true;
+    const int64_t apart = ((int64_t)(uintptr_t)k.p - (int64_t)(uintptr_t)q.p) / size;
+    if (!reaches(apart, q.token, tokens, (q.heads - 1) * q.head + q.dim, (k.heads - 1) * k.head + k.dim))
+        return false;
+    if (q.heads * k.heads > (int64_t)1 << 20)
+        return true;
+    for (int64_t i = 0; i < q.heads; ++i)
+        for (int64_t j = 0; j < k.heads; ++j)
+            if (reaches(apart + j * k.head - i * q.head, q.token, tokens, q.dim, k.dim))
+                return true;
+    return false;
+}
+
 int64_t cache_span(const detfold_paged_cache &c, bool values)
 {
     const int64_t d[3][2] = {{c.pages, values ? c.v_page : c.k_page},
@@ -147,12 +182,14 @@ int check_append(const detfold_paged_cache *c, const detfold_append *a)
                         range(c->k_scale, c->heads, 4), range(c->v_scale, c->heads, 4)};
     const Range out = range(a->q_out, os, size);
     // In place, a query view among its neighbours of one projection: the
-    // spans of k and v interleave with it, its elements do not.
+    // spans of k and v interleave with it, its elements must not.
     const bool in_place = a->q_out && a->q_out == a->q && a->out_token == a->q_token && a->out_head == a->q_head;
+    const Heads turned = {a->q, a->q_token, a->q_head, nq, c->dim};
+    const Heads beside[] = {{a->k, a->k_token, a->k_head, c->heads, c->dim}, {a->v, a->v_token, a->v_head, c->heads, c->v_dim}};
     for (int i = 0; i < (int)(sizeof(in) / sizeof(in[0])); ++i) {
         if (meet(k, in[i]) || meet(v, in[i]))
             return DETFOLD_EOVERLAP;
-        if (!(in_place && i < 3) && meet(out, in[i]))
+        if (meet(out, in[i]) && !(in_place && (i == 2 || (i < 2 && !share_elements(turned, beside[i], a->tokens, size)))))
             return DETFOLD_EOVERLAP;
     }
     if (meet(out, k) || meet(out, v))

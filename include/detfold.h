@@ -427,7 +427,9 @@ typedef struct detfold_paged_cache {
  *              table of angles turns its token into NaN
  *   cos, sin   device, [angles][rot / 2] floats; needed with rot > 0
  *   q, q_out   device, [tokens][q_heads][dim]; both NULL when q_heads = 0.
- *              q_out may be q itself (same strides) and else overlaps nothing
+ *              q_out may be q itself (same strides) and else overlaps nothing;
+ *              the spans of k and v may then interleave with it (views of one
+ *              projection, whose tokens are equally far apart), not their elements
  *   type       of k, v, q and q_out
  * Strides are in elements; values of a head are contiguous.
  * Errors: DETFOLD_EINVAL (also for types that do not go together), DETFOLD_EOVERLAP,
