@@ -290,17 +290,6 @@ template <typename T> const void *pick_softmax(int v, bool once)
     return v == 4 ? softmax_once<T, 4>(once) : v == 2 ? softmax_once<T, 2>(once) : softmax_once<T, 1>(once);
 }
 
-// The widest access of at most 16 bytes that each of these runs of values holds
-// at least once (the last one of a run may then overlap another, which writes
-// the same), or, where a write must not come before another's read, divides.
-int width(int type, bool overlap, int64_t a, int64_t b, int64_t c)
-{
-    int v = 16 / elem_size(type);
-    for (int64_t n : {a, b, c})
-        while (overlap ? n > 0 && n < v : n % v != 0)
-            v /= 2;
-    return v;
-}
 int chunks(int64_t n, int v) { return (int)((n + v - 1) / v); }
 
 bool launch(const void *k, int64_t blocks, int threads, void *args, void *stream)
@@ -314,7 +303,7 @@ bool launch(const void *k, int64_t blocks, int threads, void *args, void *stream
 int launch_append(const AppendArgs &a, void *stream)
 {
     AppendArgs p = a;
-    const int v = width(a.a.type, a.a.q != a.a.q_out, a.a.rot / 2, a.c.dim - a.a.rot, a.c.v_dim);
+    const int v = a.width;
     p.chunks = divider(chunks(a.a.rot / 2, v) + chunks(a.c.dim - a.a.rot, v));
     p.v_chunks = divider(chunks(a.c.v_dim, v));
     // One head a thread where there are not enough tokens to fill the device
@@ -340,7 +329,7 @@ int launch_append(const AppendArgs &a, void *stream)
 int launch_softmax(const SoftmaxArgs &a, void *stream)
 {
     SoftmaxArgs p = a;
-    const int v = width(a.type, true, a.dim, 0, 0);
+    const int v = access_width(a.type, true, a.dim, 0, 0);
     const bool once = a.rows * a.dim * elem_size(a.type) >= kOnceBytes;
     const void *k = a.type == DETFOLD_F32 ? pick_softmax<float>(v, once) : a.type == DETFOLD_BF16 ? pick_softmax<bf16>(v, once) : pick_softmax<f16>(v, once);
     p.chunks = divider((uint32_t)chunks(a.dim, v));

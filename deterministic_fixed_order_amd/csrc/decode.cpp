@@ -197,6 +197,24 @@ int check_append(const detfold_paged_cache *c, const detfold_append *a)
     return DETFOLD_OK;
 }
 
+// The widest access of at most 16 bytes that each of these runs of values holds
+// at least once (the last one of a run may then overlap another, which writes
+// the same), or, where a write must not come before another's read, divides.
+int access_width(int type, bool overlap, int64_t a, int64_t b, int64_t c)
+{
+    int v = 16 / elem_size(type);
+    for (int64_t n : {a, b, c})
+        while (overlap ? n > 0 && n < v : n % v != 0)
+            v /= 2;
+    return v;
+}
+
+int append_width(const detfold_paged_cache &c, const detfold_append &a)
+{
+    const bool in_place = a.q_heads > 0 && a.q == a.q_out;
+    return access_width(a.type, !in_place, a.rot / 2, c.dim - a.rot, c.v_dim);
+}
+
 int plan_attend(const detfold_paged_cache &c, int64_t batch, int32_t q_heads, int64_t max_len,
                 int64_t window, int32_t split, bool wide, int32_t cu_count, AttendPlan *p)
 {
@@ -358,6 +376,7 @@ int detfold_cache_append(const detfold_paged_cache *cache, const detfold_append 
     k.c = *cache;
     k.a = *args;
     k.page = divider((uint32_t)cache->page);
+    k.width = append_width(*cache, *args);
     return launch_append(k, stream);
 }
 

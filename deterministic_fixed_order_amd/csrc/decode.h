@@ -49,6 +49,7 @@ struct AppendArgs {
     int64_t token0;
     uint32_t tokens, turn;
     int32_t q_groups;
+    int32_t width;  // values of an access
 };
 
 struct AttendArgs {
@@ -110,6 +111,8 @@ struct SoftmaxArgs {
 bool types_pair(int32_t type, int32_t cache_type);
 int check_cache(const detfold_paged_cache *c);
 int check_append(const detfold_paged_cache *c, const detfold_append *a);
+int access_width(int type, bool overlap, int64_t a, int64_t b, int64_t c);
+int append_width(const detfold_paged_cache &c, const detfold_append &a);
 int check_attend(const detfold_paged_cache *c, const detfold_attend *a);
 int check_softmax(const SoftmaxArgs &s);
 struct AttendPlan : detfold_attend_plan {

@@ -6,8 +6,8 @@
 
 namespace detfold_impl {
 
-static int launches;
-int launch_append(const AppendArgs &, void *) { return ++launches, DETFOLD_OK; }
+static int launches, width;
+int launch_append(const AppendArgs &a, void *) { return ++launches, width = a.width, DETFOLD_OK; }
 int launch_softmax(const SoftmaxArgs &, void *) { return ++launches, DETFOLD_OK; }
 int launch_attend(const AttendArgs &, void *) { return ++launches, DETFOLD_OK; }
 int current_cu_count(int32_t *cu) { return *cu = 256, DETFOLD_OK; }
@@ -15,3 +15,4 @@ int current_cu_count(int32_t *cu) { return *cu = 256, DETFOLD_OK; }
 }  // namespace detfold_impl
 
 extern "C" int recorded_launches() { return detfold_impl::launches; }
+extern "C" int recorded_width() { return detfold_impl::width; }  // of the last append
