@@ -168,13 +168,20 @@ def build_library(out: str = LIB, extra: list[str] | None = None) -> str:
     return out
 
 
-def build_binding(out: str = BINDING_LIB) -> str:
+def build_binding(out: str = BINDING_LIB) -> str | None:
     """Compile bind.cpp, the C++ side of decode.py's calls (host code only),
     against the installed torch.  It holds the digest of the sources, so that
-    it is never used beside a library of other ones."""
+    it is never used beside a library of other ones.  Without torch there are no
+    such calls, and nothing is built."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        print("torch is not installed: %s, the C++ side of decode.py, is not built" % os.path.basename(out))
+        return None
     from torch.utils import cpp_extension
     tmp = out + ".tmp%d" % os.getpid()
     flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
