@@ -473,6 +473,9 @@ __global__ __launch_bounds__(512) void k_attend(AttendArgs)
                     qw[i].w[j] = col < live ? qw[i].w[j] & keep_from(drop * QS, j) : 0u;
                 if constexpr (QK == kSplit) {
 #pragma unroll
+                    for (int j = 0; j < 8; ++j)  // a NaN whose bits all lie below the first part's would be an infinity there
+                        qw[i].w[j] = __builtin_isnan(__builtin_bit_cast(float, qw[i].w[j])) ? 0x7fc00000u : qw[i].w[j];
+#pragma unroll
                     for (int part = 0; part < 3; ++part) {  // the highest bits, of which two values' are stored together
                         u4 w;
 #pragma unroll
