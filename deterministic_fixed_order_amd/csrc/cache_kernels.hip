@@ -201,6 +201,14 @@ template <typename T> __device__ __forceinline__ float weight(float x)
     return sizeof(T) == 4 ? expf(x) : __builtin_amdgcn_exp2f(x * kLog2e);
 }
 
+// A sum over its weights' sum (by: that one's inverse): divided in float32; to 16
+// bits, whose own rounding is 2^13 times that of another product, multiplied (1 to 5%
+// of the time of large folds).
+template <typename T> __device__ __forceinline__ float mean(float sum, float total, float by)
+{
+    return sizeof(T) == 4 ? sum / total : sum * by;
+}
+
 // The softmax fold.  A thread takes V neighbouring values of a row, eight
 // partials' loads at a time, and forms the row's weights itself: eight
 // exponentials cost less than handing them round.  Ascending in w throughout.
@@ -248,11 +256,11 @@ template <typename T, int V, bool ONCE> __global__ __launch_bounds__(kFold) void
                     acc[n] = acc[n] + (lse[j] == -INFINITY ? 0.0f : a * to_f32(x[j].x[n]));
             }
     }
-    const float by = total == 0.0f ? 0.0f : 1.0f / total;
+    const float some = total == 0.0f ? 1.0f : total, by = 1.0f / some;  // no partial had a token: the sums are zero
     Vec<T, V> o;
 #pragma unroll
     for (int n = 0; n < V; ++n)
-        o.x[n] = from_f32<T>(acc[n] * by);
+        o.x[n] = from_f32<T>(mean<T>(acc[n], some, by));
     store_vec<T, V, ONCE>((T *)s.out + at, o);
     if (s.lse && u == 0)
         s.lse[row] = (top == -INFINITY ? 0.0f : top) + logf(total);

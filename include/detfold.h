@@ -520,7 +520,7 @@ int detfold_attend_workspace(const detfold_paged_cache *cache, int64_t batch, in
  * the softmax-weighted mean outs_w of its own tokens with lse_w the logarithm
  * of its sum of exponentials (the ranks of a cache split over its length):
  *     top = max_w lse_w,  a_w = exp(lse_w - top),  l = a_0 + a_1 + ... ,
- *     out[i] = ((a_0 * outs_0[i] + a_1 * outs_1[i]) + ...) * (1 / l),  lse = top + log(l),
+ *     out[i] = ((a_0 * outs_0[i] + a_1 * outs_1[i]) + ...) / l,  lse = top + log(l),
  * strictly ascending in w and held in binary32, so the bits do not depend on
  * the launch.  A partial with lse_w = -infinity had no token: it adds nothing,
  * whatever its outs hold.  Where no partial had one, out = 0 and lse = -infinity.
