@@ -124,10 +124,13 @@ int launch_attend(const AttendArgs &a, void *stream)
     const int heads = a.group < 16 ? a.group : 16;
     const int queries = a.beside * k.q_bytes, sums = a.waves * (128 + heads * k.head_bytes), lds = queries > sums ? queries : sums;
     if (a.shares.d) {
-        // Where rows have few parts, what counts is how many waves look for one:
-        // 64 ragged rows 5 us with two a workgroup, 12 with eight, which take 5
-        // us less than two where 16 rows have eight parts each.
-        const bool few = a.a.batch * 4 >= a.shares.d;
+        // Where rows have few parts, what counts is how many waves look for one: the
+        // join of 64 ragged rows takes 7 us with two a workgroup and 12 with eight,
+        // of 256 rows 5 and 7, of 16 rows of eight parts each 5.2 and 6.4.  Rows of
+        // many parts want the waves: 1 x 131072 over two key heads of e4m3 (256
+        // parts) 28 us in all with two, 24 with eight; 2 rows (128) 24 and 22, 4
+        // rows (64) 22.1 both, 8 rows (32) 21.2 and 22.3.
+        const bool few = a.a.batch * 32 >= a.shares.d;
         return launch(k.f, (int64_t)a.shares.d * a.units.d, 64 * a.waves, lds) &&
                        launch(few ? pick_join<2>(a.c.v_dim) : pick_join<8>(a.c.v_dim), (a.by_row ? a.a.batch : a.shares.d) * a.a.q_heads,
                               few ? 128 : 512, 0)
