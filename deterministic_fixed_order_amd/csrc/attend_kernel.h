@@ -29,14 +29,14 @@
 //   the device: 64 ragged rows took 281 us in parts of a fixed size, 160 so.
 //
 // Measured (MI355X, GPU time of the call with its join): 1 x 131072 bfloat16, 32
-// heads over 8 of 128: 90 us, 6.0 TB/s; 64 ragged rows of up to 8192: 160 us, 6.3
-// TB/s; 256 x 4096 e4m3: 326 us, 6.6 TB/s; 16 x 16384 float32: 316 us, 6.8 TB/s;
+// heads over 8 of 128: 90 us, 6.0 TB/s; 64 ragged rows of up to 8192: 161 us, 6.3
+// TB/s; 256 x 4096 e4m3: 328 us, 6.6 TB/s; 16 x 16384 float32: 316 us, 6.8 TB/s;
 // one row of 1000: 11.5 us, of which the loads' dependent latencies are 6 and the
 // join's launch 4.
 //
 // Weights are rounded to the cache's 16-bit type for the second product where
 // the output is of 16 bits too: half a step of what the output itself is rounded
-// to (0.0018 relative against the definition, 0.0017 with float32 weights).  A
+// to (0.0017 to 0.0019 relative against the definition, 0.0017 with float32 weights).  A
 // float32 output takes them whole.
 #ifndef DETFOLD_ATTEND_KERNEL_H
 #define DETFOLD_ATTEND_KERNEL_H
