@@ -26,6 +26,12 @@ The decode step around the fold (``decode.py``):
     attend_paged(out, q, cache, table, lens) one new token per row over its pages
     fold_softmax(out, outs, lses)            fixed-order join of attention partials
 
+The drafted step, several new tokens of a row at once (``draft.py``):
+
+    attend_tree(out, q, cache, table, lens)  a tree of drafted tokens per row over its pages
+    cache_copy(cache, src, dst)              pages to pages (forks, moves)
+    cache_compact(cache, table, picks, counts)  a row's kept tokens together
+
 ``stacked`` is a ``[W, len]`` float32 CUDA/HIP tensor (row r = slot r); a view
 with a storage offset is fine as long as it is contiguous.
 """
@@ -57,7 +63,8 @@ EXPORTS = (
     "detfold_one_shot_rank", "detfold_fold_ranks_timed", "detfold_loopback_round_static",
     "fold_ranks_batch", "fold_ranks_batch_scaled", "detfold_plan_fold_ranks_batch",
     "detfold_cache_append", "detfold_attend_paged", "detfold_plan_attend",
-    "detfold_attend_workspace", "detfold_fold_softmax",
+    "detfold_attend_workspace", "detfold_fold_softmax", "detfold_attend_tree", "detfold_plan_tree",
+    "detfold_tree_workspace", "detfold_cache_copy", "detfold_cache_compact",
 )
 MAX_JOBS = 32
 
@@ -148,6 +155,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.detfold_one_shot_all_reduce.argtypes = [ctypes.POINTER(OneShotLinkC), f32p, f32p, i64]
     lib.detfold_one_shot_rank.argtypes = [ctypes.POINTER(OneShotLinkC), i32, f32p, i64, vp]
     decode.bind(lib)
+    draft.bind(lib)
     for name in EXPORTS:
         if name != "detfold_strerror":
             getattr(lib, name).restype = ctypes.c_int
@@ -626,3 +634,5 @@ def plan_fold_into(dst_addr: int, stage_addr: int, n: int, cu_count: int) -> dic
 from . import decode  # noqa: E402  (after what it takes from here)
 from .decode import (PagedCache, attend_paged, attend_workspace, cache_append,  # noqa: E402
                      fold_softmax, plan_attend)
+from . import draft  # noqa: E402
+from .draft import attend_tree, cache_compact, cache_copy, plan_tree  # noqa: E402

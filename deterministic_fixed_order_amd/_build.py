@@ -5,8 +5,11 @@ plan.cpp (host-only planning and argument checks), detfold.cpp (call sequences
 and the C ABI), internal.h (their shared declarations); of the decode-step
 operators cache_kernels.hip and attend_kernels.hip (device code and launches),
 attend_f32.hip, attend_f16.hip and attend_bf16.hip (the instances of
-attend_kernel.h), decode.cpp (checks, planning and the C ABI), decode.h and
-decode_device.h; and bind.cpp, the C++ side of decode.py, a library of its own.
+attend_kernel.h), decode.cpp (checks, planning and the C ABI), decode.h,
+decode_check.h and decode_device.h; of the drafted step's tree_kernels.hip and
+page_kernels.hip (device code and launches), draft.cpp (checks, planning and the
+C ABI) and draft.h; and bind.cpp, the C++ side of both modules' calls, a library
+of its own.
 exports.map limits the exported symbols to the C ABI of include/detfold.h.
 
 The .hip files are compiled in two passes, so that device-only flags reach
@@ -49,8 +52,10 @@ SOURCES = [KERNELS] + HOST_SOURCES
 INTERNAL_HEADER = os.path.join(CSRC, "internal.h")
 DECODE_KERNELS = [os.path.join(CSRC, f) for f in ("cache_kernels.hip", "attend_kernels.hip", "attend_f32.hip",
                                                      "attend_f16.hip", "attend_bf16.hip")]
-DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_device.h", "attend_kernel.h",
-                                                                 "bind.cpp")]
+DRAFT_KERNELS = [os.path.join(CSRC, f) for f in ("tree_kernels.hip", "page_kernels.hip")]
+DRAFT_SOURCES = DRAFT_KERNELS + [os.path.join(CSRC, f) for f in ("draft.cpp", "draft.h")]
+DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_check.h", "decode_device.h",
+                                                                 "attend_kernel.h", "bind.cpp")]
 BINDING = os.path.join(CSRC, "bind.cpp")
 EXPORTS_MAP = os.path.join(CSRC, "exports.map")
 HEADER = os.path.join(ROOT, "include", "detfold.h")
@@ -86,7 +91,7 @@ def link_flags() -> list[str]:
 
 def source_digest() -> str:
     h = hashlib.sha256()
-    for path in SOURCES + DECODE_SOURCES + [INTERNAL_HEADER, EXPORTS_MAP, HEADER]:
+    for path in SOURCES + DECODE_SOURCES + DRAFT_SOURCES + [INTERNAL_HEADER, EXPORTS_MAP, HEADER]:
         with open(path, "rb") as f:
             h.update(os.path.basename(path).encode() + b"\0" + f.read() + b"\0")
     h.update("\0".join(common_flags() + device_flags() + link_flags()).encode())
@@ -138,8 +143,8 @@ def _host_object(src: str, work: str, extra: list[str]) -> str:
 
 
 def _objects(work: str, extra: list[str]) -> list[str]:
-    kernels = DECODE_KERNELS[::-1] + [KERNELS]
-    hosts = HOST_SOURCES + [s for s in DECODE_SOURCES if s.endswith(".cpp") and s != BINDING]
+    kernels = DECODE_KERNELS[::-1] + DRAFT_KERNELS + [KERNELS]
+    hosts = HOST_SOURCES + [s for s in DECODE_SOURCES + DRAFT_SOURCES if s.endswith(".cpp") and s != BINDING]
     with ThreadPoolExecutor(max_workers=min(6, os.cpu_count() or 1)) as pool:
         jobs = [pool.submit(_kernel_object, s, work, extra) for s in kernels]
         jobs += [pool.submit(_host_object, s, work, extra) for s in hosts]

@@ -265,6 +265,143 @@ PyObject *fold(PyObject *, PyObject *const *args, Py_ssize_t n)
                                     W > 1 ? o.stride(0) : rows * dim, W > 1 ? lses.t->stride(0) : rows, stream));
 }
 
+typedef int (*TreeFn)(const detfold_paged_cache *, const detfold_tree *, void *);
+typedef int (*CopyFn)(const detfold_paged_cache *, const detfold_paged_cache *, const int32_t *, const int32_t *, const int32_t *, int64_t,
+                      void *);
+typedef int (*CompactFn)(const detfold_paged_cache *, const detfold_compact *, void *);
+
+// A float, or a whole number in place of one.
+bool real(PyObject *o, float *to)
+{
+    double v = 0.0;
+    if (PyFloat_Check(o)) {
+        v = PyFloat_AS_DOUBLE(o);
+    } else if (PyLong_CheckExact(o)) {
+        v = PyLong_AsDouble(o);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return false;
+        }
+    } else {
+        return false;
+    }
+    *to = (float)v;
+    return std::isfinite(v) == std::isfinite(*to);
+}
+
+// An optional contiguous tensor.
+bool plain_or_none(const Arg &x, int64_t dev, c10::ScalarType type, c10::IntArrayRef shape) { return x.none || x.plain(dev, type, shape); }
+
+bool table_of(const Arg &x, int64_t dev, int64_t batch)
+{
+    return x.on(dev) && x.t->scalar_type() == c10::kInt && x.t->dim() == 2 && x.t->size(0) == batch;
+}
+
+// (function, cache, device, stream, out, q, table, lens, masks, counts, depths, cap, slopes, scale, window, max_len, lse,
+// workspace, split); q [batch, drafts, q_heads, dim], or [batch, q_heads, dim] of one token a row
+PyObject *tree(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    detfold_paged_cache c;
+    Numbers num;
+    if (n != 19)
+        return not_taken();
+    const TreeFn f = (TreeFn)num.address(args[0]);
+    const int64_t dev = num.whole(args[2]);
+    if (!cache_of(args[1], dev, false, &c))
+        return not_taken();
+    void *stream = num.address(args[3]);
+    const Arg out(args[4]), q(args[5]), table(args[6]), lens(args[7]), masks(args[8]), counts(args[9]), depths(args[10]), slopes(args[12]),
+        lse(args[16]), workspace(args[17]);
+    detfold_tree t = {};
+    detfold_attend &a = t.attend;
+    a.window = num.whole(args[14]), a.max_len = num.whole(args[15]);
+    const int64_t split = num.whole(args[18]);
+    if (!num.ok || !real(args[11], &t.cap) || !real(args[13], &a.scale) || split < 0 || split > INT32_MAX || !q.on(dev) || !out.on(dev))
+        return not_taken();
+    const int64_t dims = q.t->dim(), batch = q.t->size(0);
+    if ((dims != 3 && dims != 4) || out.t->dim() != dims)
+        return not_taken();
+    const int64_t drafts = dims == 4 ? q.t->size(1) : 1, q_heads = q.t->size(dims - 2);
+    if (drafts < 1 || drafts > DETFOLD_MAX_DRAFTS || q_heads > INT32_MAX || q.t->size(dims - 1) != c.dim)
+        return not_taken();
+    const int64_t out_shape[4] = {batch, drafts, q_heads, c.v_dim}, one_shape[3] = {batch, q_heads, c.v_dim};
+    const c10::IntArrayRef shape = dims == 4 ? c10::IntArrayRef(out_shape, 4) : c10::IntArrayRef(one_shape, 3);
+    const c10::ScalarType type = q.t->scalar_type(), out_type = out.t->scalar_type();
+    a.type = type_of(type), a.out_type = type_of(out_type);
+    if (a.type < 0 || (out_type != type && out_type != c10::kFloat) || out.t->sizes() != shape || !lens.plain(dev, c10::kInt, {batch}) ||
+        !table_of(table, dev, batch) || !plain_or_none(lse, dev, c10::kFloat, shape.slice(0, dims - 1)) ||
+        !plain_or_none(masks, dev, c10::kLong, {batch, drafts}) || !plain_or_none(counts, dev, c10::kInt, {batch}) ||
+        !plain_or_none(depths, dev, c10::kInt, {batch, drafts}) || !plain_or_none(slopes, dev, c10::kFloat, {q_heads}))
+        return not_taken();
+    if (!workspace.t || workspace.t->get_device() != dev || !workspace.t->is_contiguous())
+        return not_taken();
+    a.out = out.written(), a.out_row = out.t->stride(0), a.out_head = out.t->stride(dims - 2);
+    a.q = q.read(), a.q_row = q.t->stride(0), a.q_head = q.t->stride(dims - 2);
+    t.q_draft = dims == 4 ? q.t->stride(1) : 0, t.out_draft = dims == 4 ? out.t->stride(1) : 0;
+    a.lse = lse.written<float>();
+    a.table = table.read<int32_t>(), a.table_row = table.t->stride(0), a.table_width = table.t->size(1);
+    a.lens = lens.read<int32_t>();
+    t.masks = masks.read<int64_t>(), t.counts = counts.read<int32_t>(), t.depths = depths.read<int32_t>(), t.slopes = slopes.read<float>();
+    a.workspace = workspace.written(), a.workspace_bytes = (int64_t)workspace.t->nbytes();
+    a.batch = batch, a.q_heads = (int32_t)q_heads, a.split = (int32_t)split;
+    t.drafts = (int32_t)drafts;
+    return PyLong_FromLong(unlocked(f, &c, &t, stream));
+}
+
+// (function, cache, device, stream, src, dst, tokens, into)
+PyObject *copy(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    detfold_paged_cache c, to;
+    Numbers num;
+    if (n != 8)
+        return not_taken();
+    const CopyFn f = (CopyFn)num.address(args[0]);
+    const int64_t dev = num.whole(args[2]);
+    const bool other = args[7] != Py_None;
+    if (!cache_of(args[1], dev, !other, &c) || (other && !cache_of(args[7], dev, true, &to)))
+        return not_taken();
+    if (other && (to.page != c.page || to.heads != c.heads || to.dim != c.dim || to.v_dim != c.v_dim || to.type != c.type))
+        return not_taken();
+    void *stream = num.address(args[3]);
+    const Arg src(args[4]), dst(args[5]), tokens(args[6]);
+    if (!num.ok || !src.t || src.t->dim() != 1)
+        return not_taken();
+    const int64_t count = src.t->size(0);
+    if (!src.plain(dev, c10::kInt, {count}) || !dst.plain(dev, c10::kInt, {count}) || !plain_or_none(tokens, dev, c10::kInt, {count}))
+        return not_taken();
+    return PyLong_FromLong(unlocked(f, &c, other ? &to : nullptr, src.read<int32_t>(), dst.read<int32_t>(), tokens.read<int32_t>(), count, stream));
+}
+
+// (function, cache, device, stream, table, picks, counts, starts, to)
+PyObject *compact(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    detfold_paged_cache c;
+    Numbers num;
+    if (n != 9)
+        return not_taken();
+    const CompactFn f = (CompactFn)num.address(args[0]);
+    const int64_t dev = num.whole(args[2]);
+    if (!cache_of(args[1], dev, true, &c))
+        return not_taken();
+    void *stream = num.address(args[3]);
+    const Arg table(args[4]), picks(args[5]), counts(args[6]), starts(args[7]), to(args[8]);
+    if (!num.ok || !picks.t || picks.t->dim() != 2)
+        return not_taken();
+    detfold_compact a = {};
+    a.batch = picks.t->size(0), a.most = picks.t->size(1);
+    if (!picks.plain(dev, c10::kInt, picks.t->sizes()) || !counts.plain(dev, c10::kInt, {a.batch}) ||
+        !plain_or_none(starts, dev, c10::kInt, {a.batch}) || !table_of(table, dev, a.batch))
+        return not_taken();
+    if (!to.none) {
+        if (!table_of(to, dev, a.batch) || to.t->numel() == 0)
+            return not_taken();
+        a.to = to.read<int32_t>(), a.to_row = to.t->stride(0), a.to_width = to.t->size(1);
+    }
+    a.table = table.read<int32_t>(), a.table_row = table.t->stride(0), a.table_width = table.t->size(1);
+    a.picks = picks.read<int32_t>(), a.counts = counts.read<int32_t>(), a.starts = starts.read<int32_t>();
+    return PyLong_FromLong(unlocked(f, &c, &a, stream));
+}
+
 // A call that lets no C++ exception into the interpreter, which would end the
 // process.  The library's functions are C and throw none, so nothing was done yet.
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
@@ -282,6 +419,9 @@ PyMethodDef methods[] = {
     {"append", (PyCFunction)(void (*)(void))guarded<append>, METH_FASTCALL, nullptr},
     {"attend", (PyCFunction)(void (*)(void))guarded<attend>, METH_FASTCALL, nullptr},
     {"fold", (PyCFunction)(void (*)(void))guarded<fold>, METH_FASTCALL, nullptr},
+    {"tree", (PyCFunction)(void (*)(void))guarded<tree>, METH_FASTCALL, nullptr},
+    {"copy", (PyCFunction)(void (*)(void))guarded<copy>, METH_FASTCALL, nullptr},
+    {"compact", (PyCFunction)(void (*)(void))guarded<compact>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,278 @@
+// draft.cpp -- the host side of the drafted step's operators: argument checks
+// and planning (no device access), and their C ABI.  Every check comes before
+// any HIP call, so an argument error never touches the device; nothing here
+// allocates, synchronizes or keeps a pointer.
+
+#include <cmath>
+#include <cstdint>
+
+#include "decode_check.h"
+#include "draft.h"
+#include "internal.h"
+
+namespace detfold_impl {
+namespace {
+
+constexpr int64_t kMaxPage = (int64_t)1 << 31;  // values of a page's keys or values that are copied
+
+// Whether a written [n0][n1][n2][last] buffer has no element twice: in the order
+// of the strides, each passes what lies within it.
+bool distinct3(int64_t (&d)[3][2], int64_t last)
+{
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (d[j][1] > d[j + 1][1]) {
+                const int64_t n = d[j][0], s = d[j][1];
+                d[j][0] = d[j + 1][0], d[j][1] = d[j + 1][1];
+                d[j + 1][0] = n, d[j + 1][1] = s;
+            }
+    int64_t inner = last;
+    for (const auto &x : d)
+        if (x[0] > 1) {
+            if (x[1] < inner)
+                return false;
+            inner += (x[0] - 1) * x[1];
+        }
+    return true;
+}
+
+int64_t span3(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t last)
+{
+    const int64_t d[3][2] = {{n0, s0}, {n1, s1}, {n2, s2}};
+    return span(d, 3, last);
+}
+
+bool same_cache(const detfold_paged_cache &a, const detfold_paged_cache &b)
+{
+    return a.k == b.k && a.v == b.v && a.pages == b.pages && a.k_page == b.k_page && a.k_token == b.k_token && a.k_head == b.k_head &&
+           a.v_page == b.v_page && a.v_token == b.v_token && a.v_head == b.v_head;
+}
+
+}  // namespace
+
+int check_tree(const detfold_paged_cache *c, const detfold_tree *t)
+{
+    int rc = check_cache(c);
+    if (rc != DETFOLD_OK)
+        return rc;
+    if (!t)
+        return DETFOLD_EINVAL;
+    const detfold_attend &a = t->attend;
+    if (a.reserved != 0 || !types_pair(a.type, c->type) || (a.out_type != a.type && a.out_type != DETFOLD_F32) || t->drafts < 1 ||
+        t->drafts > DETFOLD_MAX_DRAFTS || !(t->cap >= 0.0f) || !std::isfinite(t->cap))
+        return DETFOLD_EINVAL;
+    detfold_attend_plan p;  // checks the counts; the device's own plan follows
+    if ((rc = detfold_plan_tree(c, a.batch, t->drafts, a.q_heads, a.max_len, a.window, a.split, a.type, a.out_type, 1, &p)) != DETFOLD_OK)
+        return rc;
+    if (!std::isfinite(a.scale) || a.table_width < 0 || a.table_row < 0 || a.workspace_bytes < 0)
+        return DETFOLD_EINVAL;
+    if (t->masks && !t->depths && (a.window > 0 || t->slopes))
+        return DETFOLD_EINVAL;
+    if (a.batch == 0)
+        return DETFOLD_OK;
+    if (!a.out || !a.q || !a.lens || (a.table_width > 0 && !a.table))
+        return DETFOLD_EINVAL;
+    const int size = elem_size(a.type), out_size = elem_size(a.out_type);
+    const int64_t qs = span3(a.batch, a.q_row, t->drafts, t->q_draft, a.q_heads, a.q_head, c->dim);
+    const int64_t os = span3(a.batch, a.out_row, t->drafts, t->out_draft, a.q_heads, a.out_head, c->v_dim);
+    const int64_t ts = a.table_width > 0 ? span2(a.batch, a.table_row, 1, 0, a.table_width) : 0;
+    if (qs < 0 || os < 0 || ts < 0)
+        return DETFOLD_EINVAL;
+    if (!aligned(a.q, (uintptr_t)size) || !aligned(a.out, (uintptr_t)out_size) || !aligned(a.lse, 4) || !aligned(a.table, 4) ||
+        !aligned(a.lens, 4) || !aligned(a.workspace, 16) || !aligned(t->masks, 8) || !aligned(t->counts, 4) || !aligned(t->depths, 4) ||
+        !aligned(t->slopes, 4))
+        return DETFOLD_EINVAL;
+    int64_t dims[3][2] = {{a.batch, a.out_row}, {t->drafts, t->out_draft}, {a.q_heads, a.out_head}};
+    if (!distinct3(dims, c->v_dim))
+        return DETFOLD_EOVERLAP;
+    const int64_t queries = a.batch * t->drafts;
+    const Range out = range(a.out, os, out_size), lse = range(a.lse, queries * a.q_heads, 4);
+    const Range work = range(a.workspace, a.workspace_bytes, 1);
+    const Range in[] = {range(a.q, qs, size), range(a.table, ts, 4), range(a.lens, a.batch, 4), range(t->masks, queries, 8),
+                        range(t->counts, a.batch, 4), range(t->depths, queries, 4), range(t->slopes, a.q_heads, 4),
+                        cache_range(*c, false), cache_range(*c, true), range(c->k_scale, c->heads, 4), range(c->v_scale, c->heads, 4)};
+    for (const Range &r : in)
+        if (meet(out, r) || meet(lse, r) || meet(work, r))
+            return DETFOLD_EOVERLAP;
+    if (meet(out, lse) || meet(out, work) || meet(lse, work))
+        return DETFOLD_EOVERLAP;
+    return DETFOLD_OK;
+}
+
+int check_copy(const detfold_paged_cache *c, const detfold_paged_cache *into, const int32_t *src, const int32_t *dst,
+               const int32_t *tokens, int64_t count)
+{
+    int rc = check_cache(c);
+    if (rc != DETFOLD_OK || (into && (rc = check_cache(into)) != DETFOLD_OK))
+        return rc;
+    if (into && (into->page != c->page || into->heads != c->heads || into->dim != c->dim || into->v_dim != c->v_dim || into->type != c->type))
+        return DETFOLD_EINVAL;
+    if (count < 0 || count >= kMaxCount || c->page > kMaxPage / c->heads / (c->dim > c->v_dim ? c->dim : c->v_dim))
+        return DETFOLD_EINVAL;
+    if (count == 0)
+        return DETFOLD_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(tokens, 4))
+        return DETFOLD_EINVAL;
+    const Range from[] = {cache_range(*c, false), cache_range(*c, true)};
+    const detfold_paged_cache &w = into ? *into : *c;
+    const Range to[] = {cache_range(w, false), cache_range(w, true)};
+    const Range lists[] = {range(src, count, 4), range(dst, count, 4), range(tokens, count, 4)};
+    for (const Range &t : to) {
+        for (const Range &r : lists)
+            if (meet(t, r))
+                return DETFOLD_EOVERLAP;
+        if (into && !same_cache(*c, *into))
+            for (const Range &r : from)
+                if (meet(t, r))
+                    return DETFOLD_EOVERLAP;
+    }
+    return DETFOLD_OK;
+}
+
+int check_compact(const detfold_paged_cache *c, const detfold_compact *a)
+{
+    int rc = check_cache(c);
+    if (rc != DETFOLD_OK)
+        return rc;
+    if (!a || a->batch < 0 || a->batch >= kMaxCount || a->most < 0 || a->most >= kMaxCount || a->table_row < 0 || a->table_width < 0 ||
+        (a->to && (a->to_row < 0 || a->to_width < 0)))
+        return DETFOLD_EINVAL;
+    if (a->batch == 0 || a->most == 0)
+        return DETFOLD_OK;
+    if (!a->picks || !a->counts || (a->table_width > 0 && !a->table))
+        return DETFOLD_EINVAL;
+    for (const void *p : {a->table, a->to, a->picks, a->counts, a->starts})
+        if (!aligned(p, 4))
+            return DETFOLD_EINVAL;
+    const int64_t ts = a->table_width > 0 ? span2(a->batch, a->table_row, 1, 0, a->table_width) : 0;
+    const int64_t os = a->to && a->to_width > 0 ? span2(a->batch, a->to_row, 1, 0, a->to_width) : 0;
+    if (ts < 0 || os < 0 || a->most > kMaxElems / a->batch)
+        return DETFOLD_EINVAL;
+    const Range in[] = {range(a->table, ts, 4), range(a->to, os, 4), range(a->picks, a->batch * a->most, 4), range(a->counts, a->batch, 4),
+                        range(a->starts, a->batch, 4)};
+    const Range k = cache_range(*c, false), v = cache_range(*c, true);
+    for (const Range &r : in)
+        if (meet(k, r) || meet(v, r))
+            return DETFOLD_EOVERLAP;
+    return DETFOLD_OK;
+}
+
+namespace {
+
+int chunks_of(int64_t bytes) { return (int)((bytes + 15) / 16); }
+
+// The runs of bytes that a page's tokens make in both caches: heads that lie beside
+// each other are one run, and whole pages whose tokens do are one, too.
+CopyRuns runs_of(const detfold_paged_cache &c, const detfold_paged_cache &w, bool values, bool whole)
+{
+    const int64_t size = elem_size(c.type), dim = values ? c.v_dim : c.dim;
+    CopyRuns r = {};
+    r.from = (const char *)(values ? c.v : c.k), r.to = (char *)(values ? w.v : w.k);
+    r.from_page = size * (values ? c.v_page : c.k_page), r.to_page = size * (values ? w.v_page : w.k_page);
+    r.from_token = size * (values ? c.v_token : c.k_token), r.to_token = size * (values ? w.v_token : w.k_token);
+    r.from_head = size * (values ? c.v_head : c.k_head), r.to_head = size * (values ? w.v_head : w.k_head);
+    int64_t run = size * dim, heads = c.heads, tokens = c.page;
+    constexpr int64_t kMaxRun = (int64_t)1 << 30;
+    auto joins = [&](int64_t from, int64_t to, int64_t n) { return n == 1 || (from == run && to == run && run * n < kMaxRun); };
+    // Both orders: heads of a token beside each other, or tokens of a head.
+    for (int turn = 0; turn < 2; ++turn) {
+        if (heads > 1 && joins(r.from_head, r.to_head, heads))
+            run *= heads, heads = 1;
+        if (whole && tokens > 1 && joins(r.from_token, r.to_token, tokens))
+            run *= tokens, tokens = 1;
+    }
+    r.run = (int32_t)run;
+    r.chunks = divider((uint32_t)chunks_of(run));
+    r.heads = divider((uint32_t)heads);
+    r.page = divider(r.chunks.d * (uint32_t)heads * (uint32_t)tokens);
+    return r;
+}
+
+}  // namespace
+
+}  // namespace detfold_impl
+
+using namespace detfold_impl;
+
+// ---------------------------------------------------------------------------
+// C ABI
+
+extern "C" {
+
+int detfold_plan_tree(const detfold_paged_cache *cache, int64_t batch, int32_t drafts, int32_t q_heads, int64_t max_len,
+                      int64_t window, int32_t split, int32_t type, int32_t out_type, int32_t cu_count, detfold_attend_plan *plan)
+{
+    if (!plan || drafts < 1 || drafts > DETFOLD_MAX_DRAFTS)
+        return DETFOLD_EINVAL;
+    AttendPlan p;
+    int rc = check_cache(cache);
+    if (rc == DETFOLD_OK)
+        rc = plan_attend(*cache, batch, q_heads, max_len, window, split, false, cu_count, &p);
+    if (rc == DETFOLD_OK)
+        *plan = p, plan->workspace_bytes = plan->workspace_upto = 0;
+    return rc;
+}
+
+int detfold_tree_workspace(const detfold_paged_cache *cache, int64_t batch, int32_t drafts, int32_t q_heads, int64_t max_len,
+                           int32_t split, int64_t *bytes)
+{
+    if (!bytes)
+        return DETFOLD_EINVAL;
+    detfold_attend_plan p;
+    const int rc = detfold_plan_tree(cache, batch, drafts, q_heads, max_len, 0, split, DETFOLD_F32, DETFOLD_F32, 1, &p);
+    *bytes = p.workspace_upto;
+    return rc;
+}
+
+int detfold_attend_tree(const detfold_paged_cache *cache, const detfold_tree *args, void *stream)
+{
+    int rc = check_tree(cache, args);
+    if (rc != DETFOLD_OK || args->attend.batch == 0)
+        return rc;
+    TreeArgs k = {};
+    k.c = *cache;
+    k.a = args->attend;
+    k.masks = args->masks, k.counts = args->counts, k.depths = args->depths, k.slopes = args->slopes;
+    k.q_draft = args->q_draft, k.out_draft = args->out_draft;
+    k.window = k.a.window;
+    k.cap = args->cap;
+    k.drafts = args->drafts;
+    k.group = k.a.q_heads / cache->heads;
+    k.heads_of = divider((uint32_t)k.group);
+    k.page = divider((uint32_t)cache->page);
+    if (k.window > 0)
+        k.a.window += k.drafts - 1;
+    return launch_tree(k, stream);
+}
+
+int detfold_cache_copy(const detfold_paged_cache *cache, const detfold_paged_cache *into, const int32_t *src, const int32_t *dst,
+                       const int32_t *tokens, int64_t count, void *stream)
+{
+    const int rc = check_copy(cache, into, src, dst, tokens, count);
+    if (rc != DETFOLD_OK || count == 0)
+        return rc;
+    const detfold_paged_cache &w = into ? *into : *cache;
+    CopyArgs k = {};
+    k.k = runs_of(*cache, w, false, !tokens);
+    k.v = runs_of(*cache, w, true, !tokens);
+    k.src = src, k.dst = dst, k.tokens = tokens;
+    k.pages = cache->pages, k.into_pages = w.pages;
+    return launch_copy_pages(k, count, stream);
+}
+
+int detfold_cache_compact(const detfold_paged_cache *cache, const detfold_compact *args, void *stream)
+{
+    const int rc = check_compact(cache, args);
+    if (rc != DETFOLD_OK || args->batch == 0 || args->most == 0)
+        return rc;
+    CompactArgs k = {};
+    k.c = *cache;
+    k.a = *args;
+    k.page = divider((uint32_t)cache->page);
+    k.heads = divider((uint32_t)cache->heads);
+    k.k_chunks = divider((uint32_t)chunks_of((int64_t)cache->dim * elem_size(cache->type)));
+    k.v_chunks = divider((uint32_t)chunks_of((int64_t)cache->v_dim * elem_size(cache->type)));
+    return launch_compact(k, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,62 @@
+// draft.h -- declarations shared by the drafted step's operators: draft.cpp
+// (host-only checks and planning, and their C ABI), tree_kernels.hip with the
+// tree_*.hip instances of tree_kernel.h (the attention of drafted tokens) and
+// page_kernels.hip (copies and compaction of the cache).
+#ifndef DETFOLD_DRAFT_H
+#define DETFOLD_DRAFT_H
+
+#include "decode.h"
+
+namespace detfold_impl {
+
+// Kernel arguments of the attention of drafted tokens.  The base's window is
+// widened by the drafted tokens, so that a row's first seen token is one that
+// any of its queries may see; `window` is the caller's.
+struct TreeArgs : AttendArgs {
+    const int64_t *masks;
+    const int32_t *counts, *depths;
+    const float *slopes;
+    int64_t q_draft, out_draft, window;
+    float cap;
+    int32_t drafts;
+    Divider heads_of; // query heads of a key-value head
+};
+
+// Kernel arguments of the page copy: a page's tokens are `tokens` runs of `heads`
+// runs of bytes, in the keys and in the values, taken in chunks.
+struct CopyRuns {
+    const char *from;
+    char *to;
+    int64_t from_page, from_token, from_head, to_page, to_token, to_head;  // bytes
+    int32_t run;                 // bytes
+    Divider chunks, heads, page; // chunks of a run, runs of a token, chunks of a page
+};
+struct CopyArgs {
+    CopyRuns k, v;
+    const int32_t *src, *dst, *tokens;
+    int64_t pages, into_pages;
+    int64_t first;              // copy of the launch
+    uint32_t count, key_blocks; // copies of the launch, and its workgroups that take keys
+};
+
+struct CompactArgs {
+    detfold_paged_cache c;
+    detfold_compact a;
+    Divider page, heads, k_chunks, v_chunks; // chunks of a key's and a value's head
+    int64_t row0;
+};
+
+// --- draft.cpp: host only, no device access ----------------------------------
+int check_tree(const detfold_paged_cache *c, const detfold_tree *t);
+int check_copy(const detfold_paged_cache *c, const detfold_paged_cache *into, const int32_t *src, const int32_t *dst,
+               const int32_t *tokens, int64_t count);
+int check_compact(const detfold_paged_cache *c, const detfold_compact *a);
+
+// --- tree_kernels.hip, page_kernels.hip: launches -----------------------------
+int launch_tree(const TreeArgs &a, void *stream);
+int launch_copy_pages(const CopyArgs &a, int64_t count, void *stream);
+int launch_compact(const CompactArgs &a, void *stream);
+
+}  // namespace detfold_impl
+
+#endif  // DETFOLD_DRAFT_H

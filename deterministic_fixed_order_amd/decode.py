@@ -274,9 +274,10 @@ def _within(stream, dev: int):
     return torch.cuda.stream(torch.cuda.ExternalStream(int(stream.cuda_stream), device=dev))
 
 
-def attend_workspace(cache: PagedCache, batch: int, q_heads: int, max_len: int, *, split: int = 0):
+def attend_workspace(cache: PagedCache, batch: int, q_heads: int, max_len: int, *, split: int = 0, drafts: int = 1):
     """The device memory that ``attend_paged`` joins the parts of long rows in,
-    for calls whose batch and ``max_len`` are at most these (a uint8 tensor).
+    for calls whose batch and ``max_len`` are at most these (a uint8 tensor);
+    with ``drafts``, ``attend_tree`` too, for at most so many drafted tokens.
     Calls that overlap in time must not share one.  It is allocated on torch's
     current stream: for calls on another one, make it within that
     (``torch.cuda.stream``), or keep it until they are done."""
@@ -284,11 +285,17 @@ def attend_workspace(cache: PagedCache, batch: int, q_heads: int, max_len: int, 
     n = ctypes.c_int64()
     _check(_load().detfold_attend_workspace(cache._c, batch, q_heads, max_len, split, ctypes.byref(n)),
            "attend_workspace")
-    return torch.empty(n.value, dtype=torch.uint8, device=cache.k.device)
+    size = n.value if drafts == 1 else max(n.value, _draft()._workspace(cache, batch, drafts, q_heads, max_len, split))
+    return torch.empty(size, dtype=torch.uint8, device=cache.k.device)
+
+
+def _draft():
+    from . import draft
+    return draft
 
 
 def attend_paged(out, q, cache: PagedCache, table, lens, *, scale=None, window: int = 0, max_len=None, lse=None,
-                 workspace=None, split: int = 0, stream=None) -> None:
+                 workspace=None, split: int = 0, cap: float = 0.0, slopes=None, stream=None) -> None:
     """Attention of one new token per row: ``out`` [batch, q_heads, v_dim] and,
     where given, ``lse`` [batch, q_heads] (float32) of ``q`` [batch, q_heads,
     dim] over the first ``lens`` (int32) tokens of each row, whose pages
@@ -301,7 +308,12 @@ def attend_paged(out, q, cache: PagedCache, table, lens, *, scale=None, window: 
     ``out`` is of q's type or float32.  ``workspace`` is ``attend_workspace``'s
     (allocated for the call where it is missing).  ``split`` fixes the tokens
     of one part (a multiple of 32), so that a row's bits do not depend on the
-    batch around it."""
+    batch around it.
+
+    With ``cap`` > 0 a score s becomes cap * tanh(s / cap); then ``slopes``
+    (float32 [q_heads]) add slope * (t - (len - 1)) to the score of token t."""
+    if cap or slopes is not None:
+        return _draft().scored(out, q, cache, table, lens, cap, slopes, scale, window, max_len, lse, workspace, split, stream)
     dev = cache.device_index
     current, _, _, call, of = (_native or _bound())[:5]
     rc = call(of, cache, dev, current(dev) if stream is None else int(stream.cuda_stream), out, q, table, lens,

@@ -535,6 +535,107 @@ int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *
                          int32_t W, int64_t rows, int64_t dim, int64_t outs_pitch,
                          int64_t lses_pitch, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The drafted step: several new tokens of a row at once, of which some are kept.
+ *
+ * detfold_attend_tree -- attention of up to DETFOLD_MAX_DRAFTS drafted tokens
+ * per row over the cache, and of one token whose scores are capped or biased
+ * (drafts = 1).  The drafted tokens are the last ones of their row, appended
+ * before: with n = min(counts[b], drafts) of them the row's first
+ * base = max(lens[b] - n, 0) tokens are its prefix, and drafted token j is token
+ * base + j.  A token t of the prefix stands at position t, a drafted one at
+ * base + depths[b][j].  Drafted query i sees token t of the row if
+ *     t < base, or bit t - base of masks[b][i] is set,
+ * and, with window > 0, if its own position less t's is below `window`.  Of what
+ * it sees
+ *     s_t = scale * (q . k_t);  cap > 0: s_t = cap * tanh(s_t / cap);
+ *     s_t = s_t + slopes[g] * (position of t - position of i),
+ *     lse = log(sum_t exp(s_t)),  out = sum_t exp(s_t - lse) v_t.
+ * A query that sees no token gives 0 and -infinity.  Tokens that a query does
+ * not see are never part of its result, whatever they hold.  Queries from n on
+ * (the padding of a smaller tree) are not computed: their out and lse stay as
+ * they were.
+ *   attend    as detfold_attend_paged's arguments; q and out are [batch][drafts]
+ *             [q_heads][...], lse is [batch][drafts][q_heads]; lens count the
+ *             drafted tokens.  A length or page out of range gives NaN in that
+ *             row's out and lse
+ *   masks     device, int64 [batch][drafts], or NULL: a chain, whose token i sees
+ *             the drafted tokens 0 .. i.  A token sees itself only if its own bit
+ *             says so
+ *   counts    device, int32 [batch], or NULL: all are there (negative: none)
+ *   depths    device, int32 [batch][drafts], each taken as 0 .. 63, or NULL: i of
+ *             token i.  Needed with masks where there is a window or slopes
+ *   slopes    device, [q_heads] floats, or NULL
+ *   cap       0: none; else positive and finite
+ * Bits, splits and the workspace (detfold_tree_workspace) as of
+ * detfold_attend_paged.
+ * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP, DETFOLD_ESIZE, DETFOLD_EDEVICE,
+ * DETFOLD_ELAUNCH.
+ */
+#define DETFOLD_MAX_DRAFTS 64
+typedef struct detfold_tree {
+    detfold_attend attend;
+    const int64_t *masks;
+    const int32_t *counts, *depths;
+    const float *slopes;
+    int64_t q_draft, out_draft; /* elements from one drafted token to the next */
+    float cap;
+    int32_t drafts; /* 1 .. DETFOLD_MAX_DRAFTS */
+} detfold_tree;
+int detfold_attend_tree(const detfold_paged_cache *cache, const detfold_tree *args, void *stream);
+
+/* How such a call is split (host only), and workspace_upto of that plan, for
+ * queries of any type, on the current device. */
+int detfold_plan_tree(const detfold_paged_cache *cache, int64_t batch, int32_t drafts, int32_t q_heads,
+                      int64_t max_len, int64_t window, int32_t split, int32_t type, int32_t out_type,
+                      int32_t cu_count, detfold_attend_plan *plan);
+int detfold_tree_workspace(const detfold_paged_cache *cache, int64_t batch, int32_t drafts, int32_t q_heads,
+                           int64_t max_len, int32_t split, int64_t *bytes);
+
+/*
+ * detfold_cache_copy -- copy pages: page dst[i] of `into` becomes a byte copy of
+ * page src[i] of `cache`, keys and values, for each i below count (a request's
+ * fork, which copies its last page; a pool that is moved or closed up).
+ *   into    a cache of the same page size, heads, head sizes and type, whose pages
+ *           may lie in another order of memory; NULL: `cache` itself
+ *   src,    device, int32 [count].  A pair of which either page is not in its
+ *   dst     cache is left out (padding of a list)
+ *   tokens  device, int32 [count], or NULL: only the first tokens[i] slots of the
+ *           page are copied
+ * The copies run in no order: no page may be both written and read, or written
+ * twice, in one call.  Scales of 8-bit caches are not touched.  The keys of a
+ * page, and its values, are at most 2^31.
+ * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP (`into` shares memory with `cache`
+ * and is not it; a list lies in a cache), DETFOLD_ELAUNCH.
+ */
+int detfold_cache_copy(const detfold_paged_cache *cache, const detfold_paged_cache *into, const int32_t *src,
+                       const int32_t *dst, const int32_t *tokens, int64_t count, void *stream);
+
+/*
+ * detfold_cache_compact -- move the kept tokens of each row together: for each i
+ * below counts[b], token starts[b] + i of row b becomes what token
+ * starts[b] + picks[b][i] was, keys and values (the accepted path of a drafted
+ * tree; what stays of a prompt).
+ *   table   device, int32 [batch][table_width] at table_row: the rows' pages
+ *   to      device, int32 [batch][to_width] at to_row, or NULL.  NULL: in place,
+ *           as if all tokens were read before any is written; a pick below its own
+ *           i is then left out.  Else the moved tokens go to the pages that `to`
+ *           names, none of which may be read in this call
+ *   picks   device, int32 [batch][most]
+ *   counts  device, int32 [batch], each taken as 0 .. most
+ *   starts  device, int32 [batch], or NULL: 0
+ * A move from or to a token that the table, or the cache, does not have is left
+ * out.  A page that is written may be one row's only, and there once.
+ * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP (an array lies in the cache),
+ * DETFOLD_ELAUNCH.
+ */
+typedef struct detfold_compact {
+    const int32_t *table, *to, *picks, *counts, *starts;
+    int64_t batch, most;
+    int64_t table_row, table_width, to_row, to_width; /* entries */
+} detfold_compact;
+int detfold_cache_compact(const detfold_paged_cache *cache, const detfold_compact *args, void *stream);
+
 /* Static, NUL-terminated description of a return code (never NULL). */
 const char *detfold_strerror(int rc);
 
