@@ -7,8 +7,9 @@ operators cache_kernels.hip and attend_kernels.hip (device code and launches),
 attend_f32.hip, attend_f16.hip and attend_bf16.hip (the instances of
 attend_kernel.h), decode.cpp (checks, planning and the C ABI), decode.h,
 decode_check.h and decode_device.h; of the drafted step's tree_kernels.hip and
-page_kernels.hip (device code and launches), draft.cpp (checks, planning and the
-C ABI) and draft.h; and bind.cpp, the C++ side of both modules' calls, a library
+page_kernels.hip (device code and launches), tree_f32.hip, tree_f16.hip and
+tree_bf16.hip (the instances of tree_kernel.h), draft.cpp (checks, planning and
+the C ABI) and draft.h; and bind.cpp, the C++ side of both modules' calls, a library
 of its own.
 exports.map limits the exported symbols to the C ABI of include/detfold.h.
 
@@ -52,8 +53,9 @@ SOURCES = [KERNELS] + HOST_SOURCES
 INTERNAL_HEADER = os.path.join(CSRC, "internal.h")
 DECODE_KERNELS = [os.path.join(CSRC, f) for f in ("cache_kernels.hip", "attend_kernels.hip", "attend_f32.hip",
                                                      "attend_f16.hip", "attend_bf16.hip")]
-DRAFT_KERNELS = [os.path.join(CSRC, f) for f in ("tree_kernels.hip", "page_kernels.hip")]
-DRAFT_SOURCES = DRAFT_KERNELS + [os.path.join(CSRC, f) for f in ("draft.cpp", "draft.h")]
+DRAFT_KERNELS = [os.path.join(CSRC, f) for f in ("tree_kernels.hip", "page_kernels.hip", "tree_f32.hip", "tree_f16.hip",
+                                                     "tree_bf16.hip")]
+DRAFT_SOURCES = DRAFT_KERNELS + [os.path.join(CSRC, f) for f in ("draft.cpp", "draft.h", "tree_kernel.h")]
 DECODE_SOURCES = DECODE_KERNELS + [os.path.join(CSRC, f) for f in ("decode.cpp", "decode.h", "decode_check.h", "decode_device.h",
                                                                  "attend_kernel.h", "bind.cpp")]
 BINDING = os.path.join(CSRC, "bind.cpp")
@@ -143,7 +145,7 @@ def _host_object(src: str, work: str, extra: list[str]) -> str:
 
 
 def _objects(work: str, extra: list[str]) -> list[str]:
-    kernels = DECODE_KERNELS[::-1] + DRAFT_KERNELS + [KERNELS]
+    kernels = DRAFT_KERNELS[::-1] + DECODE_KERNELS[::-1] + [KERNELS]
     hosts = HOST_SOURCES + [s for s in DECODE_SOURCES + DRAFT_SOURCES if s.endswith(".cpp") and s != BINDING]
     with ThreadPoolExecutor(max_workers=min(6, os.cpu_count() or 1)) as pool:
         jobs = [pool.submit(_kernel_object, s, work, extra) for s in kernels]

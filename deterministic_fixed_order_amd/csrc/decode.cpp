@@ -12,15 +12,6 @@
 namespace detfold_impl {
 namespace {
 
-constexpr int64_t kWavesPerCu = 8;                // of the attention, resident
-constexpr int64_t kShortRow = 512;                // tokens that are not worth cutting where rows fill the device
-// Of the cache, read in a step of 64 tokens: with less, or with products in
-// float32 from narrower values, a compute unit takes 8 waves instead of 4 (heads
-// of 64 bfloat16 27.7 us instead of 28.3; bfloat16 to float32 194 instead of 230).
-constexpr int64_t kStepBytes = 32768;
-constexpr int64_t kMaxEven = 4096;                // rows that every workgroup adds up the lengths of
-constexpr int64_t kLongPart = 8192;               // tokens of a part where there are more rows
-constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // workgroups of a launch, well below what a grid takes
 
 // A view [tokens][heads][dim], in elements.
 struct Heads {

@@ -1,5 +1,5 @@
 // decode_check.h -- what the host checks of the decode-step operators share:
-// limits, alignment, the extents of strided buffers and whether two meet.
+// limits, what plans go by, alignment, the extents of strided buffers and whether two meet.
 // Host only; nothing here touches the device.
 #ifndef DETFOLD_DECODE_CHECK_H
 #define DETFOLD_DECODE_CHECK_H
@@ -14,6 +14,17 @@ namespace detfold_impl {
 constexpr int64_t kMaxCount = (int64_t)1 << 31;   // counts that the kernels hold in 32 bits
 constexpr int64_t kMaxElems = (int64_t)1 << 46;   // extent of one buffer, in elements
 constexpr int32_t kMaxHeads = 1 << 16;
+
+// What the plans of the attention go by.
+constexpr int64_t kWavesPerCu = 8;                // of the attention, resident
+constexpr int64_t kShortRow = 512;                // tokens that are not worth cutting where rows fill the device
+// Of the cache, read in a step of 64 tokens: with less, or with products in
+// float32 from narrower values, a compute unit takes 8 waves instead of 4 (heads
+// of 64 bfloat16 27.7 us instead of 28.3; bfloat16 to float32 194 instead of 230).
+constexpr int64_t kStepBytes = 32768;
+constexpr int64_t kMaxEven = 4096;                // rows that every workgroup adds up the lengths of
+constexpr int64_t kLongPart = 8192;               // tokens of a part where there are more rows
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // workgroups of a launch, well below what a grid takes
 
 inline bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 

@@ -50,6 +50,86 @@ bool same_cache(const detfold_paged_cache &a, const detfold_paged_cache &b)
 
 }  // namespace
 
+namespace {
+
+// Tiles of 16 queries to a wave: as many as a key-value head has, where the products
+// are of 16 bits and the sums leave the registers room, which of heads above 128 two
+// do.  Products in float32, and in parts, are what bounds one tile already.  One
+// token a row is split as attend_paged splits it, in the same workspace.
+int tiles_of(int64_t cols, int32_t drafts, int wide_head, bool narrow)
+{
+    return !narrow || drafts == 1 || cols <= 16 ? 1 : cols <= 32 || wide_head == 256 ? 2 : 4;
+}
+
+}  // namespace
+
+// What plan_attend does, with up to 64 queries of a key-value head to a unit.
+int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32_t q_heads, int64_t max_len, int64_t window, int32_t split,
+              int32_t type, int32_t out_type, int32_t cu_count, TreePlan *p)
+{
+    AttendPlan checked;
+    const int rc = plan_attend(c, batch, q_heads, max_len, window, split, false, cu_count, &checked);
+    if (rc != DETFOLD_OK)
+        return rc;
+    if (drafts < 1 || drafts > DETFOLD_MAX_DRAFTS || max_len > kMaxCount - 1 - DETFOLD_MAX_DRAFTS || !types_pair(type, c.type) ||
+        (out_type != type && out_type != DETFOLD_F32))
+        return DETFOLD_EINVAL;
+    const int64_t cols = (int64_t)drafts * (q_heads / c.heads);
+    const int head = c.dim > c.v_dim ? c.dim : c.v_dim, wide_head = head <= 64 ? 64 : head <= 128 ? 128 : 256;
+    const int tiles = tiles_of(cols, drafts, wide_head, type != DETFOLD_F32 && out_type != DETFOLD_F32);
+    const int64_t units = c.heads * ((cols + 16 * tiles - 1) / (16 * tiles));
+    const int64_t queries = c.heads * (cols > 32 ? (cols + 63) / 64 * 64 : (cols + 15) / 16 * 16);  // at least units times a slot's
+    if (batch > 0 && queries > kMaxElems / 16 / batch)
+        return DETFOLD_EINVAL;
+    const int64_t seen = window > 0 && window < max_len - (drafts - 1) ? window + drafts - 1 : max_len;
+    const int64_t per_cu = tree_heavy(tiles, wide_head) ? kWavesPerCu / 2 : kWavesPerCu, full = cu_count, waves = full * per_cu;
+    p->tiles_of = tiles;
+    p->slot_cols = (int32_t)(cols < 16 * tiles ? cols : 16 * tiles);
+    p->units = batch * units;
+    p->shares = 0;
+    p->waves = (int32_t)per_cu;
+    p->beside = units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
+    p->brief = seen <= 32;
+    const int64_t groups = units / p->beside;
+    const int fit = 1024 / (wide_head * elem_size(c.type)), most_tiles = tiles > 1 || wide_head == 256 ? 2 : 4;
+    const int64_t few = 3 * 16 * (fit < most_tiles ? fit : most_tiles) * (4 / p->beside);
+    int64_t part = split > 0 ? split : kLongPart;
+    if (split == 0) {
+        if (seen <= few || (batch * groups >= full && seen <= kShortRow)) {
+            part = seen;
+        } else if (batch > 0 && batch * ((seen + 31) / 32) <= waves / units) {
+            part = DETFOLD_ATTEND_STEP;
+            p->brief = true;
+            p->waves = p->beside;
+        } else if (batch > 0 && groups <= full / 2 && batch <= kMaxEven && batch * (seen / 32 + 2) < kMaxCount / 2) {
+            p->shares = full / groups;
+            const int64_t even = (batch * seen + p->shares - 1) / p->shares, half = (seen + 1) / 2;
+            part = even < half ? even : half;
+        } else if (batch > 0 && seen > kMaxBlocks / p->units * part) {
+            part = (seen - 1) / (kMaxBlocks / p->units + 1) + 1;
+        }
+        part = (part + DETFOLD_ATTEND_STEP - 1) / DETFOLD_ATTEND_STEP * DETFOLD_ATTEND_STEP + (part == 0) * DETFOLD_ATTEND_STEP;
+    }
+    p->splits = seen > part ? (seen + part - 1) / part : 1;
+    p->split = p->splits > 1 ? part : seen;
+    // A part leaves v_dim sums, its maximum and its sum of weights per query.
+    // Shares and short parts leave no more than the device holds queries of at once,
+    // twice, whatever the rows; parts of a fixed length as many as the rows have.
+    const int64_t each = ((int64_t)c.v_dim + 2) * 4, least = split > 0 ? split : kLongPart, most = (max_len + least - 1) / least;
+    p->slots = p->shares ? 2 * p->shares * units : p->splits > 1 ? p->units * p->splits : 0;
+    p->workspace_bytes = batch > 0 ? p->slots * p->slot_cols * each + p->shares * 12 : 0;
+    if (split > 0 && most > 0 && batch > 0 && queries * batch > kMaxElems / most)
+        return DETFOLD_EINVAL;
+    int64_t upto = most > 1 ? (most < kMaxBlocks ? most : kMaxBlocks) * queries * batch : 0;
+    if (split == 0) {
+        const int64_t capped = kMaxBlocks * 64 + 2 * queries * batch, even = kWavesPerCu * cu_count * (cols < 64 ? cols : 64);
+        upto = upto > capped ? capped : upto;
+        upto = upto > even ? upto : even;
+    }
+    p->workspace_upto = batch > 0 && max_len > (split > 0 ? split : DETFOLD_ATTEND_STEP) ? upto * each + full * 12 : 0;
+    return DETFOLD_OK;
+}
+
 int check_tree(const detfold_paged_cache *c, const detfold_tree *t)
 {
     int rc = check_cache(c);
@@ -59,10 +139,10 @@ int check_tree(const detfold_paged_cache *c, const detfold_tree *t)
         return DETFOLD_EINVAL;
     const detfold_attend &a = t->attend;
     if (a.reserved != 0 || !types_pair(a.type, c->type) || (a.out_type != a.type && a.out_type != DETFOLD_F32) || t->drafts < 1 ||
-        t->drafts > DETFOLD_MAX_DRAFTS || !(t->cap >= 0.0f) || !std::isfinite(t->cap))
+        t->drafts > DETFOLD_MAX_DRAFTS || !(t->cap == 0.0f || std::isnormal(t->cap)) || t->cap < 0.0f)
         return DETFOLD_EINVAL;
-    detfold_attend_plan p;  // checks the counts; the device's own plan follows
-    if ((rc = detfold_plan_tree(c, a.batch, t->drafts, a.q_heads, a.max_len, a.window, a.split, a.type, a.out_type, 1, &p)) != DETFOLD_OK)
+    TreePlan p;  // checks the counts; the device's own plan follows
+    if ((rc = plan_tree(*c, a.batch, t->drafts, a.q_heads, a.max_len, a.window, a.split, a.type, a.out_type, 1, &p)) != DETFOLD_OK)
         return rc;
     if (!std::isfinite(a.scale) || a.table_width < 0 || a.table_row < 0 || a.workspace_bytes < 0)
         return DETFOLD_EINVAL;
@@ -204,12 +284,12 @@ int detfold_plan_tree(const detfold_paged_cache *cache, int64_t batch, int32_t d
 {
     if (!plan || drafts < 1 || drafts > DETFOLD_MAX_DRAFTS)
         return DETFOLD_EINVAL;
-    AttendPlan p;
+    TreePlan p;
     int rc = check_cache(cache);
     if (rc == DETFOLD_OK)
-        rc = plan_attend(*cache, batch, q_heads, max_len, window, split, false, cu_count, &p);
+        rc = plan_tree(*cache, batch, drafts, q_heads, max_len, window, split, type, out_type, cu_count, &p);
     if (rc == DETFOLD_OK)
-        *plan = p, plan->workspace_bytes = plan->workspace_upto = 0;
+        *plan = p;
     return rc;
 }
 
@@ -219,7 +299,15 @@ int detfold_tree_workspace(const detfold_paged_cache *cache, int64_t batch, int3
     if (!bytes)
         return DETFOLD_EINVAL;
     detfold_attend_plan p;
-    const int rc = detfold_plan_tree(cache, batch, drafts, q_heads, max_len, 0, split, DETFOLD_F32, DETFOLD_F32, 1, &p);
+    // What any type of query needs: float32 goes with every cache but of float16.
+    const int32_t type = cache && cache->type == DETFOLD_F16 ? DETFOLD_F16 : DETFOLD_F32;
+    int rc = detfold_plan_tree(cache, batch, drafts, q_heads, max_len, 0, split, type, type, 1, &p);
+    if (rc != DETFOLD_OK)
+        return rc;
+    int32_t cu = 0;
+    if ((rc = current_cu_count(&cu)) != DETFOLD_OK)
+        return rc;
+    rc = detfold_plan_tree(cache, batch, drafts, q_heads, max_len, 0, split, type, type, cu, &p);
     *bytes = p.workspace_upto;
     return rc;
 }
@@ -229,19 +317,48 @@ int detfold_attend_tree(const detfold_paged_cache *cache, const detfold_tree *ar
     int rc = check_tree(cache, args);
     if (rc != DETFOLD_OK || args->attend.batch == 0)
         return rc;
+    int32_t cu = 0;
+    if ((rc = current_cu_count(&cu)) != DETFOLD_OK)
+        return rc;
+    const detfold_attend &a = args->attend;
+    TreePlan p;
+    if ((rc = plan_tree(*cache, a.batch, args->drafts, a.q_heads, a.max_len, a.window, a.split, a.type, a.out_type, cu, &p)) != DETFOLD_OK)
+        return rc;
+    const int64_t units = p.units / a.batch;
+    if (units / p.beside * p.splits > kMaxBlocks)
+        return DETFOLD_EINVAL;
+    if (p.workspace_bytes > 0 && (!a.workspace || a.workspace_bytes < p.workspace_bytes))
+        return DETFOLD_ESIZE;
     TreeArgs k = {};
     k.c = *cache;
-    k.a = args->attend;
+    k.a = a;
     k.masks = args->masks, k.counts = args->counts, k.depths = args->depths, k.slopes = args->slopes;
     k.q_draft = args->q_draft, k.out_draft = args->out_draft;
-    k.window = k.a.window;
+    k.window = a.window;
+    if (a.window > 0)
+        k.a.window = (a.window < kMaxCount ? a.window : kMaxCount) + args->drafts - 1;
     k.cap = args->cap;
     k.drafts = args->drafts;
-    k.group = k.a.q_heads / cache->heads;
+    k.group = a.q_heads / cache->heads;
     k.heads_of = divider((uint32_t)k.group);
     k.page = divider((uint32_t)cache->page);
-    if (k.window > 0)
-        k.a.window += k.drafts - 1;
+    k.tiles_of = p.tiles_of;
+    k.slot_cols = p.slot_cols;
+    k.tiles = divider((uint32_t)(units / cache->heads));
+    k.beside = p.beside;
+    k.units = divider((uint32_t)(units / p.beside));
+    k.parts = divider((uint32_t)(p.shares ? 1 : p.splits));
+    k.shares = p.shares ? divider((uint32_t)p.shares) : Divider{0, 0, 0};
+    k.brief = p.brief;
+    k.split = p.split;
+    k.tiled = attend_tiled(*cache);
+    k.keep = attend_keep(*cache, k.tiles.d, k.brief);
+    k.waves = p.waves;
+    const int64_t queries = p.slots * p.slot_cols;
+    k.ml = (float2 *)a.workspace;
+    k.acc = (float *)(k.ml + queries);
+    k.cut = (int3 *)(k.acc + queries * cache->v_dim);
+    k.by_row = a.batch <= p.shares;
     return launch_tree(k, stream);
 }
 

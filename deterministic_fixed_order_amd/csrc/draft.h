@@ -19,7 +19,30 @@ struct TreeArgs : AttendArgs {
     int64_t q_draft, out_draft, window;
     float cap;
     int32_t drafts;
-    Divider heads_of; // query heads of a key-value head
+    int32_t tiles_of;    // tiles of 16 queries of a unit
+    int32_t slot_cols;   // queries of a slot, see AttendArgs
+    Divider heads_of;    // query heads of a key-value head
+    Divider join_blocks; // workgroups of the join for a row's queries
+};
+
+// Whether the sums and a step of so many tiles of queries and of heads of so many
+// dims leave a compute unit's registers four waves, not eight.
+constexpr bool tree_heavy(int tiles, int head) { return tiles * head > 256 || head > 128; }
+
+// A kernel of the attention of drafted tokens and the LDS it takes: for a unit's
+// queries, and for a wave's sums.
+struct TreeKernel {
+    const void *f;
+    int unit_bytes, wave_bytes;
+};
+TreeKernel tree_bf16(const TreeArgs &a);
+TreeKernel tree_f16(const TreeArgs &a);
+TreeKernel tree_f32(const TreeArgs &a);
+
+struct TreePlan : detfold_attend_plan {
+    int64_t shares, slots;
+    int32_t waves, beside, tiles_of, slot_cols;
+    bool brief;
 };
 
 // Kernel arguments of the page copy: a page's tokens are `tokens` runs of `heads`
@@ -47,6 +70,8 @@ struct CompactArgs {
 };
 
 // --- draft.cpp: host only, no device access ----------------------------------
+int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32_t q_heads, int64_t max_len, int64_t window, int32_t split,
+              int32_t type, int32_t out_type, int32_t cu_count, TreePlan *p);
 int check_tree(const detfold_paged_cache *c, const detfold_tree *t);
 int check_copy(const detfold_paged_cache *c, const detfold_paged_cache *into, const int32_t *src, const int32_t *dst,
                const int32_t *tokens, int64_t count);

@@ -1,0 +1,659 @@
+// tree_kernel.h -- the kernel of the attention of drafted tokens: up to 64 new
+// tokens per row over a paged key-value cache, each seeing the row's prefix and
+// its own branch.  Included by the tree_*.hip files, each of which instantiates
+// the kernels of one query type.
+//
+// Mathematics and layouts as in attend_kernel.h.  The columns of both products are
+// a key-value head's queries, drafted token by drafted token, 16 * QT of them to a
+// wave, so that what is loaded of the cache serves QT products.  A capped score is
+// cap * tanh(s / cap); a biased one gets slope * (position of the token - position
+// of the query); what a query does not see scores -infinity.  Only steps that hold
+// drafted tokens, or tokens at the window's edge, look at masks.
+#ifndef DETFOLD_TREE_KERNEL_H
+#define DETFOLD_TREE_KERNEL_H
+
+#include "attend_kernel.h"
+#include "draft.h"
+
+namespace detfold_impl {
+
+typedef const __attribute__((address_space(4))) TreeArgs *TreeArgsPtr;
+__device__ __forceinline__ const TreeArgs &tree_arguments()
+{
+    uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const TreeArgs *)(TreeArgsPtr)p;
+}
+
+// tanh(x), to 24 units in the last place (tested over all magnitudes): the [7/6]
+// fraction of its continued fraction below 1.5, off by 2^-25 there; above, from
+// exp(-2 |x|), whose rounding is at most a tenth of the result.
+__device__ __forceinline__ float tanh_near(float x)
+{
+    const float z = x * x;
+    const float over = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 1.0f, 378.0f), z, 17325.0f), z, 135135.0f);
+    const float under = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 28.0f, 3150.0f), z, 62370.0f), z, 135135.0f);
+    return x * over * __builtin_amdgcn_rcpf(under);
+}
+__device__ __forceinline__ float tanh_far(float x)
+{
+    const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * (-2.0f * kLog2e));
+    return __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), x);
+}
+constexpr float kTanhNear = 1.5f;
+
+// What a query of a column goes by.
+struct Column {
+    uint64_t mask;
+    int32_t at;  // its position
+    float slope;
+};
+
+// Whether a word of the cache holds a value that is no number or infinite.
+template <typename C> __device__ __forceinline__ bool odd_word(uint32_t w)
+{
+    if constexpr (sizeof(C) == 4) {
+        return (~w & 0x7f800000u) == 0;
+    } else if constexpr (sizeof(C) == 1) {
+        const uint32_t x = ~w & 0x7f7f7f7fu;  // a byte of zero
+        return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
+    } else {
+        const uint32_t x = ~w & (__is_same(C, bf16) ? 0x7f807f80u : 0x7c007c00u);
+        return (x & 0xffffu) == 0 || (x >> 16) == 0;
+    }
+}
+
+// A word of the cache with zeros in the place of such values.
+template <typename C> __device__ __forceinline__ uint32_t finite_word(uint32_t w)
+{
+    if constexpr (sizeof(C) == 4) {
+        return odd_word<C>(w) ? 0u : w;
+    } else if constexpr (sizeof(C) == 2) {
+        constexpr uint32_t top = __is_same(C, bf16) ? 0x7f80u : 0x7c00u;
+        return ((w & top) == top ? 0u : w & 0xffffu) | ((w >> 16 & top) == top ? 0u : w & 0xffff0000u);
+    } else {
+        uint32_t r = 0;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+            r |= (w >> i & 0x7f) == 0x7f ? 0u : w & 0xffu << i;
+        return r;
+    }
+}
+
+template <typename C, int QK, int PV, int D, bool TILED, int QT, int MOST, int KEEP>
+__global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs)
+{
+    typedef Attend<C, QK, PV, D, TILED, MOST, KEEP> S;
+    constexpr int CS = S::kSize, E = S::kChunk, NC = S::kChunks, UT = S::kTiles, VW = S::kWide, NP = S::kParts, NT = S::kTokens;
+    constexpr int COLS = 16 * QT;
+    extern __shared__ __align__(16) char lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const TreeArgs &p0 = tree_arguments();
+    const uint32_t y = divide(blockIdx.x, p0.units);
+    // A wave takes one of the workgroup's units, or one of several turns at it.
+    const int beside = p0.beside, in = wave & (beside - 1), turn = wave / beside, turns = waves / beside;
+    const uint32_t unit = (blockIdx.x - y * p0.units.d) * beside + in;
+
+    int64_t b;
+    uint32_t part = 0;
+    Share mine = {};
+    if (p0.shares.d) {
+        mine = find_share(p0, y, TILED);
+        if (mine.left == 0) {
+            if (!p0.by_row && unit == 0 && threadIdx.x == 0)
+                p0.cut[y] = make_int3(-1, 0, 0);
+            return;
+        }
+        b = mine.row;
+    } else {
+        const uint32_t row = divide(y, p0.parts);
+        part = y - row * p0.parts.d;
+        b = p0.row0 + row;
+        mine.len = scalar_load(p0.a.lens + b);
+    }
+
+    for (;;) {
+        const TreeArgs &p = tree_arguments();
+        const detfold_attend &a = p.a;
+        const detfold_paged_cache &c = p.c;
+        const int lane = anew((int)threadIdx.x & 63), col = lane & 15, grp = lane >> 4;
+        const uint32_t h = divide(unit, p.tiles), tile = unit - h * p.tiles.d;
+        const int drafted = min(max(p.counts ? scalar_load(p.counts + b) : p.drafts, 0), p.drafts);
+        const int col0 = (int)tile * COLS, live = min(max(drafted * p.group - col0, 0), COLS);
+        const char *k0 = (const char *)c.k + (int64_t)h * c.k_head * CS, *v0 = (const char *)c.v + (int64_t)h * c.v_head * CS;
+        const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
+        const uint32_t pages = (uint32_t)c.pages;
+        const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f);
+        const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
+
+        // Where a lane's loads lie within a key and a value.
+        uint32_t k_at[NC], v_at[NP];
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            k_at[i] = (uint32_t)min(E * (4 * i + grp), c.dim - E) * CS + (TILED ? col * (uint32_t)k_token : 0);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            v_at[i] = (uint32_t)min(VW * (16 * i + col), c.v_dim - VW) * CS + (TILED ? 4 * grp * (uint32_t)v_token : 0);
+
+        const RowTokens row = row_tokens(p, mine.len, TILED);
+        bool bad = row.bad;
+        uint32_t begin = row.begin, end = row.end, done = 0;
+        const int32_t base = max((int32_t)row.end - drafted, 0);  // tokens of the prefix
+        int64_t slot = -1;  // where the sums of this part go if the row has others
+        if (p.shares.d) {
+            const uint32_t x = mine.at - mine.row_at;
+            done = min(row.units - x, mine.left);
+            if (done < row.units)
+                slot = ((int64_t)y * (p.units.d * beside) + unit) * 2 + (x == 0);
+            if (unit == 0 && lane == 0 && turn == 0 && (p.by_row ? x == 0 : done == mine.left)) {
+                const bool cut = x == 0 && done < row.units;  // it begins here, and does not end here
+                p.cut[p.by_row ? b : y] = make_int3(cut ? (int)b : -1, (int)y, cut ? (int)((mine.at + row.units - 1) / mine.each) : 0);
+            }
+            end = x + done < row.units ? row.a0 + kUnit * (x + done) : end;
+            begin = x ? row.a0 + kUnit * x : begin;
+        } else if (p.parts.d > 1) {
+            slot = (b * p.parts.d + part) * (p.units.d * beside) + unit;
+            const int64_t x = begin + part * p.split;
+            begin = (uint32_t)min(x, (int64_t)end), end = (uint32_t)min(x + p.split, (int64_t)end);
+        }
+        const uint32_t a0 = TILED ? begin & ~15u : begin, last = end > 0 ? end - 1 : 0;
+        const uint32_t steps = end > begin && live > 0 ? (end - a0 + S::kStep - 1) / S::kStep : 0;
+        // Tokens below `low` are behind some query's window; a distance of `window` hides.
+        const int32_t window = p.window > 0 ? (int32_t)min(p.window, (int64_t)INT32_MAX) : INT32_MAX;
+        const int32_t low = p.window > 0 ? (int32_t)max((int64_t)base + (p.depths ? DETFOLD_MAX_DRAFTS : p.drafts) - window, (int64_t)0) : 0;
+
+        // The columns, and the drafted tokens' depths, which all waves share.
+        char *const queries = lds + in * (QT * S::kQ);
+        Column *const columns = (Column *)(lds + beside * (QT * S::kQ)) + in * COLS;
+        int32_t *const depths = (int32_t *)(lds + beside * (QT * S::kQ + COLS * (int)sizeof(Column)));
+        auto depth = [&](int j) { return p.depths ? min(max(p.depths[b * p.drafts + j], 0), DETFOLD_MAX_DRAFTS - 1) : j; };
+        if (turn == 0 && lane < live) {
+            const int i = (int)divide((uint32_t)(col0 + lane), p.heads_of);
+            Column x;
+            x.mask = p.masks ? (uint64_t)p.masks[b * p.drafts + i] : ~0ull >> (63 - i);
+            x.at = base + depth(i);
+            x.slope = p.slopes ? p.slopes[h * p.group + (col0 + lane - i * p.group)] : 0.0f;
+            columns[lane] = x;
+        }
+        if (wave == 0)
+            depths[lane] = lane < drafted ? depth(lane) : 0;
+
+        // The queries as the operand of the score products, one lane's 16 bytes
+        // after the other; a chunk that would pass the head's end starts earlier,
+        // and what it repeats counts as zero.
+        constexpr int QS = QK == kF32 || QK == kSplit ? 4 : 2, PER = QK == kF32 ? 4 : 8, NQ = D / (4 * PER);
+        auto query_chunk = [&](int i) { return E * (4 * (i * PER / E) + grp); };
+        Words<PER * QS> qw[QT][NQ] = {};
+#pragma unroll
+        for (int n = 0; n < QT; ++n) {
+            const int x = col0 + min(16 * n + col, max(live - 1, 0)), i = (int)divide((uint32_t)x, p.heads_of);
+            const char *q = (const char *)a.q + (b * a.q_row + i * p.q_draft + ((int64_t)h * p.group + (x - i * p.group)) * a.q_head) * QS;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+                if (live > 0 && ((n * NQ + i) & (turns - 1)) == turn)
+                    __builtin_memcpy(&qw[n][i], q + (min(query_chunk(i), c.dim - E) + i * PER % E) * QS, PER * QS);
+        }
+
+        const int32_t *table = a.table + b * a.table_row;
+        // The pages of a step's tokens, looked up two steps ahead of the products.
+        constexpr int IDS = TILED ? UT : 1;
+        const uint32_t own = lane & (S::kStep - 1);
+        struct Pages {
+            int32_t id[IDS];
+            uint32_t off[IDS];
+        };
+        auto look_up = [&](uint32_t s) {
+            const uint32_t t0 = a0 + s * S::kStep;
+            Pages g;
+#pragma unroll
+            for (int u = 0; u < IDS; ++u) {
+                const uint32_t t = TILED ? min(t0 + 16 * u, last & ~15u) : min(t0 + own, last), n = divide(t, p.page);
+                g.id[u] = TILED ? scalar_load(table + n) : table[n];
+                g.off[u] = t - n * p.page.d;
+            }
+            return g;
+        };
+        auto valid = [&](int32_t id) {  // the page, 0 for one that is none
+            const bool no = (uint32_t)id >= pages;
+            bad |= no;
+            return (int64_t)(no ? 0 : id);
+        };
+
+        Words<16> kw[UT][NC];
+        Words<VW * CS> vw[NT][NP];
+        auto load_keys = [&](const Pages &g) {
+            int64_t at = 0;
+            if (!TILED)
+                at = valid(g.id[0]) * k_page + g.off[0] * k_token;
+#pragma unroll
+            for (int u = 0; u < UT; ++u) {
+                const char *k = k0 + (TILED ? valid(g.id[u % IDS]) * k_page + g.off[u % IDS] * k_token : from_lane(at, 16 * u + col));
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    kw[u][i] = load_words<16, KEEP == kNothing>(k + anew(k_at[i]));
+            }
+        };
+        auto load_values = [&](const Pages &g) {
+            int64_t at = 0;
+            if (!TILED)
+                at = valid(g.id[0]) * v_page + g.off[0] * v_token;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const char *v = v0 + (TILED ? valid(g.id[j / 4 % IDS]) * v_page + (g.off[j / 4 % IDS] + j % 4) * v_token
+                                            : from_lane(at, 16 * (j / 4) + 4 * grp + j % 4));
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    vw[j][i] = load_words<VW * CS, KEEP != kAll>(v + anew(v_at[i]));
+            }
+        };
+
+        // Weights of 16-bit floats are held 2^15 times larger, so that small ones
+        // keep their digits; the sum is too, and both are put right at the end.
+        constexpr int kLift = PV == kF16 ? 15 : 0;
+        float m[QT], l[QT];
+        f4 acc[QT][NP][VW];
+#pragma unroll
+        for (int n = 0; n < QT; ++n) {
+            m[n] = -INFINITY, l[n] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int j = 0; j < VW; ++j)
+                    acc[n][i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+
+        uint32_t s = turn;
+        Pages now = {}, next = {};
+        if (s < steps)
+            now = look_up(s);
+#pragma unroll
+        for (int n = 0; n < QT; ++n)
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+                if (((n * NQ + i) & (turns - 1)) == turn) {
+                    const int drop = query_chunk(i) - min(query_chunk(i), c.dim - E) - i * PER % E;
+                    Words<PER * QS> &w = qw[n][i];
+#pragma unroll
+                    for (int j = 0; j < PER * QS / 4; ++j)
+                        w.w[j] = 16 * n + col < live ? w.w[j] & keep_from(drop * QS, j) : 0u;
+                    char *const to = queries + n * S::kQ + lane * 16;
+                    if constexpr (QK == kSplit) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)  // a NaN whose bits all lie below the first part's would be an infinity there
+                            w.w[j] = __builtin_isnan(__builtin_bit_cast(float, w.w[j])) ? 0x7fc00000u : w.w[j];
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) {  // the highest bits, of which two values' are stored together
+                            u4 x;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                x[j] = __builtin_amdgcn_perm(w.w[2 * j + 1], w.w[2 * j], 0x07060302u);
+                                w.w[2 * j] = below(w.w[2 * j]), w.w[2 * j + 1] = below(w.w[2 * j + 1]);
+                            }
+                            *(u4 *)(to + (part * NQ + i) * 1024) = x;
+                        }
+                    } else {
+                        *(u4 *)(to + i * 1024) = u4{w.w[0], w.w[1], w.w[2], w.w[3]};
+                    }
+                }
+        __builtin_amdgcn_sched_barrier(0);  // else the queries' registers add to those of the loads below
+        if (s < steps) {
+            load_keys(now);
+            load_values(now);
+            now = look_up(min(s + turns, steps - 1));
+        }
+        __syncthreads();
+        // Whether some query does not see some token of the step at t0, or sees it at
+        // another position than its own; and whether one sees a token of the row.
+        auto is_mixed = [&](uint32_t t0) { return (int32_t)(t0 + S::kStep) > base || (int32_t)t0 < low || t0 < begin || t0 + S::kStep > end; };
+        auto sees = [&](uint64_t mask, int32_t at, uint32_t t, int32_t pos) {
+            return ((int32_t)t < base || (mask >> min((int32_t)t - base, 63) & 1)) && at - pos < window;
+        };
+        bool odd = false;  // whether a mixed step had a value that is infinite or no number
+        // One step; but for the last one it also issues the next one's loads, and
+        // is compiled for that alone (see attend_kernel.h).
+        auto step = [&](auto last_one) {
+            constexpr bool more = !decltype(last_one)::value;
+            const uint32_t t0 = a0 + s * S::kStep;
+            const uint32_t q_at = anew(lane) * 16;
+            // Scores: a row per token, a column per query.
+            f4 x[QT][UT];
+#pragma unroll
+            for (int n = 0; n < QT; ++n)
+#pragma unroll
+                for (int u = 0; u < UT; ++u)
+                    x[n][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                // Chunks past the head's end are not multiplied, and what the one at
+                // its end repeats is cleared: zero times an infinite key would be NaN.
+                if (4 * E * i >= c.dim)
+                    break;
+                if (CS != 1 && 4 * E * (i + 1) > c.dim) {
+                    const int at = E * (4 * i + anew(grp)), drop = at - min(at, c.dim - E);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t keep = keep_from(CS * drop, j);
+#pragma unroll
+                        for (int u = 0; u < UT; ++u)
+                            kw[u][i].w[j] &= keep;
+                    }
+                }
+                if constexpr (QK == kF32) {
+#pragma unroll
+                    for (int e = 0; e < E; e += 4)
+#pragma unroll
+                        for (int n = 0; n < QT; ++n) {
+                            const f4 q = *(const f4 *)(queries + n * S::kQ + (i * (E / 4) + e / 4) * 1024 + q_at);
+#pragma unroll
+                            for (int u = 0; u < UT; ++u)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    x[n][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(kw[u][i].w, e + j), q[j], x[n][u], 0, 0, 0);
+                        }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; e += 8) {
+                        u4 k[UT];
+#pragma unroll
+                        for (int u = 0; u < UT; ++u)
+                            k[u] = u4{pair16<C, QK>(kw[u][i].w, e / 2), pair16<C, QK>(kw[u][i].w, e / 2 + 1),
+                                      pair16<C, QK>(kw[u][i].w, e / 2 + 2), pair16<C, QK>(kw[u][i].w, e / 2 + 3)};
+#pragma unroll
+                        for (int n = 0; n < QT; ++n)
+#pragma unroll
+                            for (int part = 0; part < (QK == kSplit ? 3 : 1); ++part) {
+                                const u4 q = *(const u4 *)(queries + n * S::kQ + (part * NQ + i * (E / 8) + e / 8) * 1024 + q_at);
+#pragma unroll
+                                for (int u = 0; u < UT; ++u)
+                                    x[n][u] = mfma16<QK>(k[u], q, x[n][u]);
+                            }
+                    }
+                }
+            }
+            if constexpr (more) {
+                next = look_up(min(s + 2 * turns, steps - 1));
+                load_keys(now);
+            }
+            auto every = [&](auto f) {
+#pragma unroll
+                for (int n = 0; n < QT; ++n)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        x[n][j / 4][j % 4] = f(x[n][j / 4][j % 4]);
+            };
+            every([&](float z) { return z * by; });
+            if (p.cap > 0.0f) {
+                const float over = 1.0f / p.cap;
+                float most = 0.0f;
+                every([&](float z) {
+                    z *= over;
+                    most = fmaxf(most, __builtin_fabsf(z));
+                    return z;
+                });
+                if (__any(!(most < kTanhNear)))
+                    every([&](float z) { return p.cap * (__builtin_fabsf(z) < kTanhNear ? tanh_near(z) : tanh_far(z)); });
+                else
+                    every([&](float z) { return p.cap * tanh_near(z); });
+            }
+            // Whether all queries see all of the step's tokens, each at its own position.
+            const bool mixed = is_mixed(t0);
+            auto token = [&](int j) { return t0 + 16 * (j / 4) + 4 * grp + j % 4; };
+            if (mixed) {
+                // Tokens of other parts, or none: their values may be anything.  Zero
+                // times a value that a query does not see would be NaN where that is
+                // infinite or no number: such values count as zero here, and are added
+                // to the sums of those that see them at the end.
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint32_t t = token(j);
+                    const bool out = t < begin || t >= end;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int n = 0; n < VW * CS / 4; ++n) {
+                            const uint32_t v = vw[j][i].w[n], f = finite_word<C>(v);
+                            odd |= !out && f != v;
+                            vw[j][i].w[n] = out ? 0u : f;
+                        }
+                }
+#pragma unroll
+                for (int n = 0; n < QT; ++n) {
+                    const Column w = columns[16 * n + col];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint32_t t = anew(token(j));
+                        const int32_t pos = (int32_t)t < base ? (int32_t)t : base + depths[min((int32_t)t - base, DETFOLD_MAX_DRAFTS - 1)];
+                        float z = x[n][j / 4][j % 4];
+                        if (p.slopes)
+                            z += w.slope * (float)(pos - w.at);
+                        x[n][j / 4][j % 4] = t >= begin && t < end && sees(w.mask, w.at, t, pos) ? z : -INFINITY;
+                    }
+                }
+            } else if (p.slopes) {
+#pragma unroll
+                for (int n = 0; n < QT; ++n) {
+                    const Column w = columns[16 * n + col];
+                    const int32_t at = (int32_t)t0 + 4 * grp - w.at;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        x[n][j / 4][j % 4] += w.slope * (float)(at + 16 * (j / 4) + j % 4);
+                }
+            }
+            // Weights, relative to the largest score so far.
+#pragma unroll
+            for (int n = 0; n < QT; ++n) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    top = fmaxf(top, x[n][j / 4][j % 4]);
+                top = fmaxf(m[n], over_groups(top, [](float y, float z) { return fmaxf(y, z); }));
+                const float origin = top == -INFINITY ? 0.0f : top;
+                if (__any(top > m[n])) {
+                    const float turn = weight_of(m[n] - origin);
+                    l[n] *= turn;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int j = 0; j < VW; ++j)
+                            acc[n][i][j] *= turn;
+                    m[n] = top;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    x[n][j / 4][j % 4] = weight_of<kLift>(x[n][j / 4][j % 4] - origin);
+                    l[n] += x[n][j / 4][j % 4];
+                }
+            }
+            // Values: the output's rows are its dims, its columns the queries.
+            if constexpr (PV == kF32) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int e = 0; e < VW; ++e)
+#pragma unroll
+                            for (int n = 0; n < QT; ++n)
+                                acc[n][i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(vw[j][i].w, e), x[n][j / 4][j % 4], acc[n][i][e], 0, 0, 0);
+            } else {
+                constexpr int TERMS = PV == kSplit ? 3 : 1;
+#pragma unroll
+                for (int u = 0; u < UT; u += 2) {
+                    u4 w[QT][TERMS];
+#pragma unroll
+                    for (int n = 0; n < QT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float y = x[n][u + j / 2][2 * (j % 2)], z = x[n][u + j / 2][2 * (j % 2) + 1];
+                            if constexpr (PV == kF16) {
+                                w[n][0][j] = __builtin_bit_cast(uint32_t, f16x2{(f16)y, (f16)z});
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < TERMS; ++e) {
+                                    const bf16x2 part = {(bf16)y, (bf16)z};
+                                    w[n][e][j] = __builtin_bit_cast(uint32_t, part);
+                                    y -= (float)part.x, z -= (float)part.y;
+                                }
+                            }
+                        }
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int e = 0; e < VW; e += 2) {
+                            u4 lo, hi;  // dims e and e + 1 of the lane's eight tokens
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t y = pair16<C, PV>(vw[4 * u + 2 * j][i].w, e / 2), z = pair16<C, PV>(vw[4 * u + 2 * j + 1][i].w, e / 2);
+                                lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
+                                hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
+                            }
+#pragma unroll
+                            for (int n = 0; n < QT; ++n)
+#pragma unroll
+                                for (int q = 0; q < TERMS; ++q) {
+                                    acc[n][i][e] = mfma16<PV>(lo, w[n][q], acc[n][i][e]);
+                                    acc[n][i][e + 1] = mfma16<PV>(hi, w[n][q], acc[n][i][e + 1]);
+                                }
+                        }
+                }
+            }
+            if constexpr (more) {
+                load_values(now);
+                now = next;
+            }
+        };
+        for (; s + turns < steps; s += turns)
+            step(Last<false>{});
+        if (s < steps)
+            step(Last<true>{});
+
+        // The waves' states, joined in order, a tile of columns at a time: each
+        // leaves its columns' sums in LDS, over the queries, and a thread takes four
+        // dims of a column from every turn.
+        f2 *const state = (f2 *)lds;
+        int *const odds = (int *)(lds + waves * 16 * sizeof(f2));
+        float *const sums = (float *)(odds + 4 * waves);
+        const bool any_bad = __any(bad), any_odd = __any(odd);
+#pragma unroll
+        for (int n = 0; n < QT; ++n) {
+            float total = over_groups(l[n], [](float y, float z) { return y + z; });
+            const float lift = PV == kF16 ? 0x1p-15f : 1.0f;
+            total *= lift;
+            if (any_bad)
+                total = __builtin_nanf("");
+            __syncthreads();
+            if (16 * n + col < live) {
+                float *mine = sums + (wave * 16 + col) * S::kRow;
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < VW; e += 4)
+                            *(f4 *)(mine + VW * (16 * i + 4 * grp + j) + e) =
+                                f4{acc[n][i][e][j], acc[n][i][e + 1][j], acc[n][i][e + 2][j], acc[n][i][e + 3][j]} * lift;
+                if (grp == 0)
+                    state[wave * 16 + col] = f2{m[n], total};
+            }
+            if (lane == 0)
+                odds[wave] = any_odd;
+            __syncthreads();
+            const TreeArgs &p = tree_arguments();
+            const detfold_attend &a = p.a;
+            const int here = min(live - 16 * n, 16);
+            for (int i = 64 * turn + lane; i < here * (D / 4); i += 64 * turns) {
+                const int head = i / (D / 4), at = i % (D / 4) * 4, at0 = at / VW * VW;
+                if (at0 >= p.c.v_dim)
+                    continue;
+                float top = -INFINITY;
+                for (int w = in; w < waves; w += beside)
+                    top = fmaxf(top, state[w * 16 + head].x);
+                const float origin = top == -INFINITY ? 0.0f : top;
+                f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                float weights = 0.0f;
+                int unfinished = 0;
+                for (int w = in; w < waves; w += beside) {
+                    const f2 ml = state[w * 16 + head];
+                    const float by = weight_of(ml.x - origin);
+                    weights += ml.y * by;
+                    sum += *(const f4 *)(sums + (w * 16 + head) * S::kRow + at) * by;
+                    unfinished |= odds[w];
+                }
+                const int d = min(at0, p.c.v_dim - VW) + at - at0, x = col0 + 16 * n + head, q = (int)divide((uint32_t)x, p.heads_of);
+                if (unfinished) {  // the values that the mixed steps left out
+                    const uint64_t mask = p.masks ? (uint64_t)p.masks[b * p.drafts + q] : ~0ull >> (63 - q);
+#pragma unroll 1
+                    for (uint32_t t = begin; t < end; ++t) {
+                        if (!is_mixed(a0 + (t - a0) / S::kStep * S::kStep)) {
+                            t = a0 + ((t - a0) / S::kStep + 1) * S::kStep - 1;
+                            continue;
+                        }
+                        const uint32_t pg = divide(t, p.page), id = (uint32_t)table[pg];
+                        if (id >= pages || !sees(mask, base + depth(q), t, (int32_t)t < base ? (int32_t)t : base + depth((int32_t)t - base)))
+                            continue;
+                        const C *v = (const C *)(v0 + id * v_page + (t - pg * p.page.d) * v_token) + d;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float z = to_f32(v[e]);
+                            sum[e] += __builtin_fabsf(z) < INFINITY ? 0.0f : z;
+                        }
+                    }
+                }
+                if (slot >= 0) {
+                    const int64_t from = slot * p.slot_cols + 16 * n + head;
+                    __builtin_memcpy(p.acc + from * p.c.v_dim + d, &sum, sizeof(sum));
+                    if (at == 0)
+                        p.ml[from] = make_float2(top, weights);
+                } else {
+                    const int g = (int)h * p.group + x - q * p.group;
+                    const float by = out_scale(v_scale, weights);
+                    const float o[4] = {sum.x * by, sum.y * by, sum.z * by, sum.w * by};
+                    put_out<4>(a, b * a.out_row + q * p.out_draft + (int64_t)g * a.out_head + d, o);
+                    if (a.lse && at == 0)
+                        a.lse[(b * p.drafts + q) * a.q_heads + g] = log_sum(top, weights);
+                }
+            }
+        }
+        mine.left -= done;
+        if (mine.left == 0)
+            return;
+        mine.at = mine.row_at = mine.at + done;
+        ++b;
+        mine.len = scalar_load(tree_arguments().a.lens + b);
+        __syncthreads();
+    }
+}
+
+// The kernel of a call and the LDS it takes: for a unit's queries and columns, and
+// for the sums of a wave's tile.
+template <typename C, int QK, int PV, int D, int QT, int MOST, int KEEP> TreeKernel pick_tree_tiled(const TreeArgs &a)
+{
+    typedef Attend<C, QK, PV, D, true, MOST, KEEP> S;
+    const void *f = a.tiled ? (const void *)k_tree<C, QK, PV, D, true, QT, MOST, KEEP> : (const void *)k_tree<C, QK, PV, D, false, QT, MOST, KEEP>;
+    return {f, QT * (S::kQ + 16 * (int)sizeof(Column)), 16 * (8 + S::kRow * 4) + 16};
+}
+template <typename C, int QK, int PV, int D> TreeKernel pick_tree_columns(const TreeArgs &a)
+{
+    if constexpr (QK != kF32 && QK != kSplit && PV != kF32 && PV != kSplit) {
+        if constexpr (D < 256)
+            if (a.tiles_of == 4)
+                return pick_tree_tiled<C, QK, PV, D, 4, 2, kKeys>(a);
+        if (a.tiles_of >= 2)
+            return pick_tree_tiled<C, QK, PV, D, 2, 2, kKeys>(a);
+    }
+    // A step of one tile is 16 KiB, or 32 of heads above 128.
+    constexpr int MOST = D * sizeof(C) <= 128 ? 4 : 2;
+    if constexpr (MOST > 2)
+        if (a.brief)
+            return pick_tree_tiled<C, QK, PV, D, 1, 2, kAll>(a);
+    return a.keep == kAll ? pick_tree_tiled<C, QK, PV, D, 1, MOST, kAll>(a) : pick_tree_tiled<C, QK, PV, D, 1, MOST, kKeys>(a);
+}
+template <typename C, int QK, int PV> TreeKernel pick_tree(const TreeArgs &a)
+{
+    const int dim = a.c.dim > a.c.v_dim ? a.c.dim : a.c.v_dim;
+    return dim <= 64 ? pick_tree_columns<C, QK, PV, 64>(a) : dim <= 128 ? pick_tree_columns<C, QK, PV, 128>(a) : pick_tree_columns<C, QK, PV, 256>(a);
+}
+
+}  // namespace detfold_impl
+
+#endif  // DETFOLD_TREE_KERNEL_H

@@ -1,129 +1,155 @@
-// tree_kernels.hip -- the attention of drafted tokens over a paged cache, for gfx950.
+// tree_kernels.hip -- the launch of the attention of drafted tokens and the join
+// of the parts of long rows, for gfx950.
 
 #include <hip/hip_runtime.h>
 
-#include "decode_device.h"
-#include "draft.h"
+#include "tree_kernel.h"
 
 namespace detfold_impl {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int64_t kMaxBlocks = (int64_t)1 << 22;
+constexpr int kBlock = 256;                       // threads of the join
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds at most 2^32 threads
 
-// One workgroup per row, drafted query and query head; 256 tokens at a time.
-template <typename T, typename C> __global__ __launch_bounds__(kBlock) void k_tree(TreeArgs p, int64_t block0)
+// The sums of each query of a row, or of the row that a share begins without
+// ending it, joined in order.  A lane takes four dims, LANES lanes a part, and
+// GROUPS groups of lanes every GROUPS-th part of a query; the loads of eight
+// parts go out together.  Parts that are empty add zeros, so a row's bits do not
+// depend on how many follow its last one.
+template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_join_tree(TreeArgs p)
 {
+    constexpr int QUERIES = kBlock / (LANES * GROUPS);  // of a workgroup
     const detfold_attend &a = p.a;
-    const detfold_paged_cache &c = p.c;
-    const int64_t block = block0 + blockIdx.x;
-    const int g = (int)(block % a.q_heads), i = (int)(block / a.q_heads % p.drafts), h = g / p.group;
-    const int64_t b = block / a.q_heads / p.drafts;
-    const int drafted = min(max(p.counts ? p.counts[b] : p.drafts, 0), p.drafts);
-    if (i >= drafted)
-        return;
-    const int64_t n0 = max(a.lens[b], 0);
-    bool bad = n0 > a.max_len || n0 > a.table_width * c.page;
-    const int64_t n = bad ? 0 : n0, base = max(n - drafted, (int64_t)0);
-    auto depth = [&](int64_t j) { return p.depths ? min(max(p.depths[b * p.drafts + j], 0), DETFOLD_MAX_DRAFTS - 1) : (int)j; };
-    const uint64_t mask = p.masks ? (uint64_t)p.masks[b * p.drafts + i] : ~0ull >> (63 - i);
-    const int64_t own = base + depth(i);
-    const T *q = (const T *)a.q + b * a.q_row + i * p.q_draft + g * a.q_head;
-    const float by = a.scale * (c.k_scale ? c.k_scale[h] : 1.0f), slope = p.slopes ? p.slopes[g] : 0.0f;
-    const int32_t *table = a.table + b * a.table_row;
-
-    __shared__ float weights[kBlock];
-    __shared__ int64_t places[kBlock];
-    __shared__ float red[kBlock];
-    __shared__ int bads;
-    if (threadIdx.x == 0)
-        bads = bad;
-    __syncthreads();
-    float m = -INFINITY, l = 0.0f, acc = 0.0f;
-    const int64_t begin = p.window > 0 ? max(base - p.window, (int64_t)0) : 0;
-    for (int64_t t0 = begin; t0 < n; t0 += kBlock) {
-        const int64_t t = t0 + threadIdx.x;
-        float s = -INFINITY;
-        int64_t at = -1;
-        if (t < n) {
-            const int64_t pos = t < base ? t : base + depth(t - base);
-            const bool seen = (t < base || (mask >> (t - base) & 1)) && (p.window == 0 || own - pos < p.window);
-            if (seen) {
-                const int64_t id = table[t / c.page];
-                if (id < 0 || id >= c.pages) {
-                    bads = 1;
-                } else {
-                    const C *k = (const C *)c.k + id * c.k_page + t % c.page * c.k_token + h * c.k_head;
-                    float dot = 0.0f;
-                    for (int d = 0; d < c.dim; ++d)
-                        dot += to_f32(q[d]) * to_f32(k[d]);
-                    s = dot * by;
-                    if (p.cap > 0.0f)
-                        s = p.cap * tanhf(s / p.cap);
-                    if (p.slopes)
-                        s += slope * (float)(pos - own);
-                    at = id * c.v_page + t % c.page * c.v_token + h * c.v_head;
-                }
-            }
-        }
-        red[threadIdx.x] = s;
-        __syncthreads();
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES % GROUPS, own = threadIdx.x / (LANES * GROUPS);
+    const uint32_t y = divide(blockIdx.x, p.join_blocks);
+    const int query = (int)(blockIdx.x - y * p.join_blocks.d) * QUERIES + own;
+    const int64_t units = (int64_t)p.units.d * p.beside;
+    int64_t b = p.row0 + y;
+    int n = (int)p.parts.d;
+    bool there = query < p.drafts * a.q_heads;
+    int3 cut = {};
+    if (p.shares.d) {
+        cut = p.cut[y];
+        if (cut.x < 0)
+            return;
+        b = cut.x;
+        n = cut.z - cut.y + 1;
+    }
+    const int i = (int)((uint32_t)query / (uint32_t)a.q_heads), head = query - i * a.q_heads;
+    there &= i < (p.counts ? p.counts[b] : p.drafts);
+    const int h = (int)divide((uint32_t)head, p.heads_of), col = i * p.group + head - h * p.group;
+    const int tile = col / (16 * p.tiles_of);
+    const int64_t unit = h * (int64_t)p.tiles.d + tile;
+    int64_t first, next, step;  // slots
+    if (p.shares.d) {
+        step = 2 * units;
+        next = (cut.y * units + unit) * 2;
+        first = next + 1;
+    } else {
+        step = units;
+        first = next = b * n * step + unit;
+    }
+    auto slot = [&](int i) { return (i ? next + i * step : first) * p.slot_cols + (col - tile * 16 * p.tiles_of); };
+    const int d0 = 4 * lane, d = min(d0, p.c.v_dim - 4);
+    f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    float m = -INFINITY, l = 0.0f;
+    for (int i0 = group; there && i0 < n; i0 += 8 * GROUPS) {  // eight parts' loads together
+        f4 x[8];
+        float2 s[8];
         float top = m;
-        bool odd = false;
-        for (int j = 0; j < kBlock; ++j)
-            top = fmaxf(top, red[j]), odd |= __builtin_isnan(red[j]);
-        const float origin = top == -INFINITY ? 0.0f : top, turn = expf(m - origin);
-        weights[threadIdx.x] = at < 0 ? 0.0f : expf(s - origin);
-        places[threadIdx.x] = at;
-        __syncthreads();
-        l *= turn, acc *= turn, m = top;
-        for (int j = 0; j < kBlock; ++j) {
-            l += weights[j];
-            if (places[j] >= 0 && (int)threadIdx.x < c.v_dim)
-                acc += weights[j] * to_f32(((const C *)c.v + places[j])[threadIdx.x]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * GROUPS;
+            const int64_t at = slot(min(i, n - 1));
+            s[j] = p.ml[at];
+            __builtin_memcpy(&x[j], p.acc + at * p.c.v_dim + d, sizeof(f4));
+            if (i >= n)
+                s[j] = make_float2(-INFINITY, 0.0f), x[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        if (odd)
-            l = __builtin_nanf("");
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            top = fmaxf(top, s[j].x);
+        const float origin = top == -INFINITY ? 0.0f : top, turn = weight_of(m - origin);
+        l *= turn;
+        acc *= turn;
+        m = top;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w = weight_of(s[j].x - origin);
+            l += s[j].y * w;
+            acc += x[j] * w;
+        }
+    }
+    float top = m;
+    if constexpr (GROUPS > 1) {
+        __shared__ f4 accs[QUERIES][GROUPS][LANES];
+        __shared__ float2 mls[QUERIES][GROUPS];
+        accs[own][group][lane] = acc;
+        if (lane == 0)
+            mls[own][group] = make_float2(m, l);
         __syncthreads();
+        there &= group == 0;
+        top = -INFINITY;
+        for (int i = 0; i < GROUPS; ++i)
+            top = fmaxf(top, mls[own][i].x);
+        const float origin = top == -INFINITY ? 0.0f : top;
+        acc = f4{0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
+        for (int i = 0; i < GROUPS; ++i) {
+            const float w = weight_of(mls[own][i].x - origin);
+            l += mls[own][i].y * w;
+            acc += accs[own][i][lane] * w;
+        }
     }
-    __syncthreads();
-    if (bads)
-        l = __builtin_nanf("");
-    const float out = (l == 0.0f ? 0.0f : 1.0f / l) * acc * (c.v_scale ? c.v_scale[h] : 1.0f);
-    const int64_t to = b * a.out_row + i * p.out_draft + g * a.out_head + threadIdx.x;
-    if ((int)threadIdx.x < c.v_dim) {
-        if (a.out_type == DETFOLD_F32)
-            ((float *)a.out)[to] = out;
-        else if constexpr (sizeof(T) == 2)
-            ((T *)a.out)[to] = (T)out;
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[(b * p.drafts + i) * a.q_heads + g] = (m == -INFINITY ? 0.0f : m) + logf(l);
+    if (!there)
+        return;
+    const float by = out_scale(p.c.v_scale ? p.c.v_scale[h] : 1.0f, l), out[4] = {acc.x * by, acc.y * by, acc.z * by, acc.w * by};
+    if (d0 < p.c.v_dim)
+        put_out<4>(a, b * a.out_row + i * p.out_draft + (int64_t)head * a.out_head + d, out);
+    if (a.lse && lane == 0)
+        a.lse[(b * p.drafts + i) * a.q_heads + head] = log_sum(top, l);
 }
 
-template <typename T> const void *pick(int cache)
+template <int GROUPS> const void *pick_join(int dim)
 {
-    if (cache == DETFOLD_E4M3)
-        return (const void *)k_tree<T, e4m3>;
-    if constexpr (sizeof(T) == 4)
-        if (cache == DETFOLD_BF16)
-            return (const void *)k_tree<T, bf16>;
-    return (const void *)k_tree<T, T>;
+    if constexpr (GROUPS <= 4)
+        if (dim > 128)
+            return (const void *)k_join_tree<64, GROUPS>;
+    return dim <= 64 ? (const void *)k_join_tree<16, GROUPS> : (const void *)k_join_tree<32, GROUPS>;
 }
 
 }  // namespace
 
 int launch_tree(const TreeArgs &a, void *stream)
 {
+    const TreeKernel k = a.a.type == DETFOLD_F32 ? tree_f32(a) : a.a.type == DETFOLD_BF16 ? tree_bf16(a) : tree_f16(a);
     TreeArgs copy = a;
-    const void *f = a.a.type == DETFOLD_F32 ? pick<float>(a.c.type) : a.a.type == DETFOLD_BF16 ? pick<bf16>(a.c.type) : pick<f16>(a.c.type);
-    const int64_t total = a.a.batch * a.drafts * a.a.q_heads;
-    for (int64_t first = 0; first < total; first += kMaxBlocks) {
-        void *args[] = {&copy, &first};
-        if (hipLaunchKernel(f, dim3((unsigned)(total - first < kMaxBlocks ? total - first : kMaxBlocks)), dim3(kBlock), args, 0,
-                            static_cast<hipStream_t>(stream)) != hipSuccess)
-            return DETFOLD_ELAUNCH;
-    }
+    void *args[] = {&copy};
+    auto launch = [&](const void *f, int64_t blocks, int threads, int lds) {
+        return hipLaunchKernel(f, dim3((unsigned)blocks), dim3(threads), args, lds, static_cast<hipStream_t>(stream)) == hipSuccess;
+    };
+    // Some rows to a launch, whatever a row's workgroups.
+    auto rows = [&](int64_t each, const void *f, int threads, int lds) {
+        const int64_t some = each < kMaxBlocks ? kMaxBlocks / each : 1;
+        for (copy.row0 = 0; copy.row0 < a.a.batch; copy.row0 += some)
+            if (!launch(f, (a.a.batch - copy.row0 < some ? a.a.batch - copy.row0 : some) * each, threads, lds))
+                return false;
+        return true;
+    };
+    const int queries = a.beside * k.unit_bytes + 4 * DETFOLD_MAX_DRAFTS, sums = a.waves * k.wave_bytes, lds = queries > sums ? queries : sums;
+    if (!(a.shares.d ? launch(k.f, (int64_t)a.shares.d * a.units.d, 64 * a.waves, lds) : rows((int64_t)a.units.d * a.parts.d, k.f, 64 * a.waves, lds)))
+        return DETFOLD_ELAUNCH;
+    if (!a.shares.d && a.parts.d <= 1)
+        return DETFOLD_OK;
+    // Where rows have many parts, and few queries wait for them, several groups of
+    // lanes take a query's.
+    const int lanes = a.c.v_dim <= 64 ? 16 : a.c.v_dim <= 128 ? 32 : 64;
+    const int64_t parts = a.shares.d ? a.shares.d / a.a.batch : a.parts.d, queries_all = (int64_t)a.drafts * a.a.q_heads;
+    const int groups = parts > 8 ? 256 / lanes < 8 ? 4 : 8 : 1, per = kBlock / (lanes * groups);
+    const int64_t each = (queries_all + per - 1) / per;
+    copy.join_blocks = divider((uint32_t)each);
+    const void *join = groups == 8 ? pick_join<8>(a.c.v_dim) : groups == 4 ? pick_join<4>(a.c.v_dim) : pick_join<1>(a.c.v_dim);
+    if (!(a.shares.d ? launch(join, (a.by_row ? a.a.batch : a.shares.d) * each, kBlock, 0) : rows(each, join, kBlock, 0)))
+        return DETFOLD_ELAUNCH;
     return DETFOLD_OK;
 }
 

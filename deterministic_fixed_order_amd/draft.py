@@ -174,7 +174,7 @@ def _attend(what, out, q, cache, table, lens, masks, counts, depths, cap, slopes
     if masks is not None and depths is None and (window or slopes is not None):
         raise ValueError("masks with a window or slopes need depths")
     if max_len is None:
-        max_len = min(width * cache.page, 2 ** 31 - 1)
+        max_len = min(width * cache.page, 2 ** 31 - 1 - MAX_DRAFTS)
     if workspace is None:  # in the pool of the stream that uses it, as attend_paged's
         import torch
         with _d._within(stream, dev):

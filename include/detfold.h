@@ -566,7 +566,8 @@ int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *
  *   depths    device, int32 [batch][drafts], each taken as 0 .. 63, or NULL: i of
  *             token i.  Needed with masks where there is a window or slopes
  *   slopes    device, [q_heads] floats, or NULL
- *   cap       0: none; else positive and finite
+ *   cap       0: none; else a positive, finite, normal number
+ *   max_len   at most 2^31 - 65
  * Bits, splits and the workspace (detfold_tree_workspace) as of
  * detfold_attend_paged.
  * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP, DETFOLD_ESIZE, DETFOLD_EDEVICE,
