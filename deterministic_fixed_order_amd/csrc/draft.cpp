@@ -13,7 +13,7 @@
 namespace detfold_impl {
 namespace {
 
-constexpr int64_t kMaxPage = (int64_t)1 << 31;  // values of a page's keys or values that are copied
+constexpr int64_t kMaxMoved = (int64_t)1 << 22;  // tokens of a page, or of a row, that one launch moves
 
 // Whether a written [n0][n1][n2][last] buffer has no element twice: in the order
 // of the strides, each passes what lies within it.
@@ -52,18 +52,16 @@ bool same_cache(const detfold_paged_cache &a, const detfold_paged_cache &b)
 
 namespace {
 
-// Tiles of 16 queries to a wave: as many as a key-value head has, where the products
-// are of 16 bits and the sums leave the registers room, which of heads above 128 two
-// do.  Products in float32, and in parts, are what bounds one tile already.  One
-// token a row is split as attend_paged splits it, in the same workspace.
-int tiles_of(int64_t cols, int32_t drafts, int wide_head, bool narrow)
-{
-    return !narrow || drafts == 1 || cols <= 16 ? 1 : cols <= 32 || wide_head == 256 ? 2 : 4;
-}
+// Tiles of 16 queries to a wave: two, which share what is loaded, where the products
+// are of 16 bits and there are as many queries.  Four do not fit the registers with
+// eight waves to a compute unit (1 x 16 tokens over 131072 took 163 us with four, 139
+// with two).  Products in float32, and in parts, are what bounds one tile already.
+// One token a row is split as attend_paged splits it, in the same workspace.
+int tiles_of(int64_t cols, int32_t drafts, bool narrow) { return narrow && drafts > 1 && cols > 16 ? 2 : 1; }
 
 }  // namespace
 
-// What plan_attend does, with up to 64 queries of a key-value head to a unit.
+// What plan_attend does, with up to 32 queries of a key-value head to a unit.
 int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32_t q_heads, int64_t max_len, int64_t window, int32_t split,
               int32_t type, int32_t out_type, int32_t cu_count, TreePlan *p)
 {
@@ -76,9 +74,9 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
         return DETFOLD_EINVAL;
     const int64_t cols = (int64_t)drafts * (q_heads / c.heads);
     const int head = c.dim > c.v_dim ? c.dim : c.v_dim, wide_head = head <= 64 ? 64 : head <= 128 ? 128 : 256;
-    const int tiles = tiles_of(cols, drafts, wide_head, type != DETFOLD_F32 && out_type != DETFOLD_F32);
+    const int tiles = tiles_of(cols, drafts, type != DETFOLD_F32 && out_type != DETFOLD_F32);
     const int64_t units = c.heads * ((cols + 16 * tiles - 1) / (16 * tiles));
-    const int64_t queries = c.heads * (cols > 32 ? (cols + 63) / 64 * 64 : (cols + 15) / 16 * 16);  // at least units times a slot's
+    const int64_t queries = c.heads * (cols > 16 ? (cols + 31) / 32 * 32 : cols);  // at least units times a slot's
     if (batch > 0 && queries > kMaxElems / 16 / batch)
         return DETFOLD_EINVAL;
     const int64_t seen = window > 0 && window < max_len - (drafts - 1) ? window + drafts - 1 : max_len;
@@ -122,7 +120,7 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
         return DETFOLD_EINVAL;
     int64_t upto = most > 1 ? (most < kMaxBlocks ? most : kMaxBlocks) * queries * batch : 0;
     if (split == 0) {
-        const int64_t capped = kMaxBlocks * 64 + 2 * queries * batch, even = kWavesPerCu * cu_count * (cols < 64 ? cols : 64);
+        const int64_t capped = kMaxBlocks * 32 + 2 * queries * batch, even = kWavesPerCu * cu_count * (cols < 32 ? cols : 32);
         upto = upto > capped ? capped : upto;
         upto = upto > even ? upto : even;
     }
@@ -187,7 +185,7 @@ int check_copy(const detfold_paged_cache *c, const detfold_paged_cache *into, co
         return rc;
     if (into && (into->page != c->page || into->heads != c->heads || into->dim != c->dim || into->v_dim != c->v_dim || into->type != c->type))
         return DETFOLD_EINVAL;
-    if (count < 0 || count >= kMaxCount || c->page > kMaxPage / c->heads / (c->dim > c->v_dim ? c->dim : c->v_dim))
+    if (count < 0 || count >= kMaxCount || c->page > kMaxMoved)
         return DETFOLD_EINVAL;
     if (count == 0)
         return DETFOLD_OK;
@@ -224,6 +222,8 @@ int check_compact(const detfold_paged_cache *c, const detfold_compact *a)
     for (const void *p : {a->table, a->to, a->picks, a->counts, a->starts})
         if (!aligned(p, 4))
             return DETFOLD_EINVAL;
+    if (a->to && a->most > kMaxMoved)
+        return DETFOLD_EINVAL;
     const int64_t ts = a->table_width > 0 ? span2(a->batch, a->table_row, 1, 0, a->table_width) : 0;
     const int64_t os = a->to && a->to_width > 0 ? span2(a->batch, a->to_row, 1, 0, a->to_width) : 0;
     if (ts < 0 || os < 0 || a->most > kMaxElems / a->batch)
@@ -241,31 +241,31 @@ namespace {
 
 int chunks_of(int64_t bytes) { return (int)((bytes + 15) / 16); }
 
-// The runs of bytes that a page's tokens make in both caches: heads that lie beside
-// each other are one run, and whole pages whose tokens do are one, too.
-CopyRuns runs_of(const detfold_paged_cache &c, const detfold_paged_cache &w, bool values, bool whole)
+// A token's runs: heads that lie beside each other, on both sides, are one.
+TokenRuns runs_of(const detfold_paged_cache &c, const detfold_paged_cache &w, bool values)
 {
     const int64_t size = elem_size(c.type), dim = values ? c.v_dim : c.dim;
-    CopyRuns r = {};
-    r.from = (const char *)(values ? c.v : c.k), r.to = (char *)(values ? w.v : w.k);
-    r.from_page = size * (values ? c.v_page : c.k_page), r.to_page = size * (values ? w.v_page : w.k_page);
-    r.from_token = size * (values ? c.v_token : c.k_token), r.to_token = size * (values ? w.v_token : w.k_token);
-    r.from_head = size * (values ? c.v_head : c.k_head), r.to_head = size * (values ? w.v_head : w.k_head);
-    int64_t run = size * dim, heads = c.heads, tokens = c.page;
-    constexpr int64_t kMaxRun = (int64_t)1 << 30;
-    auto joins = [&](int64_t from, int64_t to, int64_t n) { return n == 1 || (from == run && to == run && run * n < kMaxRun); };
-    // Both orders: heads of a token beside each other, or tokens of a head.
-    for (int turn = 0; turn < 2; ++turn) {
-        if (heads > 1 && joins(r.from_head, r.to_head, heads))
-            run *= heads, heads = 1;
-        if (whole && tokens > 1 && joins(r.from_token, r.to_token, tokens))
-            run *= tokens, tokens = 1;
-    }
-    r.run = (int32_t)run;
-    r.chunks = divider((uint32_t)chunks_of(run));
-    r.heads = divider((uint32_t)heads);
-    r.page = divider(r.chunks.d * (uint32_t)heads * (uint32_t)tokens);
+    const bool joined = values ? c.v_head == dim && w.v_head == dim : c.k_head == dim && w.k_head == dim;
+    TokenRuns r;
+    r.run = (int32_t)(size * dim * (joined ? c.heads : 1));
+    r.chunks = divider((uint32_t)chunks_of(r.run));
+    r.token = divider(r.chunks.d * (uint32_t)(joined ? 1 : c.heads));
     return r;
+}
+
+CopySide copy_side(const detfold_paged_cache &c, const detfold_paged_cache &w, bool values)
+{
+    const int64_t size = elem_size(c.type);
+    return {(const char *)(values ? c.v : c.k), (char *)(values ? w.v : w.k),
+            size * (values ? c.v_page : c.k_page), size * (values ? c.v_token : c.k_token), size * (values ? c.v_head : c.k_head),
+            size * (values ? w.v_page : w.k_page), size * (values ? w.v_token : w.k_token), size * (values ? w.v_head : w.k_head)};
+}
+
+CompactSide compact_side(const detfold_paged_cache &c, bool values)
+{
+    const int64_t size = elem_size(c.type), run = size * (values ? c.v_dim : c.dim);
+    return {(char *)(values ? c.v : c.k), size * (values ? c.v_page : c.k_page), size * (values ? c.v_token : c.k_token),
+            size * (values ? c.v_head : c.k_head), (int32_t)run, divider((uint32_t)chunks_of(run))};
 }
 
 }  // namespace
@@ -370,8 +370,9 @@ int detfold_cache_copy(const detfold_paged_cache *cache, const detfold_paged_cac
         return rc;
     const detfold_paged_cache &w = into ? *into : *cache;
     CopyArgs k = {};
-    k.k = runs_of(*cache, w, false, !tokens);
-    k.v = runs_of(*cache, w, true, !tokens);
+    k.m.k = runs_of(*cache, w, false), k.m.v = runs_of(*cache, w, true);
+    k.k = copy_side(*cache, w, false), k.v = copy_side(*cache, w, true);
+    k.page = divider((uint32_t)cache->page);
     k.src = src, k.dst = dst, k.tokens = tokens;
     k.pages = cache->pages, k.into_pages = w.pages;
     return launch_copy_pages(k, count, stream);
@@ -383,12 +384,13 @@ int detfold_cache_compact(const detfold_paged_cache *cache, const detfold_compac
     if (rc != DETFOLD_OK || args->batch == 0 || args->most == 0)
         return rc;
     CompactArgs k = {};
-    k.c = *cache;
     k.a = *args;
-    k.page = divider((uint32_t)cache->page);
+    k.m.k = runs_of(*cache, *cache, false), k.m.v = runs_of(*cache, *cache, true);
+    k.k = compact_side(*cache, false), k.v = compact_side(*cache, true);
     k.heads = divider((uint32_t)cache->heads);
-    k.k_chunks = divider((uint32_t)chunks_of((int64_t)cache->dim * elem_size(cache->type)));
-    k.v_chunks = divider((uint32_t)chunks_of((int64_t)cache->v_dim * elem_size(cache->type)));
+    k.pages = cache->pages;
+    k.page = divider((uint32_t)cache->page);
+    k.most = divider((uint32_t)args->most);
     return launch_compact(k, stream);
 }
 

@@ -45,27 +45,47 @@ struct TreePlan : detfold_attend_plan {
     bool brief;
 };
 
-// Kernel arguments of the page copy: a page's tokens are `tokens` runs of `heads`
-// runs of bytes, in the keys and in the values, taken in chunks.
-struct CopyRuns {
-    const char *from;
-    char *to;
-    int64_t from_page, from_token, from_head, to_page, to_token, to_head;  // bytes
-    int32_t run;                 // bytes
-    Divider chunks, heads, page; // chunks of a run, runs of a token, chunks of a page
+// What a token's keys, or values, are in bytes: runs, taken in chunks of 16.
+struct TokenRuns {
+    int32_t run;            // bytes
+    Divider chunks, token;  // chunks of a run, and of a token
 };
-struct CopyArgs {
-    CopyRuns k, v;
-    const int32_t *src, *dst, *tokens;
-    int64_t pages, into_pages;
-    int64_t first;              // copy of the launch
-    uint32_t count, key_blocks; // copies of the launch, and its workgroups that take keys
+// Of a launch that moves tokens: what a wave takes, and the keys' waves.
+struct MoveArgs {
+    TokenRuns k, v;
+    int64_t tokens;
+    int32_t group;
+    uint32_t waves;
 };
 
+// Kernel arguments of the page copy; strides in bytes.
+struct CopySide {
+    const char *from;
+    char *to;
+    int64_t from_page, from_token, from_head, to_page, to_token, to_head;
+};
+struct CopyArgs {
+    MoveArgs m;
+    CopySide k, v;
+    const int32_t *src, *dst, *tokens;
+    int64_t pages, into_pages;
+    int64_t first;  // copy of the launch
+    Divider page;
+};
+
+// Kernel arguments of the compaction; strides in bytes.
+struct CompactSide {
+    char *pool;
+    int64_t page_bytes, token_bytes, head_bytes;
+    int32_t run;     // of a head
+    Divider chunks;
+};
 struct CompactArgs {
-    detfold_paged_cache c;
+    MoveArgs m;
     detfold_compact a;
-    Divider page, heads, k_chunks, v_chunks; // chunks of a key's and a value's head
+    CompactSide k, v;
+    int64_t pages;
+    Divider page, most, heads;
     int64_t row0;
 };
 

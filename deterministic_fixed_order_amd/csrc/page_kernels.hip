@@ -10,102 +10,202 @@ namespace detfold_impl {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int64_t kMaxItems = (int64_t)1 << 30;  // chunks of a launch
+constexpr int64_t kMaxItems = (int64_t)1 << 22;  // tokens of a launch, or one row's or page's
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22; // workgroups of a launch
+constexpr int64_t kOnceBytes = 8 << 20;          // that are not kept in the caches
 
-// 16 bytes at any alignment, as one wide load or store.
+// 16 bytes at any alignment, as one wide load or store; once: not kept in the caches.
 typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(1)));
-
-// The copy.  A thread takes U chunks of 16 bytes, their loads in flight together.
-// The last chunk of a run starts early enough to end with it, so runs of any
-// length from 16 bytes on take wide accesses; what two chunks share is written
-// twice, with the same bytes.
-template <int U> __global__ __launch_bounds__(kBlock) void k_copy_pages(CopyArgs p)
+template <bool ONCE> __device__ __forceinline__ u4 load16(const char *p) { return ONCE ? __builtin_nontemporal_load((const u4 *)p) : *(const u4 *)p; }
+template <bool ONCE> __device__ __forceinline__ void store16(char *p, u4 x)
 {
-    const bool values = blockIdx.x >= p.key_blocks;
-    const CopyRuns &r = values ? p.v : p.k;
-    const uint32_t x0 = (blockIdx.x - (values ? p.key_blocks : 0)) * (kBlock * U) + threadIdx.x;
-    u4 data[U];
-    char *to[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-        const uint32_t x = x0 + j * kBlock, i = divide(x, r.page);
-        to[j] = nullptr;
-        if (i >= p.count)
-            continue;
-        const int32_t s = p.src[p.first + i], d = p.dst[p.first + i];
-        const uint32_t in = x - i * r.page.d, y = divide(in, r.chunks), u = in - y * r.chunks.d;
-        const uint32_t token = divide(y, r.heads), head = y - token * r.heads.d;
-        if (s < 0 || s >= p.pages || d < 0 || d >= p.into_pages || (p.tokens && (int32_t)token >= p.tokens[p.first + i]))
-            continue;
-        const int32_t at = min((int32_t)(16 * u), r.run - 16);
-        to[j] = r.to + d * r.to_page + token * r.to_token + head * r.to_head + at;
-        data[j] = *(const u4 *)(r.from + s * r.from_page + token * r.from_token + head * r.from_head + at);
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-        if (to[j])
-            *(u4 *)to[j] = data[j];
+    if (ONCE)
+        __builtin_nontemporal_store(x, (u4 *)p);
+    else
+        *(u4 *)p = x;
 }
 
-// The compaction.  A workgroup takes one head's keys or values of one row, and of
-// these as many tokens at a time as its threads hold, U chunks each.  In place a
-// move goes to a lower token: what is read with a tile of moves lies behind all
-// that earlier tiles wrote, and what it writes before all that later tiles read,
-// so that the one barrier between a tile's loads and its stores is enough.
-template <int U> __global__ __launch_bounds__(kBlock) void k_compact(CompactArgs p)
+__device__ __forceinline__ int64_t from_lane(int64_t x, int l)
 {
-    const detfold_paged_cache &c = p.c;
-    const detfold_compact &a = p.a;
-    const uint32_t y = divide(blockIdx.x >> 1, p.heads), head = (blockIdx.x >> 1) - y * p.heads.d;
-    const bool values = blockIdx.x & 1;
-    const int64_t b = p.row0 + y;
-    const int size = elem_size(c.type);
-    const Divider &per = values ? p.v_chunks : p.k_chunks;
-    const int run = (values ? c.v_dim : c.dim) * size;
-    char *const pool = (char *)(values ? c.v : c.k) + head * (values ? c.v_head : c.k_head) * size;
-    const int64_t page_bytes = (values ? c.v_page : c.k_page) * size, token_bytes = (values ? c.v_token : c.k_token) * size;
-    const int32_t *table = a.table + b * a.table_row, *to = a.to ? a.to + b * a.to_row : table;
-    const int64_t width = a.table_width, to_width = a.to ? a.to_width : width;
-    const int64_t start = a.starts ? a.starts[b] : 0;
-    const int64_t n = min((int64_t)a.counts[b], a.most);
-    const uint32_t t = divide(threadIdx.x, per), u = threadIdx.x - t * per.d, beside = kBlock / per.d;
-    const int at = min((int)(16 * u), run - 16);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)x), hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
-    // Where token x of the row lies, or nothing.
-    auto place = [&](const int32_t *pages, int64_t wide, int64_t x) -> char * {
+// What a copy, or a compaction into other pages, moves: token by token, each token a
+// number of runs of bytes, in the keys and in the values alike.  A wave takes `group`
+// tokens: each lane looks one of them up, so that the lists' and the tables' latencies
+// are paid once for all of them, and then the lanes take the tokens' chunks of 16
+// bytes side by side, kDeep loads in flight each.  The last chunk of a run starts
+// early enough to end with it, so runs of any length from 16 bytes on take wide
+// accesses; what two chunks share is written twice, with the same bytes.
+//
+// Bytes bound it, as many written as read.  2048 pages of 64 tokens of 8 heads of 128
+// bfloat16 (0.95 GB): 169 us, 5.6 TB/s, where torch copies whole tensors at 5.3; 2048
+// of 8192 tokens of 32 rows (0.54 GB): 111 us, 4.8 TB/s, reads of 2 KiB here and
+// there.  With a chunk's lists looked up by its own thread 196 and 280 us; with loads
+// and stores through the caches 5 to 10% more; one to eight loads in flight 171, 171,
+// 169 and 174 us.
+constexpr int kDeep = 4;
+template <bool ONCE, typename Look>
+__device__ __forceinline__ void move_tokens(const Look &look, const TokenRuns &r, int64_t head_from, int64_t head_to, int64_t first, int64_t tokens)
+{
+    const int lane = threadIdx.x & 63;
+    const char *from = nullptr;
+    char *to = nullptr;
+    if (lane < tokens)
+        look(first + lane, from, to);
+    if (!from)
+        to = nullptr;
+    const uint32_t items = (uint32_t)tokens * r.token.d;
+    for (uint32_t x0 = lane; x0 - lane < items; x0 += 64 * kDeep) {
+        u4 data[kDeep];
+        char *put[kDeep];
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const uint32_t x = x0 + 64 * j, k = min(divide(x, r.token), 63u), in = x - k * r.token.d, head = divide(in, r.chunks), u = in - head * r.chunks.d;
+            const int64_t at = min((int32_t)(16 * u), r.run - 16);
+            const char *get = (const char *)from_lane((int64_t)from, k) + head * head_from + at;
+            put[j] = (char *)from_lane((int64_t)to, k);
+            if (x >= items)
+                put[j] = nullptr;
+            if (put[j]) {
+                put[j] += head * head_to + at;
+                data[j] = load16<ONCE>(get);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j)
+            if (put[j])
+                store16<ONCE>(put[j], data[j]);
+    }
+}
+
+// Which tokens a wave of a launch takes: the keys' first, then the values'.
+struct Portion {
+    bool values;
+    int64_t first, tokens;
+};
+__device__ __forceinline__ Portion portion(const MoveArgs &m)
+{
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6));
+    const bool values = wave >= m.waves;
+    const int64_t first = (int64_t)(wave - (values ? m.waves : 0)) * m.group;
+    return {values, first, max(min((int64_t)m.group, m.tokens - first), (int64_t)0)};
+}
+
+template <bool ONCE> __global__ __launch_bounds__(kBlock) void k_copy_pages(CopyArgs p)
+{
+    const Portion w = portion(p.m);
+    const TokenRuns &r = w.values ? p.m.v : p.m.k;
+    const CopySide &side = w.values ? p.v : p.k;
+    auto look = [&](int64_t x, const char *&from, char *&to) {
+        const uint32_t i = divide((uint32_t)x, p.page), token = (uint32_t)x - i * p.page.d;
+        const int32_t s = p.src[p.first + i], d = p.dst[p.first + i];
+        if (s < 0 || s >= p.pages || d < 0 || d >= p.into_pages || (p.tokens && (int32_t)token >= p.tokens[p.first + i]))
+            return;
+        from = side.from + s * side.from_page + token * side.from_token;
+        to = side.to + d * side.to_page + token * side.to_token;
+    };
+    move_tokens<ONCE>(look, r, side.from_head, side.to_head, w.first, w.tokens);
+}
+
+// A row's tokens as the compaction reads and writes them: where token x of the row
+// lies, or nothing.
+struct Places {
+    char *pool;
+    int64_t page_bytes, token_bytes;
+    int32_t pages;
+    Divider page;
+    __device__ __forceinline__ char *of(const int32_t *table, int64_t wide, int64_t x) const
+    {
         if (x < 0 || x > INT32_MAX)
             return nullptr;
-        const uint32_t pg = divide((uint32_t)x, p.page);
+        const uint32_t pg = divide((uint32_t)x, page);
         if (pg >= wide)
             return nullptr;
-        const int32_t id = pages[pg];
-        return id < 0 || id >= c.pages ? nullptr : pool + id * page_bytes + (x - (int64_t)pg * c.page) * token_bytes + at;
+        const int32_t id = table[pg];
+        return id < 0 || id >= pages ? nullptr : pool + id * page_bytes + (x - (int64_t)pg * page.d) * token_bytes;
+    }
+};
+
+template <bool ONCE> __global__ __launch_bounds__(kBlock) void k_gather(CompactArgs p)
+{
+    const detfold_compact &a = p.a;
+    const Portion w = portion(p.m);
+    const CompactSide &side = w.values ? p.v : p.k;
+    const Places at = {side.pool, side.page_bytes, side.token_bytes, (int32_t)p.pages, p.page};
+    auto look = [&](int64_t x, const char *&from, char *&to) {
+        const uint32_t row = divide((uint32_t)x, p.most);
+        const int64_t b = p.row0 + row, i = (uint32_t)x - row * p.most.d;
+        if (i >= a.counts[b])
+            return;
+        const int32_t pick = a.picks[b * a.most + i];
+        if (pick < 0)
+            return;
+        const int64_t start = a.starts ? a.starts[b] : 0;
+        to = at.of(a.to + b * a.to_row, a.to_width, start + i);
+        from = to ? at.of(a.table + b * a.table_row, a.table_width, start + pick) : nullptr;
     };
-    for (int64_t i0 = 0; i0 < n; i0 += beside * U) {
+    move_tokens<ONCE>(look, w.values ? p.m.v : p.m.k, side.head_bytes, side.head_bytes, w.first, w.tokens);
+}
+
+// The compaction in place.  A workgroup takes one head's keys or values of one row,
+// and of these as many tokens at a time as its threads hold, U chunks each.  A move
+// goes to a lower token: what is read with a tile of moves lies behind all that
+// earlier tiles wrote, and what it writes before all that later tiles read.  So the
+// one barrier between a tile's loads and its stores is enough, and the next tile's
+// loads go out before this one's stores.
+template <int U> __global__ __launch_bounds__(kBlock) void k_compact(CompactArgs p)
+{
+    const detfold_compact &a = p.a;
+    const uint32_t y = divide(blockIdx.x >> 1, p.heads), head = (blockIdx.x >> 1) - y * p.heads.d;
+    const CompactSide &r = blockIdx.x & 1 ? p.v : p.k;
+    const int64_t b = p.row0 + y;
+    const int32_t *table = a.table + b * a.table_row;
+    const int64_t start = a.starts ? a.starts[b] : 0, n = min((int64_t)a.counts[b], a.most);
+    const uint32_t t = divide(threadIdx.x, r.chunks), u = threadIdx.x - t * r.chunks.d, beside = kBlock / r.chunks.d;
+    const int at = min((int)(16 * u), r.run - 16);
+    const Places places = {r.pool + head * r.head_bytes + at, r.page_bytes, r.token_bytes, (int32_t)p.pages, p.page};
+
+    struct Tile {
         u4 data[U];
         char *put[U];
+    };
+    auto load = [&](int64_t i0) {
+        Tile x;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int64_t i = i0 + j * beside + t;
-            put[j] = nullptr;
+            x.put[j] = nullptr;
+            x.data[j] = u4{};
             if (t >= beside || i >= n)
                 continue;
-            const int64_t pick = a.picks[b * a.most + i];
-            if (a.to ? pick < 0 : pick <= i)
+            const int32_t pick = a.picks[b * a.most + i];
+            if (pick <= i)  // it stays, or is left out
                 continue;
-            const char *from = place(table, width, start + pick);
-            char *x = place(to, to_width, start + i);
-            if (from && x) {
-                put[j] = x;
-                data[j] = *(const u4 *)from;
+            const char *from = places.of(table, a.table_width, start + pick);
+            char *to = places.of(table, a.table_width, start + i);
+            if (from && to) {
+                x.put[j] = to;
+                x.data[j] = *(const u4 *)from;
             }
         }
+        return x;
+    };
+    if (n <= 0)
+        return;
+    Tile now = load(0);
+    for (int64_t i0 = 0; i0 < n; i0 += beside * U) {
+        Tile next = load(i0 + beside * U);
+#pragma unroll
+        for (int j = 0; j < U; ++j)  // what this tile read is there before any of it is written over
+            asm volatile("" : "+v"(now.data[j]));
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (put[j])
-                *(u4 *)put[j] = data[j];
+            if (now.put[j])
+                *(u4 *)now.put[j] = now.data[j];
+        now = next;
     }
 }
 
@@ -117,16 +217,34 @@ bool launch(const void *k, int64_t blocks, void *args, void *stream)
 
 }  // namespace
 
+namespace {
+
+// How a launch's tokens are dealt out: a wave takes up to 64, but no more than leave
+// waves four times over what the device holds at once, nor than 2048 chunks (110.7 us
+// for the 2048 of 8192 tokens, 112.3 with waves once over).
+MoveArgs deal(MoveArgs m, int64_t tokens)
+{
+    constexpr int64_t kWaves = 256 * 64;
+    const int64_t each = m.k.token.d > m.v.token.d ? m.k.token.d : m.v.token.d;
+    m.tokens = tokens;
+    m.group = 64;
+    while (m.group > 1 && (tokens * 2 < kWaves * m.group || each * m.group > 2048))
+        m.group /= 2;
+    const int64_t waves = (tokens + m.group - 1) / m.group, block = kBlock / 64;
+    m.waves = (uint32_t)((waves + block - 1) / block * block);
+    return m;
+}
+
+}  // namespace
+
 int launch_copy_pages(const CopyArgs &a, int64_t count, void *stream)
 {
-    constexpr int U = 4;
     CopyArgs p = a;
-    const int64_t most = a.k.page.d > a.v.page.d ? a.k.page.d : a.v.page.d, some = kMaxItems / most;
+    const int64_t some = kMaxItems / a.page.d;  // pages of a launch
+    const bool once = count * a.page.d * (int64_t)(a.m.k.token.d + a.m.v.token.d) * 16 >= kOnceBytes;
     for (p.first = 0; p.first < count; p.first += some) {
-        p.count = (uint32_t)(count - p.first < some ? count - p.first : some);
-        auto blocks = [&](const CopyRuns &r) { return ((int64_t)p.count * r.page.d + kBlock * U - 1) / (kBlock * U); };
-        p.key_blocks = (uint32_t)blocks(p.k);
-        if (!launch((const void *)k_copy_pages<U>, p.key_blocks + blocks(p.v), &p, stream))
+        p.m = deal(a.m, (count - p.first < some ? count - p.first : some) * a.page.d);
+        if (!launch(once ? (const void *)k_copy_pages<true> : (const void *)k_copy_pages<false>, 2 * (int64_t)p.m.waves / (kBlock / 64), &p, stream))
             return DETFOLD_ELAUNCH;
     }
     return DETFOLD_OK;
@@ -135,10 +253,18 @@ int launch_copy_pages(const CopyArgs &a, int64_t count, void *stream)
 int launch_compact(const CompactArgs &a, void *stream)
 {
     CompactArgs p = a;
-    const int64_t each = 2 * (int64_t)a.c.heads, some = kMaxBlocks / each;
+    if (!a.a.to) {
+        const int64_t each = 2 * (int64_t)a.heads.d, some = kMaxBlocks / each;
+        for (p.row0 = 0; p.row0 < a.a.batch; p.row0 += some)
+            if (!launch((const void *)k_compact<4>, (a.a.batch - p.row0 < some ? a.a.batch - p.row0 : some) * each, &p, stream))
+                return DETFOLD_ELAUNCH;
+        return DETFOLD_OK;
+    }
+    const int64_t some = a.a.most < kMaxItems ? kMaxItems / a.a.most : 1;  // rows of a launch
+    const bool once = a.a.batch * a.a.most * (int64_t)(a.m.k.token.d + a.m.v.token.d) * 16 >= kOnceBytes;
     for (p.row0 = 0; p.row0 < a.a.batch; p.row0 += some) {
-        const int64_t rows = a.a.batch - p.row0 < some ? a.a.batch - p.row0 : some;
-        if (!launch((const void *)k_compact<4>, rows * each, &p, stream))
+        p.m = deal(a.m, (a.a.batch - p.row0 < some ? a.a.batch - p.row0 : some) * a.a.most);
+        if (!launch(once ? (const void *)k_gather<true> : (const void *)k_gather<false>, 2 * (int64_t)p.m.waves / (kBlock / 64), &p, stream))
             return DETFOLD_ELAUNCH;
     }
     return DETFOLD_OK;

@@ -41,6 +41,12 @@ __device__ __forceinline__ float tanh_far(float x)
     return __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), x);
 }
 constexpr float kTanhNear = 1.5f;
+__device__ __forceinline__ float tanh_any(float x)
+{
+    float near = tanh_near(x), far = tanh_far(x);
+    asm("" : "+v"(near), "+v"(far));  // both, without a branch for each
+    return __builtin_fabsf(x) < kTanhNear ? near : far;
+}
 
 // What a query of a column goes by.
 struct Column {
@@ -79,6 +85,10 @@ template <typename C> __device__ __forceinline__ uint32_t finite_word(uint32_t w
         return r;
     }
 }
+
+template <bool B> struct Clean {
+    static constexpr bool value = B;
+};
 
 template <typename C, int QK, int PV, int D, bool TILED, int QT, int MOST, int KEEP>
 __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs)
@@ -123,6 +133,9 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         const char *k0 = (const char *)c.k + (int64_t)h * c.k_head * CS, *v0 = (const char *)c.v + (int64_t)h * c.v_head * CS;
         const int64_t k_page = c.k_page * CS, k_token = c.k_token * CS, v_page = c.v_page * CS, v_token = c.v_token * CS;
         const uint32_t pages = (uint32_t)c.pages;
+        const int c_dim = c.dim;
+        const float cap = p.cap;
+        const bool biased = p.slopes != nullptr;
         const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f);
         const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
 
@@ -302,6 +315,22 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             now = look_up(min(s + turns, steps - 1));
         }
         __syncthreads();
+        // Where they take at most 16 registers the queries are held in them (32 are too many).
+        constexpr bool kHeld = QT * S::kQ <= 16 * 256;
+        constexpr int QW = S::kQ / 1024;
+        u4 held[kHeld ? QT : 1][kHeld ? QW : 1];
+        if constexpr (kHeld)
+#pragma unroll
+            for (int n = 0; n < QT; ++n)
+#pragma unroll
+                for (int i = 0; i < QW; ++i)
+                    held[n][i] = *(const u4 *)(queries + n * S::kQ + i * 1024 + lane * 16);
+        auto query = [&](int n, int i, uint32_t at) {
+            if constexpr (kHeld)
+                return held[n][i];
+            else
+                return *(const u4 *)(queries + n * S::kQ + i * 1024 + at);
+        };
         // Whether some query does not see some token of the step at t0, or sees it at
         // another position than its own; and whether one sees a token of the row.
         auto is_mixed = [&](uint32_t t0) { return (int32_t)(t0 + S::kStep) > base || (int32_t)t0 < low || t0 < begin || t0 + S::kStep > end; };
@@ -309,10 +338,14 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             return ((int32_t)t < base || (mask >> min((int32_t)t - base, 63) & 1)) && at - pos < window;
         };
         bool odd = false;  // whether a mixed step had a value that is infinite or no number
-        // One step; but for the last one it also issues the next one's loads, and
-        // is compiled for that alone (see attend_kernel.h).
-        auto step = [&](auto last_one) {
-            constexpr bool more = !decltype(last_one)::value;
+        // One step, which also issues the next one's loads.  Steps of which all queries
+        // see all, with another behind them, are compiled for that alone: a branch around
+        // the next one's loads would make the wait for the values take the keys issued
+        // after them for values not yet there, and what masks go by would fill the
+        // scalar registers.
+        auto step = [&](auto is_clean) {
+            constexpr bool clean = decltype(is_clean)::value;
+            const bool more = clean || s + turns < steps;
             const uint32_t t0 = a0 + s * S::kStep;
             const uint32_t q_at = anew(lane) * 16;
             // Scores: a row per token, a column per query.
@@ -322,14 +355,13 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
 #pragma unroll
                 for (int u = 0; u < UT; ++u)
                     x[n][u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            // What a lane's loads repeat past the head's end is cleared: there the queries
+            // are zero, but zero times an infinite key would be NaN (an e4m3 key is never
+            // infinite).
+            if (CS != 1 && c_dim < D) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                // Chunks past the head's end are not multiplied, and what the one at
-                // its end repeats is cleared: zero times an infinite key would be NaN.
-                if (4 * E * i >= c.dim)
-                    break;
-                if (CS != 1 && 4 * E * (i + 1) > c.dim) {
-                    const int at = E * (4 * i + anew(grp)), drop = at - min(at, c.dim - E);
+                for (int i = 0; i < NC; ++i) {
+                    const int at = E * (4 * i + anew(grp)), drop = at - min(at, c_dim - E);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t keep = keep_from(CS * drop, j);
@@ -338,12 +370,17 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                             kw[u][i].w[j] &= keep;
                     }
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                if (QK == kF32 && 4 * E * i >= c_dim)  // products that take long and add nothing
+                    break;
                 if constexpr (QK == kF32) {
 #pragma unroll
                     for (int e = 0; e < E; e += 4)
 #pragma unroll
                         for (int n = 0; n < QT; ++n) {
-                            const f4 q = *(const f4 *)(queries + n * S::kQ + (i * (E / 4) + e / 4) * 1024 + q_at);
+                            const f4 q = __builtin_bit_cast(f4, query(n, i * (E / 4) + e / 4, q_at));
 #pragma unroll
                             for (int u = 0; u < UT; ++u)
 #pragma unroll
@@ -362,7 +399,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         for (int n = 0; n < QT; ++n)
 #pragma unroll
                             for (int part = 0; part < (QK == kSplit ? 3 : 1); ++part) {
-                                const u4 q = *(const u4 *)(queries + n * S::kQ + (part * NQ + i * (E / 8) + e / 8) * 1024 + q_at);
+                                const u4 q = query(n, part * NQ + i * (E / 8) + e / 8, q_at);
 #pragma unroll
                                 for (int u = 0; u < UT; ++u)
                                     x[n][u] = mfma16<QK>(k[u], q, x[n][u]);
@@ -370,7 +407,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     }
                 }
             }
-            if constexpr (more) {
+            if (more) {
                 next = look_up(min(s + 2 * turns, steps - 1));
                 load_keys(now);
             }
@@ -382,8 +419,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         x[n][j / 4][j % 4] = f(x[n][j / 4][j % 4]);
             };
             every([&](float z) { return z * by; });
-            if (p.cap > 0.0f) {
-                const float over = 1.0f / p.cap;
+            if (cap > 0.0f) {
+                const float over = __builtin_amdgcn_rcpf(cap);
                 float most = 0.0f;
                 every([&](float z) {
                     z *= over;
@@ -391,14 +428,12 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     return z;
                 });
                 if (__any(!(most < kTanhNear)))
-                    every([&](float z) { return p.cap * (__builtin_fabsf(z) < kTanhNear ? tanh_near(z) : tanh_far(z)); });
+                    every([&](float z) { return cap * tanh_any(z); });
                 else
-                    every([&](float z) { return p.cap * tanh_near(z); });
+                    every([&](float z) { return cap * tanh_near(z); });
             }
-            // Whether all queries see all of the step's tokens, each at its own position.
-            const bool mixed = is_mixed(t0);
             auto token = [&](int j) { return t0 + 16 * (j / 4) + 4 * grp + j % 4; };
-            if (mixed) {
+            if constexpr (!clean) {
                 // Tokens of other parts, or none: their values may be anything.  Zero
                 // times a value that a query does not see would be NaN where that is
                 // infinite or no number: such values count as zero here, and are added
@@ -424,12 +459,12 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         const uint32_t t = anew(token(j));
                         const int32_t pos = (int32_t)t < base ? (int32_t)t : base + depths[min((int32_t)t - base, DETFOLD_MAX_DRAFTS - 1)];
                         float z = x[n][j / 4][j % 4];
-                        if (p.slopes)
+                        if (biased)
                             z += w.slope * (float)(pos - w.at);
                         x[n][j / 4][j % 4] = t >= begin && t < end && sees(w.mask, w.at, t, pos) ? z : -INFINITY;
                     }
                 }
-            } else if (p.slopes) {
+            } else if (biased) {
 #pragma unroll
                 for (int n = 0; n < QT; ++n) {
                     const Column w = columns[16 * n + col];
@@ -517,15 +552,16 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         }
                 }
             }
-            if constexpr (more) {
+            if (more) {
                 load_values(now);
                 now = next;
             }
         };
-        for (; s + turns < steps; s += turns)
-            step(Last<false>{});
-        if (s < steps)
-            step(Last<true>{});
+        for (; s < steps; s += turns) {
+            for (; s + turns < steps && !is_mixed(a0 + s * S::kStep); s += turns)
+                step(Clean<true>{});
+            step(Clean<false>{});
+        }
 
         // The waves' states, joined in order, a tile of columns at a time: each
         // leaves its columns' sums in LDS, over the queries, and a thread takes four
@@ -635,11 +671,8 @@ template <typename C, int QK, int PV, int D, int QT, int MOST, int KEEP> TreeKer
 template <typename C, int QK, int PV, int D> TreeKernel pick_tree_columns(const TreeArgs &a)
 {
     if constexpr (QK != kF32 && QK != kSplit && PV != kF32 && PV != kSplit) {
-        if constexpr (D < 256)
-            if (a.tiles_of == 4)
-                return pick_tree_tiled<C, QK, PV, D, 4, 2, kKeys>(a);
-        if (a.tiles_of >= 2)
-            return pick_tree_tiled<C, QK, PV, D, 2, 2, kKeys>(a);
+        if (a.tiles_of == 2)
+            return a.keep == kAll ? pick_tree_tiled<C, QK, PV, D, 2, 2, kAll>(a) : pick_tree_tiled<C, QK, PV, D, 2, 2, kKeys>(a);
     }
     // A step of one tile is 16 KiB, or 32 of heads above 128.
     constexpr int MOST = D * sizeof(C) <= 128 ? 4 : 2;

@@ -604,8 +604,8 @@ int detfold_tree_workspace(const detfold_paged_cache *cache, int64_t batch, int3
  *   tokens  device, int32 [count], or NULL: only the first tokens[i] slots of the
  *           page are copied
  * The copies run in no order: no page may be both written and read, or written
- * twice, in one call.  Scales of 8-bit caches are not touched.  The keys of a
- * page, and its values, are at most 2^31.
+ * twice, in one call.  Scales of 8-bit caches are not touched.  A page has at most
+ * 2^22 tokens.
  * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP (`into` shares memory with `cache`
  * and is not it; a list lies in a cache), DETFOLD_ELAUNCH.
  */
@@ -622,7 +622,7 @@ int detfold_cache_copy(const detfold_paged_cache *cache, const detfold_paged_cac
  *           as if all tokens were read before any is written; a pick below its own
  *           i is then left out.  Else the moved tokens go to the pages that `to`
  *           names, none of which may be read in this call
- *   picks   device, int32 [batch][most]
+ *   picks   device, int32 [batch][most]; with `to` most is at most 2^22
  *   counts  device, int32 [batch], each taken as 0 .. most
  *   starts  device, int32 [batch], or NULL: 0
  * A move from or to a token that the table, or the cache, does not have is left
