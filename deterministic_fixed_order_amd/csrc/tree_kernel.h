@@ -55,25 +55,29 @@ struct Column {
     float slope;
 };
 
-// Whether a word of the cache holds a value that is no number or infinite.
-template <typename C> __device__ __forceinline__ bool odd_word(uint32_t w)
+// Whether words of the cache hold a value that is infinite or no number: what `seen`
+// gathers from each, and what that says.
+typedef uint16_t h2 __attribute__((ext_vector_type(2)));
+template <typename C> __device__ __forceinline__ uint32_t gather_odd(uint32_t seen, uint32_t w)
 {
-    if constexpr (sizeof(C) == 4) {
-        return (~w & 0x7f800000u) == 0;
-    } else if constexpr (sizeof(C) == 1) {
-        const uint32_t x = ~w & 0x7f7f7f7fu;  // a byte of zero
-        return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
-    } else {
-        const uint32_t x = ~w & (__is_same(C, bf16) ? 0x7f807f80u : 0x7c007c00u);
-        return (x & 0xffffu) == 0 || (x >> 16) == 0;
-    }
+    if constexpr (sizeof(C) == 4)
+        return max(seen, w & 0x7fffffffu);
+    else if constexpr (sizeof(C) == 1)
+        return seen | ((w & 0x7f7f7f7fu) + 0x01010101u);
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(h2, seen), __builtin_bit_cast(h2, w & 0x7fff7fffu)));
+}
+template <typename C> __device__ __forceinline__ bool is_odd(uint32_t seen)
+{
+    constexpr uint32_t top = __is_same(C, bf16) ? 0x7f80u : 0x7c00u;
+    return sizeof(C) == 4 ? seen >= 0x7f800000u : sizeof(C) == 1 ? (seen & 0x80808080u) != 0 : (seen & 0xffffu) >= top || seen >> 16 >= top;
 }
 
 // A word of the cache with zeros in the place of such values.
 template <typename C> __device__ __forceinline__ uint32_t finite_word(uint32_t w)
 {
     if constexpr (sizeof(C) == 4) {
-        return odd_word<C>(w) ? 0u : w;
+        return is_odd<C>(w & 0x7fffffffu) ? 0u : w;
     } else if constexpr (sizeof(C) == 2) {
         constexpr uint32_t top = __is_same(C, bf16) ? 0x7f80u : 0x7c00u;
         return ((w & top) == top ? 0u : w & 0xffffu) | ((w >> 16 & top) == top ? 0u : w & 0xffff0000u);
@@ -85,6 +89,9 @@ template <typename C> __device__ __forceinline__ uint32_t finite_word(uint32_t w
         return r;
     }
 }
+
+// The lowest n of four bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 4)) - 1; }
 
 template <bool B> struct Clean {
     static constexpr bool value = B;
@@ -135,7 +142,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         const uint32_t pages = (uint32_t)c.pages;
         const int c_dim = c.dim;
         const float cap = p.cap;
-        const bool biased = p.slopes != nullptr;
+        const bool biased = p.slopes != nullptr, placed = biased || p.window > 0;  // whether positions matter
         const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f);
         const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
 
@@ -288,7 +295,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     Words<PER * QS> &w = qw[n][i];
 #pragma unroll
                     for (int j = 0; j < PER * QS / 4; ++j)
-                        w.w[j] = 16 * n + col < live ? w.w[j] & keep_from(drop * QS, j) : 0u;
+                        if (c_dim < D)
+                            w.w[j] &= keep_from(drop * QS, j);
                     char *const to = queries + n * S::kQ + lane * 16;
                     if constexpr (QK == kSplit) {
 #pragma unroll
@@ -332,11 +340,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                 return *(const u4 *)(queries + n * S::kQ + i * 1024 + at);
         };
         // Whether some query does not see some token of the step at t0, or sees it at
-        // another position than its own; and whether one sees a token of the row.
+        // another position than its number.
         auto is_mixed = [&](uint32_t t0) { return (int32_t)(t0 + S::kStep) > base || (int32_t)t0 < low || t0 < begin || t0 + S::kStep > end; };
-        auto sees = [&](uint64_t mask, int32_t at, uint32_t t, int32_t pos) {
-            return ((int32_t)t < base || (mask >> min((int32_t)t - base, 63) & 1)) && at - pos < window;
-        };
         bool odd = false;  // whether a mixed step had a value that is infinite or no number
         // One step, which also issues the next one's loads.  Steps of which all queries
         // see all, with another behind them, are compiled for that alone: a branch around
@@ -432,36 +437,71 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                 else
                     every([&](float z) { return cap * tanh_near(z); });
             }
-            auto token = [&](int j) { return t0 + 16 * (j / 4) + 4 * grp + j % 4; };
-            if constexpr (!clean) {
-                // Tokens of other parts, or none: their values may be anything.  Zero
-                // times a value that a query does not see would be NaN where that is
+            if (!clean && is_mixed(t0)) {
+                // Of the lane's four tokens of each tile, bit by bit: which are this part's.
+                // What others hold may be anything.
+                const int first = (int)(anew(grp) * 4 + t0);  // the lane's first token
+                uint32_t ours[UT];
+#pragma unroll
+                for (int u = 0; u < UT; ++u)
+                    ours[u] = low_bits((int)(end - first - 16 * u)) & ~low_bits((int)(begin - first - 16 * u));
+                if (t0 < begin || t0 + S::kStep > end) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint32_t keep = ours[j / 4] & 1u << j % 4 ? ~0u : 0u;
+#pragma unroll
+                        for (int i = 0; i < NP; ++i)
+#pragma unroll
+                            for (int n = 0; n < VW * CS / 4; ++n)
+                                vw[j][i].w[n] &= keep;
+                    }
+                }
+                // Zero times a value that a query does not see would be NaN where that is
                 // infinite or no number: such values count as zero here, and are added
                 // to the sums of those that see them at the end.
+                uint32_t gathered = 0;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint32_t t = token(j);
-                    const bool out = t < begin || t >= end;
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int i = 0; i < NP; ++i)
 #pragma unroll
-                        for (int n = 0; n < VW * CS / 4; ++n) {
-                            const uint32_t v = vw[j][i].w[n], f = finite_word<C>(v);
-                            odd |= !out && f != v;
-                            vw[j][i].w[n] = out ? 0u : f;
-                        }
+                        for (int n = 0; n < VW * CS / 4; ++n)
+                            gathered = gather_odd<C>(gathered, vw[j][i].w[n]);
+                if (__builtin_expect(__any(is_odd<C>(gathered)), 0)) {
+                    odd = true;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < NP; ++i)
+#pragma unroll
+                            for (int n = 0; n < VW * CS / 4; ++n)
+                                vw[j][i].w[n] = finite_word<C>(vw[j][i].w[n]);
                 }
 #pragma unroll
-                for (int n = 0; n < QT; ++n) {
-                    const Column w = columns[16 * n + col];
+                for (int u = 0; u < UT; ++u) {
+                    const int rel = first + 16 * u - base;  // of the first token to the first drafted one
+                    int32_t pos[4] = {};
+                    if (placed) {
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const uint32_t t = anew(token(j));
-                        const int32_t pos = (int32_t)t < base ? (int32_t)t : base + depths[min((int32_t)t - base, DETFOLD_MAX_DRAFTS - 1)];
-                        float z = x[n][j / 4][j % 4];
-                        if (biased)
-                            z += w.slope * (float)(pos - w.at);
-                        x[n][j / 4][j % 4] = t >= begin && t < end && sees(w.mask, w.at, t, pos) ? z : -INFINITY;
+                        for (int j = 0; j < 4; ++j)
+                            pos[j] = rel + j < 0 ? base + rel + j : base + depths[min(rel + j, DETFOLD_MAX_DRAFTS - 1)];
+                    }
+#pragma unroll
+                    for (int n = 0; n < QT; ++n) {
+                        const Column w = columns[16 * n + col];
+                        uint32_t sees = rel >= 0 ? (uint32_t)(w.mask >> min(rel, 63)) : (uint32_t)(w.mask << min(-rel, 4)) | low_bits(-rel);
+                        sees &= ours[u];
+                        if (placed) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                sees &= w.at - pos[j] < window ? ~0u : ~(1u << j);
+                                if (biased)
+                                    x[n][u][j] += w.slope * (float)(pos[j] - w.at);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[n][u][j] = sees & 1u << j ? x[n][u][j] : -INFINITY;
                     }
                 }
             } else if (biased) {
@@ -563,23 +603,21 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             step(Clean<false>{});
         }
 
-        // The waves' states, joined in order, a tile of columns at a time: each
-        // leaves its columns' sums in LDS, over the queries, and a thread takes four
-        // dims of a column from every turn.
+        // The waves' states, joined in order: each leaves its columns' sums in LDS, over
+        // the queries, and a thread takes four dims of a column from every turn.
         f2 *const state = (f2 *)lds;
-        int *const odds = (int *)(lds + waves * 16 * sizeof(f2));
+        int *const odds = (int *)(lds + waves * COLS * sizeof(f2));
         float *const sums = (float *)(odds + 4 * waves);
-        const bool any_bad = __any(bad), any_odd = __any(odd);
+        const bool any_bad = __any(bad);
+        __syncthreads();
 #pragma unroll
         for (int n = 0; n < QT; ++n) {
-            float total = over_groups(l[n], [](float y, float z) { return y + z; });
             const float lift = PV == kF16 ? 0x1p-15f : 1.0f;
-            total *= lift;
+            float total = over_groups(l[n], [](float y, float z) { return y + z; }) * lift;
             if (any_bad)
                 total = __builtin_nanf("");
-            __syncthreads();
             if (16 * n + col < live) {
-                float *mine = sums + (wave * 16 + col) * S::kRow;
+                float *mine = sums + (wave * COLS + 16 * n + col) * S::kRow;
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
 #pragma unroll
@@ -589,65 +627,69 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                             *(f4 *)(mine + VW * (16 * i + 4 * grp + j) + e) =
                                 f4{acc[n][i][e][j], acc[n][i][e + 1][j], acc[n][i][e + 2][j], acc[n][i][e + 3][j]} * lift;
                 if (grp == 0)
-                    state[wave * 16 + col] = f2{m[n], total};
+                    state[wave * COLS + 16 * n + col] = f2{m[n], total};
             }
-            if (lane == 0)
-                odds[wave] = any_odd;
-            __syncthreads();
-            const TreeArgs &p = tree_arguments();
-            const detfold_attend &a = p.a;
-            const int here = min(live - 16 * n, 16);
-            for (int i = 64 * turn + lane; i < here * (D / 4); i += 64 * turns) {
-                const int head = i / (D / 4), at = i % (D / 4) * 4, at0 = at / VW * VW;
-                if (at0 >= p.c.v_dim)
-                    continue;
-                float top = -INFINITY;
-                for (int w = in; w < waves; w += beside)
-                    top = fmaxf(top, state[w * 16 + head].x);
-                const float origin = top == -INFINITY ? 0.0f : top;
-                f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-                float weights = 0.0f;
-                int unfinished = 0;
-                for (int w = in; w < waves; w += beside) {
-                    const f2 ml = state[w * 16 + head];
-                    const float by = weight_of(ml.x - origin);
-                    weights += ml.y * by;
-                    sum += *(const f4 *)(sums + (w * 16 + head) * S::kRow + at) * by;
-                    unfinished |= odds[w];
-                }
-                const int d = min(at0, p.c.v_dim - VW) + at - at0, x = col0 + 16 * n + head, q = (int)divide((uint32_t)x, p.heads_of);
-                if (unfinished) {  // the values that the mixed steps left out
-                    const uint64_t mask = p.masks ? (uint64_t)p.masks[b * p.drafts + q] : ~0ull >> (63 - q);
+        }
+        if (lane == 0)
+            odds[wave] = odd;
+        __syncthreads();
+        const TreeArgs &pe = tree_arguments();
 #pragma unroll 1
-                    for (uint32_t t = begin; t < end; ++t) {
-                        if (!is_mixed(a0 + (t - a0) / S::kStep * S::kStep)) {
-                            t = a0 + ((t - a0) / S::kStep + 1) * S::kStep - 1;
-                            continue;
-                        }
-                        const uint32_t pg = divide(t, p.page), id = (uint32_t)table[pg];
-                        if (id >= pages || !sees(mask, base + depth(q), t, (int32_t)t < base ? (int32_t)t : base + depth((int32_t)t - base)))
-                            continue;
-                        const C *v = (const C *)(v0 + id * v_page + (t - pg * p.page.d) * v_token) + d;
+        for (int i = 64 * turn + lane; i < live * (D / 4); i += 64 * turns) {
+            const TreeArgs &p = pe;
+            const detfold_attend &a = p.a;
+            const int head = i / (D / 4), at = i % (D / 4) * 4, at0 = at / VW * VW;
+            if (at0 >= p.c.v_dim)
+                continue;
+            float top = -INFINITY;
+            for (int w = in; w < waves; w += beside)
+                top = fmaxf(top, state[w * COLS + head].x);
+            const float origin = top == -INFINITY ? 0.0f : top;
+            f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+            float weights = 0.0f;
+            int unfinished = 0;
+            for (int w = in; w < waves; w += beside) {
+                const f2 ml = state[w * COLS + head];
+                const float by = weight_of(ml.x - origin);
+                weights += ml.y * by;
+                sum += *(const f4 *)(sums + (w * COLS + head) * S::kRow + at) * by;
+                unfinished |= odds[w];
+            }
+            const int d = min(at0, p.c.v_dim - VW) + at - at0, x = col0 + head, q = (int)divide((uint32_t)x, p.heads_of);
+            if (unfinished) {  // the values that the mixed steps left out
+                const uint64_t mask = p.masks ? (uint64_t)p.masks[b * p.drafts + q] : ~0ull >> (63 - q);
+                const int32_t own = base + depth(q);
+#pragma unroll 1
+                for (uint32_t t = begin; t < end; ++t) {
+                    const uint32_t s = (t - a0) / S::kStep;
+                    if (!is_mixed(a0 + s * S::kStep)) {
+                        t = a0 + (s + 1) * S::kStep - 1;
+                        continue;
+                    }
+                    const int rel = (int)t - base;
+                    const uint32_t pg = divide(t, p.page), id = (uint32_t)table[pg];
+                    if (id >= pages || (rel >= 0 && !(mask >> min(rel, 63) & 1)) || own - (rel < 0 ? (int)t : base + depth(rel)) >= window)
+                        continue;
+                    const C *v = (const C *)(v0 + id * v_page + (t - pg * p.page.d) * v_token) + d;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float z = to_f32(v[e]);
-                            sum[e] += __builtin_fabsf(z) < INFINITY ? 0.0f : z;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float z = to_f32(v[e]);
+                        sum[e] += __builtin_fabsf(z) < INFINITY ? 0.0f : z;
                     }
                 }
-                if (slot >= 0) {
-                    const int64_t from = slot * p.slot_cols + 16 * n + head;
-                    __builtin_memcpy(p.acc + from * p.c.v_dim + d, &sum, sizeof(sum));
-                    if (at == 0)
-                        p.ml[from] = make_float2(top, weights);
-                } else {
-                    const int g = (int)h * p.group + x - q * p.group;
-                    const float by = out_scale(v_scale, weights);
-                    const float o[4] = {sum.x * by, sum.y * by, sum.z * by, sum.w * by};
-                    put_out<4>(a, b * a.out_row + q * p.out_draft + (int64_t)g * a.out_head + d, o);
-                    if (a.lse && at == 0)
-                        a.lse[(b * p.drafts + q) * a.q_heads + g] = log_sum(top, weights);
-                }
+            }
+            if (slot >= 0) {
+                const int64_t from = slot * p.slot_cols + head;
+                __builtin_memcpy(p.acc + from * p.c.v_dim + d, &sum, sizeof(sum));
+                if (at == 0)
+                    p.ml[from] = make_float2(top, weights);
+            } else {
+                const int g = (int)h * p.group + x - q * p.group;
+                const float by = out_scale(v_scale, weights);
+                const float o[4] = {sum.x * by, sum.y * by, sum.z * by, sum.w * by};
+                put_out<4>(a, b * a.out_row + q * p.out_draft + (int64_t)g * a.out_head + d, o);
+                if (a.lse && at == 0)
+                    a.lse[(b * p.drafts + q) * a.q_heads + g] = log_sum(top, weights);
             }
         }
         mine.left -= done;
@@ -666,7 +708,7 @@ template <typename C, int QK, int PV, int D, int QT, int MOST, int KEEP> TreeKer
 {
     typedef Attend<C, QK, PV, D, true, MOST, KEEP> S;
     const void *f = a.tiled ? (const void *)k_tree<C, QK, PV, D, true, QT, MOST, KEEP> : (const void *)k_tree<C, QK, PV, D, false, QT, MOST, KEEP>;
-    return {f, QT * (S::kQ + 16 * (int)sizeof(Column)), 16 * (8 + S::kRow * 4) + 16};
+    return {f, QT * (S::kQ + 16 * (int)sizeof(Column)), 16 * QT * (8 + S::kRow * 4) + 16};
 }
 template <typename C, int QK, int PV, int D> TreeKernel pick_tree_columns(const TreeArgs &a)
 {
