@@ -52,12 +52,15 @@ bool same_cache(const detfold_paged_cache &a, const detfold_paged_cache &b)
 
 namespace {
 
-// Tiles of 16 queries to a wave: two, which share what is loaded, where the products
-// are of 16 bits and there are as many queries.  Four do not fit the registers with
-// eight waves to a compute unit (1 x 16 tokens over 131072 took 163 us with four, 139
-// with two).  Products in float32, and in parts, are what bounds one tile already.
-// One token a row is split as attend_paged splits it, in the same workspace.
-int tiles_of(int64_t cols, int32_t drafts, bool narrow) { return narrow && drafts > 1 && cols > 16 ? 2 : 1; }
+// Whether heads are whole chunks of 16 bytes, at such addresses.
+bool tree_staged(const detfold_paged_cache &c)
+{
+    const int64_t of = 16 / elem_size(c.type);
+    for (int64_t x : {c.k_page, c.k_token, c.k_head, c.v_page, c.v_token, c.v_head, (int64_t)c.dim, (int64_t)c.v_dim})
+        if (x % of != 0)
+            return false;
+    return aligned(c.k, 16) && aligned(c.v, 16) && c.dim <= 128 && c.v_dim <= 128;
+}
 
 }  // namespace
 
@@ -72,21 +75,39 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     if (drafts < 1 || drafts > DETFOLD_MAX_DRAFTS || max_len > kMaxCount - 1 - DETFOLD_MAX_DRAFTS || !types_pair(type, c.type) ||
         (out_type != type && out_type != DETFOLD_F32))
         return DETFOLD_EINVAL;
-    const int64_t cols = (int64_t)drafts * (q_heads / c.heads);
-    const int head = c.dim > c.v_dim ? c.dim : c.v_dim, wide_head = head <= 64 ? 64 : head <= 128 ? 128 : 256;
-    const int tiles = tiles_of(cols, drafts, type != DETFOLD_F32 && out_type != DETFOLD_F32);
-    const int64_t units = c.heads * ((cols + 16 * tiles - 1) / (16 * tiles));
-    const int64_t queries = c.heads * (cols > 16 ? (cols + 31) / 32 * 32 : cols);  // at least units times a slot's
+    const int64_t cols = (int64_t)drafts * (q_heads / c.heads), queries = c.heads * (cols > 16 ? (cols + 255) / 32 * 32 : cols);
     if (batch > 0 && queries > kMaxElems / 16 / batch)
         return DETFOLD_EINVAL;
-    const int64_t seen = window > 0 && window < max_len - (drafts - 1) ? window + drafts - 1 : max_len;
-    const int64_t per_cu = tree_heavy(tiles, wide_head) ? kWavesPerCu / 2 : kWavesPerCu, full = cu_count, waves = full * per_cu;
+    const int head = c.dim > c.v_dim ? c.dim : c.v_dim, wide_head = head <= 64 ? 64 : head <= 128 ? 128 : 256;
+    const int64_t seen = window > 0 && window < max_len - (drafts - 1) ? window + drafts - 1 : max_len, full = cu_count;
+    // Two tiles of 16 queries to a wave share what is loaded, where the products are
+    // of 16 bits and there are as many queries.  Four do not fit the registers with
+    // eight waves to a compute unit (1 x 16 tokens over 131072 took 163 us with four,
+    // 139 with two).  Products in float32, and in parts, are what bounds one tile
+    // already.  Where one step for every wave that the device holds is enough, its
+    // time is the code's, which one tile has less of (1 x 8 over 1000: FIGURE us, 20
+    // with two).  One token a row is split as attend_paged splits it, in the same
+    // workspace.
+    const bool narrow = type != DETFOLD_F32 && out_type != DETFOLD_F32;
+    const bool once = split == 0 && batch * ((seen + 31) / 32) <= full * kWavesPerCu / (c.heads * ((cols + 15) / 16));
+    const int tiles = narrow && drafts > 1 && cols > 16 && !once ? 2 : 1;
+    int64_t of_head = (cols + 16 * tiles - 1) / (16 * tiles);  // units of a key-value head
+    // More units than two of a key-value head take its tokens from LDS together (32 x 64
+    // over 4096: FIGURE us, 377 straight to registers; two would hold too much on the
+    // way in registers: 1 x 16 over 131072 took 164 us, 127 so).
+    const int most_shared = wide_head * elem_size(c.type) >= 128 ? 8 : 4;
+    p->shared = tiles < 2 || of_head < 3 || !tree_staged(c) ? 0 : of_head <= 4 || most_shared == 4 ? 4 : 8;
+    if (p->shared)
+        of_head = (of_head + p->shared - 1) / p->shared * p->shared;
+    const int64_t units = c.heads * of_head;
+    // Heads above 128 leave a compute unit's registers four waves.
+    const int64_t per_cu = tree_heavy(tiles, wide_head) ? kWavesPerCu / 2 : kWavesPerCu, waves = full * per_cu;
     p->tiles_of = tiles;
     p->slot_cols = (int32_t)(cols < 16 * tiles ? cols : 16 * tiles);
     p->units = batch * units;
     p->shares = 0;
     p->waves = (int32_t)per_cu;
-    p->beside = units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
+    p->beside = p->shared ? p->shared : units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
     p->brief = seen <= 32;
     const int64_t groups = units / p->beside;
     const int fit = 1024 / (wide_head * elem_size(c.type)), most_tiles = tiles > 1 || wide_head == 256 ? 2 : 4;
@@ -95,7 +116,7 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     if (split == 0) {
         if (seen <= few || (batch * groups >= full && seen <= kShortRow)) {
             part = seen;
-        } else if (batch > 0 && batch * ((seen + 31) / 32) <= waves / units) {
+        } else if (batch > 0 && !p->shared && batch * ((seen + 31) / 32) <= waves / units) {
             part = DETFOLD_ATTEND_STEP;
             p->brief = true;
             p->waves = p->beside;
@@ -120,7 +141,7 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
         return DETFOLD_EINVAL;
     int64_t upto = most > 1 ? (most < kMaxBlocks ? most : kMaxBlocks) * queries * batch : 0;
     if (split == 0) {
-        const int64_t capped = kMaxBlocks * 32 + 2 * queries * batch, even = kWavesPerCu * cu_count * (cols < 32 ? cols : 32);
+        const int64_t capped = kMaxBlocks * 32 + 2 * queries * batch, even = kWavesPerCu * 2 * cu_count * (cols < 32 ? cols : 32);
         upto = upto > capped ? capped : upto;
         upto = upto > even ? upto : even;
     }
@@ -344,6 +365,7 @@ int detfold_attend_tree(const detfold_paged_cache *cache, const detfold_tree *ar
     k.page = divider((uint32_t)cache->page);
     k.tiles_of = p.tiles_of;
     k.slot_cols = p.slot_cols;
+    k.shared = p.shared;
     k.tiles = divider((uint32_t)(units / cache->heads));
     k.beside = p.beside;
     k.units = divider((uint32_t)(units / p.beside));
@@ -351,7 +373,7 @@ int detfold_attend_tree(const detfold_paged_cache *cache, const detfold_tree *ar
     k.shares = p.shares ? divider((uint32_t)p.shares) : Divider{0, 0, 0};
     k.brief = p.brief;
     k.split = p.split;
-    k.tiled = attend_tiled(*cache);
+    k.tiled = attend_tiled(*cache) && !p.shared;
     k.keep = attend_keep(*cache, k.tiles.d, k.brief);
     k.waves = p.waves;
     const int64_t queries = p.slots * p.slot_cols;

@@ -20,6 +20,7 @@ struct TreeArgs : AttendArgs {
     float cap;
     int32_t drafts;
     int32_t tiles_of;    // tiles of 16 queries of a unit
+    int32_t shared;      // units of a key-value head that take its tokens from LDS together, or 0
     int32_t slot_cols;   // queries of a slot, see AttendArgs
     Divider heads_of;    // query heads of a key-value head
     Divider join_blocks; // workgroups of the join for a row's queries
@@ -29,11 +30,11 @@ struct TreeArgs : AttendArgs {
 // dims leave a compute unit's registers four waves, not eight.
 constexpr bool tree_heavy(int tiles, int head) { return tiles * head > 256 || head > 128; }
 
-// A kernel of the attention of drafted tokens and the LDS it takes: for a unit's
-// queries, and for a wave's sums.
+// A kernel of the attention of drafted tokens and the LDS it takes: for staged tokens
+// and a unit's queries, and for a wave's sums.
 struct TreeKernel {
     const void *f;
-    int unit_bytes, wave_bytes;
+    int staged_bytes, unit_bytes, wave_bytes;
 };
 TreeKernel tree_bf16(const TreeArgs &a);
 TreeKernel tree_f16(const TreeArgs &a);
@@ -41,7 +42,7 @@ TreeKernel tree_f32(const TreeArgs &a);
 
 struct TreePlan : detfold_attend_plan {
     int64_t shares, slots;
-    int32_t waves, beside, tiles_of, slot_cols;
+    int32_t waves, beside, tiles_of, slot_cols, shared;
     bool brief;
 };
 

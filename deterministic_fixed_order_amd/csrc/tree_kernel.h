@@ -25,34 +25,34 @@ __device__ __forceinline__ const TreeArgs &tree_arguments()
     return *(const TreeArgs *)(TreeArgsPtr)p;
 }
 
-// tanh(x), to 24 units in the last place (tested over all magnitudes): the [7/6]
-// fraction of its continued fraction below 1.5, off by 2^-25 there; above, from
-// exp(-2 |x|), whose rounding is at most a tenth of the result.
-__device__ __forceinline__ float tanh_near(float x)
+// tanh, held to 24 units of 2^-24 relative.  Below 0.5 x + x^3 P(x^2), whose four
+// coefficients were fitted to the smallest relative error (1.3 units there); above
+// from exp(-2 |x|), of which the largest, e^-1, gives 4.
+__device__ __forceinline__ float tanh_factor(float z)  // P(z)
 {
-    const float z = x * x;
-    const float over = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 1.0f, 378.0f), z, 17325.0f), z, 135135.0f);
-    const float under = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 28.0f, 3150.0f), z, 62370.0f), z, 135135.0f);
-    return x * over * __builtin_amdgcn_rcpf(under);
+    return __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 0.0172357764f, -0.0530423597f), z, 0.133258238f), z, -0.333331406f);
 }
-__device__ __forceinline__ float tanh_far(float x)
-{
-    const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * (-2.0f * kLog2e));
-    return __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), x);
-}
-constexpr float kTanhNear = 1.5f;
 __device__ __forceinline__ float tanh_any(float x)
 {
-    float near = tanh_near(x), far = tanh_far(x);
+    const float z = x * x, e = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * (-2.0f * kLog2e));
+    float near = __builtin_fmaf(x * z, tanh_factor(z), x), far = __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), x);
     asm("" : "+v"(near), "+v"(far));  // both, without a branch for each
-    return __builtin_fabsf(x) < kTanhNear ? near : far;
+    return z < 0.25f ? near : far;
 }
+
+// The nearest finite number: zero times it is zero.
+__device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -0x1.fffffep127f), 0x1.fffffep127f); }
+
+// Scores are held times log2 e here, so that a weight is exp2 of a distance: a score
+// of more than 2^127 / log2 e counts as infinite.
+__device__ __forceinline__ float weight2_of(float s) { return __builtin_amdgcn_exp2f(s); }
+__device__ __forceinline__ float log_sum2(float m, float l) { return (m == -INFINITY ? 0.0f : m * 0.693147181f) + logf(l); }
 
 // What a query of a column goes by.
 struct Column {
     uint64_t mask;
     int32_t at;  // its position
-    float slope;
+    float slope;  // times log2 e
 };
 
 // Whether words of the cache hold a value that is infinite or no number: what `seen`
@@ -90,19 +90,52 @@ template <typename C> __device__ __forceinline__ uint32_t finite_word(uint32_t w
     }
 }
 
+// A barrier for what the workgroup keeps in LDS: loads on their way stay on it.
+__device__ __forceinline__ void meet_in_lds()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <bool FIRST, typename A, typename B> __device__ __forceinline__ auto &this_one(A &a, B &b)
+{
+    if constexpr (FIRST)
+        return a;
+    else
+        return b;
+}
+
 // The lowest n of four bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 4)) - 1; }
+
+// What SHARE waves stage of a step's 32 tokens: keys and values in chunks of 16 bytes,
+// kChunks of each thread, in two buffers of LDS, the next step's on their way in
+// registers meanwhile.  Straight to registers, as for fewer queries, every wave would
+// load all of it, and a load of keys, 16 tokens by 4 chunks, is 64 accesses of the
+// compute unit's cache where one of neighbours is 16: 32 rows of 64 drafted tokens
+// over 4096 kept it 81% busy.  Keys lie so that the 16 tokens' same chunks are on
+// different banks: a token's chunk c in the place of c ^ key(token).
+template <typename C, int D, int SHARE> struct Staged {
+    static constexpr int kRow = D * sizeof(C), kPerRow = kRow / 16, kTile = 32 * kRow;
+    static constexpr int kChunks = SHARE ? kPerRow / SHARE : 1, kIds = kChunks > 1 ? kChunks / 2 : 1;
+    static constexpr int kBytes = SHARE ? 2 * (8 / SHARE) * 2 * kTile : 0;  // of a workgroup
+    static __device__ __forceinline__ int key(int token) { return kPerRow >= 16 ? token & 15 : token / (kPerRow < 16 ? 16 / kPerRow : 1) & (kPerRow - 1); }
+};
 
 template <bool B> struct Clean {
     static constexpr bool value = B;
 };
 
-template <typename C, int QK, int PV, int D, bool TILED, int QT, int MOST, int KEEP>
+// SHARE: 0, or the units of a workgroup that are one key-value head's and take its
+// tokens from LDS together (see Staged).
+template <typename C, int QK, int PV, int D, bool TILED, int QT, int MOST, int KEEP, int SHARE>
 __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs)
 {
     typedef Attend<C, QK, PV, D, TILED, MOST, KEEP> S;
     constexpr int CS = S::kSize, E = S::kChunk, NC = S::kChunks, UT = S::kTiles, VW = S::kWide, NP = S::kParts, NT = S::kTokens;
     constexpr int COLS = 16 * QT;
+    typedef Staged<C, D, SHARE> T;
     extern __shared__ __align__(16) char lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const TreeArgs &p0 = tree_arguments();
@@ -143,7 +176,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         const int c_dim = c.dim;
         const float cap = p.cap;
         const bool biased = p.slopes != nullptr, placed = biased || p.window > 0;  // whether positions matter
-        const float by = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f);
+        const float scale = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f), by = finite(scale * kLog2e);
+        const float over = cap > 0.0f ? finite(scale / cap) : 0.0f;  // of a product, to the argument of the tanh
         const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
 
         // Where a lane's loads lie within a key and a value.
@@ -177,22 +211,23 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             begin = (uint32_t)min(x, (int64_t)end), end = (uint32_t)min(x + p.split, (int64_t)end);
         }
         const uint32_t a0 = TILED ? begin & ~15u : begin, last = end > 0 ? end - 1 : 0;
-        const uint32_t steps = end > begin && live > 0 ? (end - a0 + S::kStep - 1) / S::kStep : 0;
+        const uint32_t steps = end > begin && (SHARE || live > 0) ? (end - a0 + S::kStep - 1) / S::kStep : 0;
         // Tokens below `low` are behind some query's window; a distance of `window` hides.
         const int32_t window = p.window > 0 ? (int32_t)min(p.window, (int64_t)INT32_MAX) : INT32_MAX;
         const int32_t low = p.window > 0 ? (int32_t)max((int64_t)base + (p.depths ? DETFOLD_MAX_DRAFTS : p.drafts) - window, (int64_t)0) : 0;
 
         // The columns, and the drafted tokens' depths, which all waves share.
-        char *const queries = lds + in * (QT * S::kQ);
-        Column *const columns = (Column *)(lds + beside * (QT * S::kQ)) + in * COLS;
-        int32_t *const depths = (int32_t *)(lds + beside * (QT * S::kQ + COLS * (int)sizeof(Column)));
+        constexpr int kUnitQueries = SHARE ? 0 : QT * S::kQ;
+        char *const queries = lds + in * kUnitQueries;
+        Column *const columns = (Column *)(lds + T::kBytes + beside * kUnitQueries) + in * COLS;
+        int32_t *const depths = (int32_t *)(lds + T::kBytes + beside * (kUnitQueries + COLS * (int)sizeof(Column)));
         auto depth = [&](int j) { return p.depths ? min(max(p.depths[b * p.drafts + j], 0), DETFOLD_MAX_DRAFTS - 1) : j; };
         if (turn == 0 && lane < live) {
             const int i = (int)divide((uint32_t)(col0 + lane), p.heads_of);
             Column x;
             x.mask = p.masks ? (uint64_t)p.masks[b * p.drafts + i] : ~0ull >> (63 - i);
             x.at = base + depth(i);
-            x.slope = p.slopes ? p.slopes[h * p.group + (col0 + lane - i * p.group)] : 0.0f;
+            x.slope = p.slopes ? p.slopes[h * p.group + (col0 + lane - i * p.group)] * kLog2e : 0.0f;
             columns[lane] = x;
         }
         if (wave == 0)
@@ -210,7 +245,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             const char *q = (const char *)a.q + (b * a.q_row + i * p.q_draft + ((int64_t)h * p.group + (x - i * p.group)) * a.q_head) * QS;
 #pragma unroll
             for (int i = 0; i < NQ; ++i)
-                if (live > 0 && ((n * NQ + i) & (turns - 1)) == turn)
+                if (live > 0 && (SHARE || ((n * NQ + i) & (turns - 1)) == turn))
                     __builtin_memcpy(&qw[n][i], q + (min(query_chunk(i), c.dim - E) + i * PER % E) * QS, PER * QS);
         }
 
@@ -267,6 +302,51 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             }
         };
 
+        // The staged chunks of this thread, of step s: the pages of their tokens, their
+        // loads, and their stores to a buffer.
+        struct Ids {
+            int32_t id[T::kIds];
+        };
+        auto staged_place = [&]() { return anew(in * 64 + lane); };  // of this thread among those that stage together
+        auto staged_token = [&](int place, int k) { return (place + k * 64 * SHARE) / T::kPerRow & 31; };
+        auto staged_at = [&](int place, uint32_t s, int k) { return min(a0 + min(s, steps - 1) * 32 + staged_token(place, k), last); };
+        auto staged_values = [&](int place, int k) { return T::kChunks > 1 ? k >= T::kChunks / 2 : place >= 32 * T::kPerRow; };
+        auto stage_ids = [&](uint32_t s) {
+            const int place = staged_place();
+            Ids g;
+#pragma unroll
+            for (int k = 0; k < T::kIds; ++k)
+                g.id[k] = table[divide(staged_at(place, s, k), p.page)];
+            return g;
+        };
+        u4 staged[T::kChunks];
+        auto stage_load = [&](uint32_t s, const Ids &g) {
+            const int place = staged_place();
+#pragma unroll
+            for (int k = 0; k < T::kChunks; ++k) {
+                const uint32_t t = staged_at(place, s, k % T::kIds);
+                const int64_t off = t - divide(t, p.page) * p.page.d, id = valid(g.id[k % T::kIds]);
+                const int c = (place + k * 64 * SHARE) % T::kPerRow;
+                const bool values = staged_values(place, k);
+                const char *from = (values ? v0 + id * v_page + off * v_token : k0 + id * k_page + off * k_token) +
+                                   min(16 * c, (values ? p.c.v_dim : c_dim) * CS - 16);
+                const Words<16> w = load_words<16, false>(from);
+                staged[k] = u4{w.w[0], w.w[1], w.w[2], w.w[3]};
+            }
+        };
+        auto buffer = [&](uint32_t round) { return lds + ((round & 1) * turns + turn) * (2 * T::kTile); };
+        auto stage_store = [&](uint32_t round) {
+            const int place = staged_place();
+#pragma unroll
+            for (int k = 0; k < T::kChunks; ++k) {
+                const int c = (place + k * 64 * SHARE) % T::kPerRow, t = staged_token(place, k);
+                const bool values = staged_values(place, k);
+                if (c_dim < D)  // past the head's end: zeros
+                    staged[k] &= !values && 16 * c >= c_dim * CS ? 0u : ~0u;
+                *(u4 *)(buffer(round) + (values ? T::kTile : 0) + t * T::kRow + 16 * (values ? c : c ^ T::key(t))) = staged[k];
+            }
+        };
+
         // Weights of 16-bit floats are held 2^15 times larger, so that small ones
         // keep their digits; the sum is too, and both are put right at the end.
         constexpr int kLift = PV == kF16 ? 15 : 0;
@@ -283,14 +363,27 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         }
 
         uint32_t s = turn;
+        const uint32_t rounds = SHARE ? (steps + turns - 1) / turns : 0;  // steps of each of the workgroup's waves
         Pages now = {}, next = {};
-        if (s < steps)
+        Ids ids = {};
+        if constexpr (SHARE) {
+            if (rounds) {
+                ids = stage_ids(s);
+                stage_load(s, ids);
+                ids = stage_ids(s + turns);
+            }
+        } else if (s < steps) {
             now = look_up(s);
+            load_keys(now);
+            load_values(now);
+            now = look_up(min(s + turns, steps - 1));
+        }
+        __builtin_amdgcn_sched_barrier(0);  // the first loads are on their way while the queries arrive
 #pragma unroll
         for (int n = 0; n < QT; ++n)
 #pragma unroll
             for (int i = 0; i < NQ; ++i)
-                if (((n * NQ + i) & (turns - 1)) == turn) {
+                if (SHARE || ((n * NQ + i) & (turns - 1)) == turn) {
                     const int drop = query_chunk(i) - min(query_chunk(i), c.dim - E) - i * PER % E;
                     Words<PER * QS> &w = qw[n][i];
 #pragma unroll
@@ -298,7 +391,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         if (c_dim < D)
                             w.w[j] &= keep_from(drop * QS, j);
                     char *const to = queries + n * S::kQ + lane * 16;
-                    if constexpr (QK == kSplit) {
+                    if constexpr (SHARE) {
+                    } else if constexpr (QK == kSplit) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)  // a NaN whose bits all lie below the first part's would be an infinity there
                             w.w[j] = __builtin_isnan(__builtin_bit_cast(float, w.w[j])) ? 0x7fc00000u : w.w[j];
@@ -316,23 +410,29 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         *(u4 *)(to + i * 1024) = u4{w.w[0], w.w[1], w.w[2], w.w[3]};
                     }
                 }
-        __builtin_amdgcn_sched_barrier(0);  // else the queries' registers add to those of the loads below
-        if (s < steps) {
-            load_keys(now);
-            load_values(now);
-            now = look_up(min(s + turns, steps - 1));
+        if constexpr (SHARE) {
+            if (rounds) {
+                stage_store(0);
+                stage_load(s + turns, ids);
+                ids = stage_ids(s + 2 * turns);
+            }
         }
         __syncthreads();
-        // Where they take at most 16 registers the queries are held in them (32 are too many).
-        constexpr bool kHeld = QT * S::kQ <= 16 * 256;
+        // The queries are held in registers where those have room: 16 beside a step's
+        // keys and values (32 are too many), and 32 where these come from LDS.
+        constexpr bool kHeld = SHARE || QT * S::kQ <= 16 * 256;
         constexpr int QW = S::kQ / 1024;
         u4 held[kHeld ? QT : 1][kHeld ? QW : 1];
         if constexpr (kHeld)
 #pragma unroll
             for (int n = 0; n < QT; ++n)
 #pragma unroll
-                for (int i = 0; i < QW; ++i)
-                    held[n][i] = *(const u4 *)(queries + n * S::kQ + i * 1024 + lane * 16);
+                for (int i = 0; i < QW; ++i) {
+                    if constexpr (SHARE)
+                        held[n][i] = u4{qw[n][i].w[0], qw[n][i].w[1], qw[n][i].w[2], qw[n][i].w[3]};
+                    else
+                        held[n][i] = *(const u4 *)(queries + n * S::kQ + i * 1024 + lane * 16);
+                }
         auto query = [&](int n, int i, uint32_t at) {
             if constexpr (kHeld)
                 return held[n][i];
@@ -350,9 +450,24 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         // scalar registers.
         auto step = [&](auto is_clean) {
             constexpr bool clean = decltype(is_clean)::value;
-            const bool more = clean || s + turns < steps;
+            const bool more = !SHARE && (clean || s + turns < steps);
             const uint32_t t0 = a0 + s * S::kStep;
-            const uint32_t q_at = anew(lane) * 16;
+                        const char *const tile = buffer(s / turns);
+            const int here = anew(lane), col = here & 15, grp = here >> 4;
+            const uint32_t q_at = here * 16;
+            // Staged tokens come to registers here; others are there, held across steps.
+            Words<16> keys_here[SHARE ? UT : 1][SHARE ? NC : 1];
+            Words<VW * CS> values_here[SHARE ? NT : 1][SHARE ? NP : 1];
+            auto &kr = this_one<(SHARE > 0)>(keys_here, kw);
+            auto &vr = this_one<(SHARE > 0)>(values_here, vw);
+            if constexpr (SHARE) {
+                const int at = (grp ^ T::key(col)) * 16;
+#pragma unroll
+                for (int u = 0; u < UT; ++u)
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+                        __builtin_memcpy(&kr[u][i], tile + (16 * u + col) * T::kRow + (at ^ 64 * i), 16);
+            }
             // Scores: a row per token, a column per query.
             f4 x[QT][UT];
 #pragma unroll
@@ -363,16 +478,16 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             // What a lane's loads repeat past the head's end is cleared: there the queries
             // are zero, but zero times an infinite key would be NaN (an e4m3 key is never
             // infinite).
-            if (CS != 1 && c_dim < D) {
+            if (!SHARE && CS != 1 && c_dim < D) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    const int at = E * (4 * i + anew(grp)), drop = at - min(at, c_dim - E);
+                    const int at = E * (4 * i + grp), drop = at - min(at, c_dim - E);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t keep = keep_from(CS * drop, j);
 #pragma unroll
                         for (int u = 0; u < UT; ++u)
-                            kw[u][i].w[j] &= keep;
+                            kr[u][i].w[j] &= keep;
                     }
                 }
             }
@@ -390,7 +505,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                             for (int u = 0; u < UT; ++u)
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    x[n][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(kw[u][i].w, e + j), q[j], x[n][u], 0, 0, 0);
+                                    x[n][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(kr[u][i].w, e + j), q[j], x[n][u], 0, 0, 0);
                         }
                 } else {
 #pragma unroll
@@ -398,8 +513,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         u4 k[UT];
 #pragma unroll
                         for (int u = 0; u < UT; ++u)
-                            k[u] = u4{pair16<C, QK>(kw[u][i].w, e / 2), pair16<C, QK>(kw[u][i].w, e / 2 + 1),
-                                      pair16<C, QK>(kw[u][i].w, e / 2 + 2), pair16<C, QK>(kw[u][i].w, e / 2 + 3)};
+                            k[u] = u4{pair16<C, QK>(kr[u][i].w, e / 2), pair16<C, QK>(kr[u][i].w, e / 2 + 1),
+                                      pair16<C, QK>(kr[u][i].w, e / 2 + 2), pair16<C, QK>(kr[u][i].w, e / 2 + 3)};
 #pragma unroll
                         for (int n = 0; n < QT; ++n)
 #pragma unroll
@@ -423,24 +538,34 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     for (int j = 0; j < NT; ++j)
                         x[n][j / 4][j % 4] = f(x[n][j / 4][j % 4]);
             };
-            every([&](float z) { return z * by; });
             if (cap > 0.0f) {
-                const float over = __builtin_amdgcn_rcpf(cap);
                 float most = 0.0f;
                 every([&](float z) {
-                    z *= over;
                     most = fmaxf(most, __builtin_fabsf(z));
                     return z;
                 });
-                if (__any(!(most < kTanhNear)))
-                    every([&](float z) { return cap * tanh_any(z); });
+                if (__any(!(most * __builtin_fabsf(over) < 0.5f)))
+                    every([&](float z) { return cap * kLog2e * tanh_any(z * over); });
                 else
-                    every([&](float z) { return cap * tanh_near(z); });
+                    every([&](float z) {
+                        const float y = z * over, straight = z * by;
+                        return __builtin_fmaf(straight * (y * y), tanh_factor(y * y), straight);
+                    });
+            } else {
+                every([&](float z) { return z * by; });
+            }
+            if constexpr (SHARE) {
+                __builtin_amdgcn_sched_barrier(0);  // the values take the keys' registers
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        __builtin_memcpy(&vr[j][i], tile + T::kTile + (16 * (j / 4) + 4 * grp + j % 4) * T::kRow + VW * (16 * i + col) * CS, VW * CS);
             }
             if (!clean && is_mixed(t0)) {
                 // Of the lane's four tokens of each tile, bit by bit: which are this part's.
                 // What others hold may be anything.
-                const int first = (int)(anew(grp) * 4 + t0);  // the lane's first token
+                const int first = (int)(grp * 4 + t0);  // the lane's first token
                 uint32_t ours[UT];
 #pragma unroll
                 for (int u = 0; u < UT; ++u)
@@ -453,7 +578,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         for (int i = 0; i < NP; ++i)
 #pragma unroll
                             for (int n = 0; n < VW * CS / 4; ++n)
-                                vw[j][i].w[n] &= keep;
+                                vr[j][i].w[n] &= keep;
                     }
                 }
                 // Zero times a value that a query does not see would be NaN where that is
@@ -466,7 +591,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     for (int i = 0; i < NP; ++i)
 #pragma unroll
                         for (int n = 0; n < VW * CS / 4; ++n)
-                            gathered = gather_odd<C>(gathered, vw[j][i].w[n]);
+                            gathered = gather_odd<C>(gathered, vr[j][i].w[n]);
                 if (__builtin_expect(__any(is_odd<C>(gathered)), 0)) {
                     odd = true;
 #pragma unroll
@@ -475,7 +600,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         for (int i = 0; i < NP; ++i)
 #pragma unroll
                             for (int n = 0; n < VW * CS / 4; ++n)
-                                vw[j][i].w[n] = finite_word<C>(vw[j][i].w[n]);
+                                vr[j][i].w[n] = finite_word<C>(vr[j][i].w[n]);
                 }
 #pragma unroll
                 for (int u = 0; u < UT; ++u) {
@@ -524,7 +649,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                 top = fmaxf(m[n], over_groups(top, [](float y, float z) { return fmaxf(y, z); }));
                 const float origin = top == -INFINITY ? 0.0f : top;
                 if (__any(top > m[n])) {
-                    const float turn = weight_of(m[n] - origin);
+                    const float turn = weight2_of(m[n] - origin);
                     l[n] *= turn;
 #pragma unroll
                     for (int i = 0; i < NP; ++i)
@@ -535,7 +660,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    x[n][j / 4][j % 4] = weight_of<kLift>(x[n][j / 4][j % 4] - origin);
+                    x[n][j / 4][j % 4] = weight2_of(x[n][j / 4][j % 4] - origin + (float)kLift);
                     l[n] += x[n][j / 4][j % 4];
                 }
             }
@@ -549,7 +674,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                         for (int e = 0; e < VW; ++e)
 #pragma unroll
                             for (int n = 0; n < QT; ++n)
-                                acc[n][i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(vw[j][i].w, e), x[n][j / 4][j % 4], acc[n][i][e], 0, 0, 0);
+                                acc[n][i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(value32<C>(vr[j][i].w, e), x[n][j / 4][j % 4], acc[n][i][e], 0, 0, 0);
             } else {
                 constexpr int TERMS = PV == kSplit ? 3 : 1;
 #pragma unroll
@@ -578,7 +703,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                             u4 lo, hi;  // dims e and e + 1 of the lane's eight tokens
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const uint32_t y = pair16<C, PV>(vw[4 * u + 2 * j][i].w, e / 2), z = pair16<C, PV>(vw[4 * u + 2 * j + 1][i].w, e / 2);
+                                const uint32_t y = pair16<C, PV>(vr[4 * u + 2 * j][i].w, e / 2), z = pair16<C, PV>(vr[4 * u + 2 * j + 1][i].w, e / 2);
                                 lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
                                 hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
                             }
@@ -597,10 +722,27 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                 now = next;
             }
         };
-        for (; s < steps; s += turns) {
-            for (; s + turns < steps && !is_mixed(a0 + s * S::kStep); s += turns)
-                step(Clean<true>{});
-            step(Clean<false>{});
+        if constexpr (SHARE) {
+            // A round: this one's tokens are there once all have stored theirs, and the
+            // other buffer is free, of which the round before was computed.
+            for (uint32_t round = 0; round < rounds; ++round, s += turns) {
+                if (s < steps && live > 0) {
+                    if (!is_mixed(a0 + s * S::kStep))
+                        step(Clean<true>{});
+                    else
+                        step(Clean<false>{});
+                }
+                stage_store(round + 1);
+                stage_load(s + 2 * turns, ids);  // past the last step: that one again
+                ids = stage_ids(s + 3 * turns);
+                meet_in_lds();
+            }
+        } else {
+            for (; s < steps; s += turns) {
+                for (; s + turns < steps && !is_mixed(a0 + s * S::kStep); s += turns)
+                    step(Clean<true>{});
+                step(Clean<false>{});
+            }
         }
 
         // The waves' states, joined in order: each leaves its columns' sums in LDS, over
@@ -610,12 +752,12 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         float *const sums = (float *)(odds + 4 * waves);
         const bool any_bad = __any(bad);
         __syncthreads();
+        if (lane == 0)
+            odds[wave] = odd | any_bad << 1;
 #pragma unroll
         for (int n = 0; n < QT; ++n) {
             const float lift = PV == kF16 ? 0x1p-15f : 1.0f;
             float total = over_groups(l[n], [](float y, float z) { return y + z; }) * lift;
-            if (any_bad)
-                total = __builtin_nanf("");
             if (16 * n + col < live) {
                 float *mine = sums + (wave * COLS + 16 * n + col) * S::kRow;
 #pragma unroll
@@ -630,8 +772,6 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     state[wave * COLS + 16 * n + col] = f2{m[n], total};
             }
         }
-        if (lane == 0)
-            odds[wave] = odd;
         __syncthreads();
         const TreeArgs &pe = tree_arguments();
 #pragma unroll 1
@@ -650,13 +790,18 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             int unfinished = 0;
             for (int w = in; w < waves; w += beside) {
                 const f2 ml = state[w * COLS + head];
-                const float by = weight_of(ml.x - origin);
+                const float by = weight2_of(ml.x - origin);
                 weights += ml.y * by;
                 sum += *(const f4 *)(sums + (w * COLS + head) * S::kRow + at) * by;
                 unfinished |= odds[w];
             }
+            if constexpr (SHARE)  // every wave looked up some of the pages
+                for (int w = 0; w < waves; ++w)
+                    unfinished |= odds[w] & 2;
+            if (unfinished & 2)
+                weights = __builtin_nanf("");
             const int d = min(at0, p.c.v_dim - VW) + at - at0, x = col0 + head, q = (int)divide((uint32_t)x, p.heads_of);
-            if (unfinished) {  // the values that the mixed steps left out
+            if (unfinished & 1) {  // the values that the mixed steps left out
                 const uint64_t mask = p.masks ? (uint64_t)p.masks[b * p.drafts + q] : ~0ull >> (63 - q);
                 const int32_t own = base + depth(q);
 #pragma unroll 1
@@ -689,7 +834,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                 const float o[4] = {sum.x * by, sum.y * by, sum.z * by, sum.w * by};
                 put_out<4>(a, b * a.out_row + q * p.out_draft + (int64_t)g * a.out_head + d, o);
                 if (a.lse && at == 0)
-                    a.lse[(b * p.drafts + q) * a.q_heads + g] = log_sum(top, weights);
+                    a.lse[(b * p.drafts + q) * a.q_heads + g] = log_sum2(top, weights);
             }
         }
         mine.left -= done;
@@ -707,12 +852,24 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
 template <typename C, int QK, int PV, int D, int QT, int MOST, int KEEP> TreeKernel pick_tree_tiled(const TreeArgs &a)
 {
     typedef Attend<C, QK, PV, D, true, MOST, KEEP> S;
-    const void *f = a.tiled ? (const void *)k_tree<C, QK, PV, D, true, QT, MOST, KEEP> : (const void *)k_tree<C, QK, PV, D, false, QT, MOST, KEEP>;
-    return {f, QT * (S::kQ + 16 * (int)sizeof(Column)), 16 * QT * (8 + S::kRow * 4) + 16};
+    const void *f = a.tiled ? (const void *)k_tree<C, QK, PV, D, true, QT, MOST, KEEP, 0> : (const void *)k_tree<C, QK, PV, D, false, QT, MOST, KEEP, 0>;
+    return {f, 0, QT * (S::kQ + 16 * (int)sizeof(Column)), 16 * QT * (8 + S::kRow * 4) + 16};
+}
+template <typename C, int QK, int PV, int D, int SHARE> TreeKernel pick_tree_shared()
+{
+    typedef Attend<C, QK, PV, D, false, 2, kAll> S;
+    return {(const void *)k_tree<C, QK, PV, D, false, 2, 2, kAll, SHARE>, Staged<C, D, SHARE>::kBytes, 2 * 16 * (int)sizeof(Column), 32 * (8 + S::kRow * 4) + 16};
 }
 template <typename C, int QK, int PV, int D> TreeKernel pick_tree_columns(const TreeArgs &a)
 {
     if constexpr (QK != kF32 && QK != kSplit && PV != kF32 && PV != kSplit) {
+        if constexpr (D < 256) {
+            if (a.shared == 4)
+                return pick_tree_shared<C, QK, PV, D, 4>();
+            if constexpr (D * sizeof(C) / 16 >= 8)
+                if (a.shared == 8)
+                    return pick_tree_shared<C, QK, PV, D, 8>();
+        }
         if (a.tiles_of == 2)
             return a.keep == kAll ? pick_tree_tiled<C, QK, PV, D, 2, 2, kAll>(a) : pick_tree_tiled<C, QK, PV, D, 2, 2, kKeys>(a);
     }

@@ -69,13 +69,13 @@ template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_joi
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             top = fmaxf(top, s[j].x);
-        const float origin = top == -INFINITY ? 0.0f : top, turn = weight_of(m - origin);
+        const float origin = top == -INFINITY ? 0.0f : top, turn = weight2_of(m - origin);
         l *= turn;
         acc *= turn;
         m = top;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float w = weight_of(s[j].x - origin);
+            const float w = weight2_of(s[j].x - origin);
             l += s[j].y * w;
             acc += x[j] * w;
         }
@@ -95,7 +95,7 @@ template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_joi
         const float origin = top == -INFINITY ? 0.0f : top;
         acc = f4{0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
         for (int i = 0; i < GROUPS; ++i) {
-            const float w = weight_of(mls[own][i].x - origin);
+            const float w = weight2_of(mls[own][i].x - origin);
             l += mls[own][i].y * w;
             acc += accs[own][i][lane] * w;
         }
@@ -106,7 +106,7 @@ template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_joi
     if (d0 < p.c.v_dim)
         put_out<4>(a, b * a.out_row + i * p.out_draft + (int64_t)head * a.out_head + d, out);
     if (a.lse && lane == 0)
-        a.lse[(b * p.drafts + i) * a.q_heads + head] = log_sum(top, l);
+        a.lse[(b * p.drafts + i) * a.q_heads + head] = log_sum2(top, l);
 }
 
 template <int GROUPS> const void *pick_join(int dim)
@@ -135,7 +135,7 @@ int launch_tree(const TreeArgs &a, void *stream)
                 return false;
         return true;
     };
-    const int queries = a.beside * k.unit_bytes + 4 * DETFOLD_MAX_DRAFTS, sums = a.waves * k.wave_bytes, lds = queries > sums ? queries : sums;
+    const int queries = k.staged_bytes + a.beside * k.unit_bytes + 4 * DETFOLD_MAX_DRAFTS, sums = a.waves * k.wave_bytes, lds = queries > sums ? queries : sums;
     if (!(a.shares.d ? launch(k.f, (int64_t)a.shares.d * a.units.d, 64 * a.waves, lds) : rows((int64_t)a.units.d * a.parts.d, k.f, 64 * a.waves, lds)))
         return DETFOLD_ELAUNCH;
     if (!a.shares.d && a.parts.d <= 1)
