@@ -13,6 +13,7 @@
 namespace detfold_impl {
 namespace {
 
+constexpr int64_t kFewSteps = 4;
 constexpr int64_t kMaxMoved = (int64_t)1 << 22;  // tokens of a page, or of a row, that one launch moves
 
 // Whether a written [n0][n1][n2][last] buffer has no element twice: in the order
@@ -124,6 +125,13 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
             p->shares = full / groups;
             const int64_t even = (batch * seen + p->shares - 1) / p->shares, half = (seen + 1) / 2;
             part = even < half ? even : half;
+            // Shares of a few steps for every wave would pay for two rows' ends where a
+            // part of one row pays for one: 7 x 13 float32 tokens over 1500, FIGURE us
+            // in parts, 35 in shares.
+            if (even <= kFewSteps * 32 * (p->waves / p->beside) && batch * groups <= full) {
+                p->shares = 0;
+                part = (seen + full / (batch * groups) - 1) / (full / (batch * groups));
+            }
         } else if (batch > 0 && seen > kMaxBlocks / p->units * part) {
             part = (seen - 1) / (kMaxBlocks / p->units + 1) + 1;
         }

@@ -13,10 +13,10 @@ constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds a
 
 // The sums of each query of a row, or of the row that a share begins without
 // ending it, joined in order.  A lane takes four dims, LANES lanes a part, and
-// GROUPS groups of lanes every GROUPS-th part of a query; the loads of eight
-// parts go out together.  Parts that are empty add zeros, so a row's bits do not
+// GROUPS groups of lanes every GROUPS-th part of a query; the loads of DEEP parts
+// go out together.  Parts that are empty add zeros, so a row's bits do not
 // depend on how many follow its last one.
-template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_join_tree(TreeArgs p)
+template <int LANES, int GROUPS, int DEEP> __global__ __launch_bounds__(kBlock) void k_join_tree(TreeArgs p)
 {
     constexpr int QUERIES = kBlock / (LANES * GROUPS);  // of a workgroup
     const detfold_attend &a = p.a;
@@ -53,12 +53,12 @@ template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_joi
     const int d0 = 4 * lane, d = min(d0, p.c.v_dim - 4);
     f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     float m = -INFINITY, l = 0.0f;
-    for (int i0 = group; there && i0 < n; i0 += 8 * GROUPS) {  // eight parts' loads together
-        f4 x[8];
-        float2 s[8];
+    for (int i0 = group; there && i0 < n; i0 += DEEP * GROUPS) {
+        f4 x[DEEP];
+        float2 s[DEEP];
         float top = m;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < DEEP; ++j) {
             const int i = i0 + j * GROUPS;
             const int64_t at = slot(min(i, n - 1));
             s[j] = p.ml[at];
@@ -67,14 +67,14 @@ template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_joi
                 s[j] = make_float2(-INFINITY, 0.0f), x[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < DEEP; ++j)
             top = fmaxf(top, s[j].x);
         const float origin = top == -INFINITY ? 0.0f : top, turn = weight2_of(m - origin);
         l *= turn;
         acc *= turn;
         m = top;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < DEEP; ++j) {
             const float w = weight2_of(s[j].x - origin);
             l += s[j].y * w;
             acc += x[j] * w;
@@ -109,12 +109,12 @@ template <int LANES, int GROUPS> __global__ __launch_bounds__(kBlock) void k_joi
         a.lse[(b * p.drafts + i) * a.q_heads + head] = log_sum2(top, l);
 }
 
-template <int GROUPS> const void *pick_join(int dim)
+template <int GROUPS, int DEEP> const void *pick_join(int dim)
 {
     if constexpr (GROUPS <= 4)
         if (dim > 128)
-            return (const void *)k_join_tree<64, GROUPS>;
-    return dim <= 64 ? (const void *)k_join_tree<16, GROUPS> : (const void *)k_join_tree<32, GROUPS>;
+            return (const void *)k_join_tree<64, GROUPS, DEEP>;
+    return dim <= 64 ? (const void *)k_join_tree<16, GROUPS, DEEP> : (const void *)k_join_tree<32, GROUPS, DEEP>;
 }
 
 }  // namespace
@@ -147,7 +147,7 @@ int launch_tree(const TreeArgs &a, void *stream)
     const int groups = parts > 8 ? 256 / lanes < 8 ? 4 : 8 : 1, per = kBlock / (lanes * groups);
     const int64_t each = (queries_all + per - 1) / per;
     copy.join_blocks = divider((uint32_t)each);
-    const void *join = groups == 8 ? pick_join<8>(a.c.v_dim) : groups == 4 ? pick_join<4>(a.c.v_dim) : pick_join<1>(a.c.v_dim);
+    const void *join = groups == 8 ? pick_join<8, 8>(a.c.v_dim) : groups == 4 ? pick_join<4, 8>(a.c.v_dim) : pick_join<1, 4>(a.c.v_dim);
     if (!(a.shares.d ? launch(join, (a.by_row ? a.a.batch : a.shares.d) * each, kBlock, 0) : rows(each, join, kBlock, 0)))
         return DETFOLD_ELAUNCH;
     return DETFOLD_OK;
