@@ -298,12 +298,12 @@ bool table_of(const Arg &x, int64_t dev, int64_t batch)
 }
 
 // (function, cache, device, stream, out, q, table, lens, masks, counts, depths, cap, slopes, scale, window, max_len, lse,
-// workspace, split); q [batch, drafts, q_heads, dim], or [batch, q_heads, dim] of one token a row
+// workspace, split, dims); q [batch, drafts, q_heads, dim], or with dims = 3 [batch, q_heads, dim] of one token a row
 PyObject *tree(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     detfold_paged_cache c;
     Numbers num;
-    if (n != 19)
+    if (n != 20)
         return not_taken();
     const TreeFn f = (TreeFn)num.address(args[0]);
     const int64_t dev = num.whole(args[2]);
@@ -318,8 +318,8 @@ PyObject *tree(PyObject *, PyObject *const *args, Py_ssize_t n)
     const int64_t split = num.whole(args[18]);
     if (!num.ok || !real(args[11], &t.cap) || !real(args[13], &a.scale) || split < 0 || split > INT32_MAX || !q.on(dev) || !out.on(dev))
         return not_taken();
-    const int64_t dims = q.t->dim(), batch = q.t->size(0);
-    if ((dims != 3 && dims != 4) || out.t->dim() != dims)
+    const int64_t dims = num.whole(args[19]), batch = q.t->size(0);
+    if ((dims != 3 && dims != 4) || q.t->dim() != dims || out.t->dim() != dims)
         return not_taken();
     const int64_t drafts = dims == 4 ? q.t->size(1) : 1, q_heads = q.t->size(dims - 2);
     if (drafts < 1 || drafts > DETFOLD_MAX_DRAFTS || q_heads > INT32_MAX || q.t->size(dims - 1) != c.dim)

@@ -76,7 +76,9 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     if (drafts < 1 || drafts > DETFOLD_MAX_DRAFTS || max_len > kMaxCount - 1 - DETFOLD_MAX_DRAFTS || !types_pair(type, c.type) ||
         (out_type != type && out_type != DETFOLD_F32))
         return DETFOLD_EINVAL;
-    const int64_t cols = (int64_t)drafts * (q_heads / c.heads), queries = c.heads * (cols > 16 ? (cols + 255) / 32 * 32 : cols);
+    const int64_t cols = (int64_t)drafts * (q_heads / c.heads), pairs = (cols + 31) / 32;
+    // At least the units times a slot's queries, however they are dealt out below.
+    const int64_t queries = c.heads * (cols <= 16 ? cols : 32 * (pairs <= 2 ? pairs : pairs <= 4 ? 4 : (pairs + 7) / 8 * 8));
     if (batch > 0 && queries > kMaxElems / 16 / batch)
         return DETFOLD_EINVAL;
     const int head = c.dim > c.v_dim ? c.dim : c.v_dim, wide_head = head <= 64 ? 64 : head <= 128 ? 128 : 256;
@@ -97,7 +99,7 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     // over 4096: FIGURE us, 377 straight to registers; two would hold too much on the
     // way in registers: 1 x 16 over 131072 took 164 us, 127 so).
     const int most_shared = wide_head * elem_size(c.type) >= 128 ? 8 : 4;
-    p->shared = tiles < 2 || of_head < 3 || !tree_staged(c) ? 0 : of_head <= 4 || most_shared == 4 ? 4 : 8;
+    p->shared = tiles < 2 || of_head < 2 || !tree_staged(c) ? 0 : of_head <= 2 ? 2 : of_head <= 4 || most_shared == 4 ? 4 : 8;
     if (p->shared)
         of_head = (of_head + p->shared - 1) / p->shared * p->shared;
     const int64_t units = c.heads * of_head;

@@ -726,12 +726,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             // A round: this one's tokens are there once all have stored theirs, and the
             // other buffer is free, of which the round before was computed.
             for (uint32_t round = 0; round < rounds; ++round, s += turns) {
-                if (s < steps && live > 0) {
-                    if (!is_mixed(a0 + s * S::kStep))
-                        step(Clean<true>{});
-                    else
-                        step(Clean<false>{});
-                }
+                step(Clean<false>{});
                 stage_store(round + 1);
                 stage_load(s + 2 * turns, ids);  // past the last step: that one again
                 ids = stage_ids(s + 3 * turns);
@@ -864,6 +859,8 @@ template <typename C, int QK, int PV, int D> TreeKernel pick_tree_columns(const 
 {
     if constexpr (QK != kF32 && QK != kSplit && PV != kF32 && PV != kSplit) {
         if constexpr (D < 256) {
+            if (a.shared == 2)
+                return pick_tree_shared<C, QK, PV, D, 2>();
             if (a.shared == 4)
                 return pick_tree_shared<C, QK, PV, D, 4>();
             if constexpr (D * sizeof(C) / 16 >= 8)

@@ -123,7 +123,7 @@ def attend_tree(out, q, cache, table, lens, *, masks=None, counts=None, depths=N
     raw, here, call, of = (_native or _bound())[:4]
     if here() == dev:
         rc = call(of, cache, dev, raw(dev) if stream is None else int(stream.cuda_stream), out, q, table, lens, masks, counts,
-                  depths, cap, slopes, 1.0 / math.sqrt(cache.dim) if scale is None else scale, window, max_len, lse, workspace, split)
+                  depths, cap, slopes, 1.0 / math.sqrt(cache.dim) if scale is None else scale, window, max_len, lse, workspace, split, 4)
         if rc >= 0:
             return _check(rc, "attend_tree") if rc else None
     if q.dim() != 4:
@@ -138,7 +138,7 @@ def scored(out, q, cache, table, lens, cap, slopes, scale, window, max_len, lse,
     raw, here, call, of = (_native or _bound())[:4]
     if here() == dev:
         rc = call(of, cache, dev, raw(dev) if stream is None else int(stream.cuda_stream), out, q, table, lens, None, None,
-                  None, cap, slopes, 1.0 / math.sqrt(cache.dim) if scale is None else scale, window, max_len, lse, workspace, split)
+                  None, cap, slopes, 1.0 / math.sqrt(cache.dim) if scale is None else scale, window, max_len, lse, workspace, split, 3)
         if rc >= 0:
             return _check(rc, "attend_paged") if rc else None
     for x, name in ((q, "q"), (out, "out")):

@@ -200,16 +200,16 @@ def test_tree_random(env, seed):  # noqa: F811
 
 @pytest.mark.parametrize("dtype,cache", PAIRS)
 @pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("dim", [64, 84, 256])
-def test_tree_infinities_are_their_queries_alone(env, dtype, cache, what, dim):  # noqa: F811
+@pytest.mark.parametrize("dim,group", [(64, 3), (84, 3), (256, 3), (128, 4), (80, 7), (128, 20)])
+def test_tree_infinities_are_their_queries_alone(env, dtype, cache, what, dim, group):  # noqa: F811
     """A drafted value or key that is no number is in the results of those that see it, and in no other's; so is a
     prefix token's that a window hides from some."""
     df, torch, dev = env
     if cache == "e4m3" and not math.isnan(what):
         return  # 8 bits have no infinity
-    gen = _gen(torch, dtype, cache, what, dim)
+    gen = _gen(torch, dtype, cache, what, dim, group)
     t = _t(torch, cache)
-    n, base, heads, group = 8, 40, 2, 3
+    n, base, heads = 8, 40, 2
     k, v = (_normal(torch, gen, (4, 16, heads, dim), cache) for _ in range(2))
     masks = [0b1, 0b11, 0b101, 0b1011, 0b10101, 0b100001, 0b1000011, 0b10010101]
     depths = [0, 1, 1, 2, 2, 1, 2, 3]
@@ -305,6 +305,74 @@ def test_tree_far_pages_and_many_rows(env):  # noqa: F811
     del kc, c
     torch.cuda.empty_cache()
     _tree_case(env, [20 + i % 30 for i in range(700)], 3, 2, 1, 64, 64, "bf16", "bf16", 16)
+
+
+@pytest.mark.parametrize("drafts,q_heads,heads,dim,v_dim,page,order", [
+    (13, 12, 2, 128, 128, 7, "thd"), (33, 4, 1, 80, 48, 16, "htd"), (64, 16, 2, 64, 64, 1, "thd"), (40, 8, 8, 112, 128, 33, "thd"),
+    (64, 8, 1, 128, 64, 16, "htd"), (9, 32, 4, 32, 128, 64, "thd"), (20, 10, 1, 128, 16, 5, "thd"), (64, 3, 3, 96, 96, 16, "htd")])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("f16", "f16"), ("f16", "e4m3")])
+def test_tree_many_queries(env, drafts, q_heads, heads, dim, v_dim, page, order, dtype, cache):  # noqa: F811
+    """Key-value heads of many queries, whose tokens workgroups take from LDS."""
+    _tree_case(env, [0, 1, drafts - 1, 64, 65, 90, 500], drafts, q_heads, heads, dim, v_dim, dtype, cache, page, order, kind="bits")
+    _tree_case(env, [700, 3, 1200, 33], drafts, q_heads, heads, dim, v_dim, dtype, cache, page, order, window=100, cap=20.0, slopes=True,
+               counts=[drafts, 2, drafts // 2, 0])
+    _tree_case(env, [700, 1200], drafts, q_heads, heads, dim, v_dim, dtype, cache, page, order, split=96)
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f16", "f16"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("drafts", [2, 8, 30])
+def test_tree_lowest_scores(env, dtype, cache, drafts):  # noqa: F811
+    """Keys of the type's lowest value and of -infinity: scores of -infinity take no weight beside others, and leave
+    zeros where there is nothing else; with a cap they are -cap."""
+    df, torch, dev = env
+    t = _t(torch, cache)
+    k = torch.zeros((4, 16, 1, 64), dtype=t)
+    v = _normal(torch, _gen(torch, 31), (4, 16, 1, 64), cache)
+    k[1, :, :, 0], k[2, :, :, 0] = -math.inf, torch.finfo(t).min
+    q = torch.zeros((4, drafts, 4, 64), dtype=_t(torch, dtype))
+    q[..., 0] = 1.0
+    table = torch.tensor([[1, 1, 1], [2, 2, 2], [1, 3, 1], [2, 3, 2]], dtype=torch.int32, device=dev)
+    lens = torch.tensor([40, 40, 40, 40], dtype=torch.int32, device=dev)
+    c = df.PagedCache(k.to(dev), v.to(dev))
+    masks = torch.ones((4, drafts), dtype=torch.int64, device=dev)  # the prefix and the first drafted token
+    base = 40 - drafts
+    keys, vals = k.double()[:, :, 0, 0], v.double()[:, :, 0]
+    for cap in (0.0, 2.0):
+        out, lse = torch.empty_like(q, device=dev), torch.empty((4, drafts, 4), device=dev)
+        df.attend_tree(out, q.to(dev), c, table, lens, masks=masks, lse=lse, scale=2.0 ** -100, cap=cap)
+        for b in range(4):
+            pages = table[b].cpu().long()
+            x = torch.cat([keys[p] for p in pages])[:base + 1] * 2.0 ** -100
+            y = torch.cat([vals[p] for p in pages])[:base + 1]
+            if cap:
+                x = cap * torch.tanh(x / cap)
+            p = torch.softmax(x, 0) if bool((x > -math.inf).any()) else torch.zeros_like(x)
+            want = (p @ y).expand(drafts, 4, 64)
+            tol = torch.full_like(want, 8 * torch.finfo(_t(torch, dtype)).eps * float(y.abs().max()))
+            decode_oracle.close(out[b], want, tol, "out %d cap %g" % (b, cap))
+            wl = torch.logsumexp(x, 0).expand(drafts, 4)
+            decode_oracle.close(lse[b], wl, torch.where(torch.isfinite(wl), 1e-5 * (wl.abs() + 1), torch.zeros_like(wl)), "lse %d" % b)
+
+
+def test_tree_two_streams_at_once(env):  # noqa: F811
+    """Calls that overlap, each with a workspace of its own, and calls of many rows in parts of a fixed length."""
+    df, torch, dev = env
+    c, q, table, lens, out, lse, args = _tree_case(env, [3000, 500, 0, 2999], 8, 8, 2, 128, 128, "bf16", "bf16", 16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [(torch.empty_like(out), torch.empty_like(lse), df.attend_workspace(c, 4, 8, 3000, drafts=8)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (o, l, ws) in zip(streams, got):
+            with torch.cuda.stream(s):
+                df.attend_tree(o, q, c, table, lens, lse=l, workspace=ws, **args)
+    torch.cuda.synchronize()
+    for o, l, _ in got:
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    with pytest.raises(df.DetfoldError) as e:
+        df.attend_tree(got[0][0], q, c, table, lens, workspace=torch.empty(1024, dtype=torch.uint8, device=dev), **args)
+    assert e.value.rc == df.ESIZE
+    _tree_case(env, [10 + i * 7 % 900 for i in range(4200)], 2, 1, 1, 16, 16, "f32", "f32", 64)
 
 
 def test_tree_nothing(env):  # noqa: F811

@@ -128,3 +128,65 @@ def test_compact_refusals(lib):
         assert lib.detfold_cache_compact(cache(), compact(**bad), None) == 1, bad
     for bad in (dict(table=K), dict(to=V + 64), dict(picks=K + 4), dict(counts=V), dict(starts=K)):
         assert lib.detfold_cache_compact(cache(), compact(**bad), None) == 2, bad
+
+
+def _plan(lib, batch, drafts, q_heads, max_len, window=0, split=0, type=BF, out=None, cu=256, **kw):
+    p = d.AttendPlan()
+    assert lib.detfold_plan_tree(cache(**kw), batch, drafts, q_heads, max_len, window, split, type, type if out is None else out, cu,
+                                 ctypes.byref(p)) == 0
+    return p
+
+
+def test_plan_covers_every_length(lib):
+    for batch in (0, 1, 3, 64, 5000):
+        for drafts in (1, 2, 8, 33, 64):
+            for max_len in (0, 1, 31, 32, 33, 1000, 8192, 131072, (1 << 31) - 65):
+                for window in (0, 1, 100, 1500):
+                    for split in (0, 32, 4096):
+                        if split and batch * max_len > 1 << 36:
+                            continue  # more parts than a workspace is made for
+                        for cu in (1, 64, 256):
+                            p = _plan(lib, batch, drafts, 8, max_len, window, split, cu=cu)
+                            seen = min(max_len, window + drafts - 1) if window else max_len
+                            assert p.splits >= 1 and p.splits * p.split >= seen
+                            assert p.splits == 1 or (p.splits - 1) * p.split < seen
+                            if split:
+                                assert p.split == split or p.splits == 1
+                            assert (p.workspace_bytes > 0) == (p.splits > 1 and batch > 0)
+
+
+@pytest.mark.parametrize("heads,group,dim", [(2, 4, 64), (8, 4, 128), (1, 1, 256), (3, 5, 84), (1, 24, 16), (16, 8, 128), (4, 40, 250)])
+def test_workspace_serves_smaller_calls(lib, heads, group, dim):
+    """A workspace of some sizes serves every smaller batch, length and number of drafted tokens, every window, every
+    type of query, and the plain attention of one token."""
+    import random
+    rng = random.Random(heads * dim)
+    kw = dict(heads=heads, dim=dim, v_dim=dim, k_head=dim, k_token=heads * dim, k_page=16 * heads * dim, v_head=dim,
+              v_token=heads * dim, v_page=16 * heads * dim)
+    for _ in range(60):
+        batch, drafts = rng.choice([1, rng.randint(1, 300), 6000]), rng.randint(1, 64)
+        max_len, split = rng.choice([rng.randint(1, 3000), rng.randint(1, 200000)]), rng.choice([0, 0, 64, 2048])
+        if split and batch * heads * group * drafts * max_len // split > 1 << 38:
+            continue
+        most = _plan(lib, batch, drafts, heads * group, max_len, 0, split, F32, **kw).workspace_upto
+        for _ in range(30):
+            b, n, t = rng.randint(0, batch), rng.choice([max_len, rng.randint(0, max_len), rng.randint(0, 400)]), rng.randint(1, drafts)
+            n, w = min(n, max_len), rng.choice([0, rng.randint(1, 5000)])
+            type, out = rng.choice([(BF, BF), (BF, F32), (F32, F32)])
+            p = _plan(lib, b, t, heads * group, n, w, split, type, out, **kw)
+            assert p.workspace_bytes <= p.workspace_upto <= most, (batch, drafts, max_len, split, b, t, n, w)
+            one = _plan(lib, b, 1, heads * group, n, w, split, type, out, **kw)
+            plain = d.AttendPlan()
+            assert lib.detfold_plan_attend(cache(**kw), batch, heads * group, max_len, 0, split, 256, ctypes.byref(plain)) == 0
+            assert one.workspace_bytes <= plain.workspace_upto, (batch, max_len, split, b, n, w)
+
+
+def test_plan_refusals(lib):
+    ok = dict(batch=3, drafts=5, q_heads=4, max_len=640, window=0, split=0, type=BF, out=BF, cu=256)
+    for bad in (dict(drafts=0), dict(drafts=65), dict(q_heads=3), dict(max_len=(1 << 31) - 64), dict(type=F16), dict(out=F16), dict(type=E4),
+                dict(cu=0), dict(split=31), dict(window=-1), dict(batch=-1)):
+        a = {**ok, **bad}
+        assert lib.detfold_plan_tree(cache(), a["batch"], a["drafts"], a["q_heads"], a["max_len"], a["window"], a["split"], a["type"],
+                                     a["out"], a["cu"], ctypes.byref(d.AttendPlan())) == 1, bad
+    assert lib.detfold_plan_tree(cache(), 3, 5, 4, 640, 0, 0, BF, BF, 256, None) == 1
+    assert lib.detfold_tree_workspace(cache(), 3, 5, 4, 640, 0, None) == 1
