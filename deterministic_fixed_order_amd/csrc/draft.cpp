@@ -53,10 +53,14 @@ bool same_cache(const detfold_paged_cache &a, const detfold_paged_cache &b)
 
 namespace {
 
-// Whether heads are whole chunks of 16 bytes, at such addresses.
+// Whether heads are whole chunks of 16 bytes, at such addresses, and pages and tokens
+// less than 2^31 bytes apart.
 bool tree_staged(const detfold_paged_cache &c)
 {
     const int64_t of = 16 / elem_size(c.type);
+    for (int64_t x : {c.k_page, c.k_token, c.v_page, c.v_token})
+        if (x >= kMaxCount / elem_size(c.type))
+            return false;
     for (int64_t x : {c.k_page, c.k_token, c.k_head, c.v_page, c.v_token, c.v_head, (int64_t)c.dim, (int64_t)c.v_dim})
         if (x % of != 0)
             return false;
@@ -88,16 +92,16 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     // eight waves to a compute unit (1 x 16 tokens over 131072 took 163 us with four,
     // 139 with two).  Products in float32, and in parts, are what bounds one tile
     // already.  Where one step for every wave that the device holds is enough, its
-    // time is the code's, which one tile has less of (1 x 8 over 1000: FIGURE us, 20
-    // with two).  One token a row is split as attend_paged splits it, in the same
+    // time is the code's, which one tile has less of (1 x 8 over 1000: 17 us, 20 with
+    // two).  One token a row is split as attend_paged splits it, in the same
     // workspace.
     const bool narrow = type != DETFOLD_F32 && out_type != DETFOLD_F32;
     const bool once = split == 0 && batch * ((seen + 31) / 32) <= full * kWavesPerCu / (c.heads * ((cols + 15) / 16));
     const int tiles = narrow && drafts > 1 && cols > 16 && !once ? 2 : 1;
     int64_t of_head = (cols + 16 * tiles - 1) / (16 * tiles);  // units of a key-value head
-    // More units than two of a key-value head take its tokens from LDS together (32 x 64
-    // over 4096: FIGURE us, 377 straight to registers; two would hold too much on the
-    // way in registers: 1 x 16 over 131072 took 164 us, 127 so).
+    // More units than one of a key-value head take its tokens from LDS together: 2, 4 or
+    // 8 to a workgroup (1 x 16 tokens over 131072, two units: 122 us, 128 straight to
+    // registers; 32 x 64 over 4096, eight: 279 and 377).
     const int most_shared = wide_head * elem_size(c.type) >= 128 ? 8 : 4;
     p->shared = tiles < 2 || of_head < 2 || !tree_staged(c) ? 0 : of_head <= 2 ? 2 : of_head <= 4 || most_shared == 4 ? 4 : 8;
     if (p->shared)
@@ -114,7 +118,8 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     p->brief = seen <= 32;
     const int64_t groups = units / p->beside;
     const int fit = 1024 / (wide_head * elem_size(c.type)), most_tiles = tiles > 1 || wide_head == 256 ? 2 : 4;
-    const int64_t few = 3 * 16 * (fit < most_tiles ? fit : most_tiles) * (4 / p->beside);
+    // Three steps of a wave take less than a join, as for one token.
+    const int64_t few = p->shared ? 3 * 32 * (p->waves / p->shared) : 3 * 16 * (fit < most_tiles ? fit : most_tiles) * (4 / p->beside);
     int64_t part = split > 0 ? split : kLongPart;
     if (split == 0) {
         if (seen <= few || (batch * groups >= full && seen <= kShortRow)) {
@@ -128,8 +133,8 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
             const int64_t even = (batch * seen + p->shares - 1) / p->shares, half = (seen + 1) / 2;
             part = even < half ? even : half;
             // Shares of a few steps for every wave would pay for two rows' ends where a
-            // part of one row pays for one: 7 x 13 float32 tokens over 1500, FIGURE us
-            // in parts, 35 in shares.
+            // part of one row pays for one (7 x 13 float32 tokens over 1500: 31.5 us in
+            // parts, 35 in shares).
             if (even <= kFewSteps * 32 * (p->waves / p->beside) && batch * groups <= full) {
                 p->shares = 0;
                 part = (seen + full / (batch * groups) - 1) / (full / (batch * groups));

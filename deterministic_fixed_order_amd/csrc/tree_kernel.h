@@ -3,12 +3,28 @@
 // its own branch.  Included by the tree_*.hip files, each of which instantiates
 // the kernels of one query type.
 //
-// Mathematics and layouts as in attend_kernel.h.  The columns of both products are
-// a key-value head's queries, drafted token by drafted token, 16 * QT of them to a
-// wave, so that what is loaded of the cache serves QT products.  A capped score is
-// cap * tanh(s / cap); a biased one gets slope * (position of the token - position
-// of the query); what a query does not see scores -infinity.  Only steps that hold
-// drafted tokens, or tokens at the window's edge, look at masks.
+// Mathematics and layouts as in attend_kernel.h, with scores times log2 e.  The
+// columns of both products are a key-value head's queries, drafted token by drafted
+// token, 16 * QT of them to a wave, so that what is loaded of the cache serves QT
+// products.  A capped score is cap * tanh(s / cap); a biased one gets slope *
+// (position of the token - position of the query); what a query does not see scores
+// -infinity.
+//
+// What bounds it.  Up to 32 queries of a key-value head: the cache's bytes, read once
+// straight to registers (64 ragged rows of 8 drafted tokens over 8192 bfloat16 tokens
+// of 8 heads of 128: 182 us, 5.5 TB/s; of one capped token each over their last 4096:
+// 125 us, 5.9; 32 x 8192 e4m3: 94 us, 5.7).  Above: the instructions around the
+// products, 8 cycles a score and lane, so that waves which take the same tokens share
+// them through LDS (32 rows of 64 drafted tokens over 4096, capped: 279 us, 490
+// TFLOP/s with the vector units busy three quarters of the time; 377 us straight to
+// registers).  Small calls: the code, run once (1 x 8 over 1000: 17 us).  So:
+// * Steps all of whose tokens all queries see hold no code for masks, or jump over it;
+//   with masks in the loop their uniform values filled the scalar registers (1 x 8 over
+//   1000 25 us, 32 x 64 over 4096 419).  A mask is looked at four tokens at a time.
+// * Values that are infinite or no number are zeroed where some query may not see them
+//   (zero times them is NaN), and added at the end, once, to the sums of those that do.
+// * A capped score takes 9 instructions below half its cap, a polynomial, and 25 above.
+//
 #ifndef DETFOLD_TREE_KERNEL_H
 #define DETFOLD_TREE_KERNEL_H
 
@@ -114,7 +130,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0
 // registers meanwhile.  Straight to registers, as for fewer queries, every wave would
 // load all of it, and a load of keys, 16 tokens by 4 chunks, is 64 accesses of the
 // compute unit's cache where one of neighbours is 16: 32 rows of 64 drafted tokens
-// over 4096 kept it 81% busy.  Keys lie so that the 16 tokens' same chunks are on
+// over 4096 kept it 81% busy (377 us; 279 so), 1 x 16 over 131072 took 128 us (122 so).  Keys lie so that the 16 tokens' same chunks are on
 // different banks: a token's chunk c in the place of c ^ key(token).
 template <typename C, int D, int SHARE> struct Staged {
     static constexpr int kRow = D * sizeof(C), kPerRow = kRow / 16, kTile = 32 * kRow;
@@ -324,12 +340,13 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             const int place = staged_place();
 #pragma unroll
             for (int k = 0; k < T::kChunks; ++k) {
-                const uint32_t t = staged_at(place, s, k % T::kIds);
-                const int64_t off = t - divide(t, p.page) * p.page.d, id = valid(g.id[k % T::kIds]);
+                const uint32_t t = staged_at(place, s, k % T::kIds), off = t - divide(t, p.page) * p.page.d, id = (uint32_t)valid(g.id[k % T::kIds]);
                 const int c = (place + k * 64 * SHARE) % T::kPerRow;
                 const bool values = staged_values(place, k);
-                const char *from = (values ? v0 + id * v_page + off * v_token : k0 + id * k_page + off * k_token) +
-                                   min(16 * c, (values ? p.c.v_dim : c_dim) * CS - 16);
+                // Strides below 2^31 bytes, which the plan looks at.
+                const char *from = (values ? v0 : k0) + min(16 * c, (values ? p.c.v_dim : c_dim) * CS - 16);
+                from += (uint64_t)id * (uint32_t)(values ? v_page : k_page);
+                from += (uint64_t)off * (uint32_t)(values ? v_token : k_token);
                 const Words<16> w = load_words<16, false>(from);
                 staged[k] = u4{w.w[0], w.w[1], w.w[2], w.w[3]};
             }
