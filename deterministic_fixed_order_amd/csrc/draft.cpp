@@ -178,7 +178,8 @@ int check_tree(const detfold_paged_cache *c, const detfold_tree *t)
     TreePlan p;  // checks the counts; the device's own plan follows
     if ((rc = plan_tree(*c, a.batch, t->drafts, a.q_heads, a.max_len, a.window, a.split, a.type, a.out_type, 1, &p)) != DETFOLD_OK)
         return rc;
-    if (!std::isfinite(a.scale) || a.table_width < 0 || a.table_row < 0 || a.workspace_bytes < 0)
+    // Times log2 e, as the kernel holds them, both are finite.
+    if (!(std::fabs(a.scale) <= 0x1p127f) || !(t->cap <= 0x1p127f) || a.table_width < 0 || a.table_row < 0 || a.workspace_bytes < 0)
         return DETFOLD_EINVAL;
     if (t->masks && !t->depths && (a.window > 0 || t->slopes))
         return DETFOLD_EINVAL;

@@ -24,7 +24,6 @@
 // * Values that are infinite or no number are zeroed where some query may not see them
 //   (zero times them is NaN), and added at the end, once, to the sums of those that do.
 // * A capped score takes 9 instructions below half its cap, a polynomial, and 25 above.
-//
 #ifndef DETFOLD_TREE_KERNEL_H
 #define DETFOLD_TREE_KERNEL_H
 
@@ -130,8 +129,9 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0
 // registers meanwhile.  Straight to registers, as for fewer queries, every wave would
 // load all of it, and a load of keys, 16 tokens by 4 chunks, is 64 accesses of the
 // compute unit's cache where one of neighbours is 16: 32 rows of 64 drafted tokens
-// over 4096 kept it 81% busy (377 us; 279 so), 1 x 16 over 131072 took 128 us (122 so).  Keys lie so that the 16 tokens' same chunks are on
-// different banks: a token's chunk c in the place of c ^ key(token).
+// over 4096 kept it 81% busy and took 377 us, 279 so; 1 x 16 over 131072 128 us, 122
+// so.  Keys lie so that the 16 tokens' same chunks are on different banks: a token's
+// chunk c in the place of c ^ key(token).
 template <typename C, int D, int SHARE> struct Staged {
     static constexpr int kRow = D * sizeof(C), kPerRow = kRow / 16, kTile = 32 * kRow;
     static constexpr int kChunks = SHARE ? kPerRow / SHARE : 1, kIds = kChunks > 1 ? kChunks / 2 : 1;
@@ -469,7 +469,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
             constexpr bool clean = decltype(is_clean)::value;
             const bool more = !SHARE && (clean || s + turns < steps);
             const uint32_t t0 = a0 + s * S::kStep;
-                        const char *const tile = buffer(s / turns);
+            const char *const tile = buffer(s / turns);
             const int here = anew(lane), col = here & 15, grp = here >> 4;
             const uint32_t q_at = here * 16;
             // Staged tokens come to registers here; others are there, held across steps.

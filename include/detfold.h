@@ -565,8 +565,8 @@ int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *
  *   counts    device, int32 [batch], or NULL: all are there (negative: none)
  *   depths    device, int32 [batch][drafts], each taken as 0 .. 63, or NULL: i of
  *             token i.  Needed with masks where there is a window or slopes
- *   slopes    device, [q_heads] floats, or NULL
- *   cap       0: none; else a positive, finite, normal number
+ *   slopes    device, [q_heads] floats, or NULL; at most 2^127 in magnitude, as scale
+ *   cap       0: none; else a positive, normal number up to 2^127
  *   max_len   at most 2^31 - 65
  * Bits, splits and the workspace (detfold_tree_workspace) as of
  * detfold_attend_paged.

@@ -77,6 +77,15 @@ def test_bad_trees(lib, bad):
     assert lib.detfold_attend_tree(cache(), attend(**bad), None) == 1
 
 
+def test_largest_scales(lib):
+    """Scores are held times log2 e, and so are the cap and the scale: finite up to 2^127, which is no bad argument."""
+    past = 2.0 ** 127 * (1 + 2.0 ** -23)
+    for name in ("scale", "cap"):
+        assert lib.detfold_attend_tree(cache(), attend(**{name: past}), None) == 1
+        assert lib.detfold_attend_tree(cache(), attend(batch=0, **{name: 2.0 ** 127}), None) == 0
+    assert lib.detfold_attend_tree(cache(), attend(scale=-past), None) == 1
+
+
 @pytest.mark.parametrize("bad", [
     dict(out_head=31), dict(out_head=0), dict(out_draft=127), dict(out_draft=0), dict(out_row=639), dict(out_row=0), dict(out=Q),
     dict(out=K + 64), dict(out=V), dict(out=TABLE), dict(out=LENS), dict(out=LSE), dict(out=WORK + 16), dict(out=SIDE), dict(lse=Q),
