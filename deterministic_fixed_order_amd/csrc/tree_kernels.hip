@@ -14,8 +14,8 @@ constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds a
 // The sums of each query of a row, or of the row that a share begins without
 // ending it, joined in order.  A lane takes four dims, LANES lanes a part, and
 // GROUPS groups of lanes every GROUPS-th part of a query; the loads of DEEP parts
-// go out together.  Parts that are empty add zeros, so a row's bits do not
-// depend on how many follow its last one.
+// go out together.  Parts that are empty add zeros, so with the same GROUPS a row's
+// bits do not depend on how many follow its last one.
 template <int LANES, int GROUPS, int DEEP> __global__ __launch_bounds__(kBlock) void k_join_tree(TreeArgs p)
 {
     constexpr int QUERIES = kBlock / (LANES * GROUPS);  // of a workgroup
@@ -141,10 +141,12 @@ int launch_tree(const TreeArgs &a, void *stream)
     if (!a.shares.d && a.parts.d <= 1)
         return DETFOLD_OK;
     // Where rows have many parts, and few queries wait for them, several groups of
-    // lanes take a query's.
+    // lanes take a query's.  Groups add in another order than one does, so where
+    // `split` fixes a row's parts, and its bits with them, they do whatever the number
+    // of parts, which goes by max_len.
     const int lanes = a.c.v_dim <= 64 ? 16 : a.c.v_dim <= 128 ? 32 : 64;
     const int64_t parts = a.shares.d ? a.shares.d / a.a.batch : a.parts.d, queries_all = (int64_t)a.drafts * a.a.q_heads;
-    const int groups = parts > 8 ? 256 / lanes < 8 ? 4 : 8 : 1, per = kBlock / (lanes * groups);
+    const int groups = a.a.split > 0 || parts > 8 ? 256 / lanes < 8 ? 4 : 8 : 1, per = kBlock / (lanes * groups);
     const int64_t each = (queries_all + per - 1) / per;
     copy.join_blocks = divider((uint32_t)each);
     const void *join = groups == 8 ? pick_join<8, 8>(a.c.v_dim) : groups == 4 ? pick_join<4, 8>(a.c.v_dim) : pick_join<1, 4>(a.c.v_dim);
