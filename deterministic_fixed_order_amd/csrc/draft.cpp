@@ -276,6 +276,90 @@ int check_compact(const detfold_paged_cache *c, const detfold_compact *a)
 
 namespace {
 
+// The runs of a cache's keys or values, [pages][page][heads] of `last` elements each.
+struct Runs {
+    int64_t n[3], s[3], last;
+    int64_t span(int from) const
+    {
+        int64_t e = last;
+        for (int i = from; i < 3; ++i)
+            e += (n[i] - 1) * s[i];
+        return e;
+    }
+};
+Runs all_runs(const detfold_paged_cache &c, bool values)
+{
+    const int64_t head = values ? c.v_head : c.k_head;  // 0: all heads are one
+    return {{c.pages, c.page, head == 0 ? 1 : c.heads}, {values ? c.v_page : c.k_page, values ? c.v_token : c.k_token, head},
+            values ? c.v_dim : c.dim};
+}
+
+// Which elements two sets of runs share, of which neither has one twice: none, some of
+// runs of the same indexes, or others.  `apart` is from the first run of the one to that
+// of the other.  Dims come in the order of their strides, so what lies within one index
+// spans no more than its stride, and of all differences of an index two can meet.
+// Runs that are not equally far apart, or in another order, count as sharing others
+// where their spans meet.
+enum { kNone, kSame, kOthers };
+int shared_runs(const Runs &a, const Runs &b, int64_t apart, int i = 0, bool moved = false)
+{
+    if (apart >= a.span(i) || apart <= -b.span(i))
+        return kNone;
+    if (i == 3)
+        return moved ? kOthers : kSame;
+    if (a.n[i] == 1 && b.n[i] == 1)
+        return shared_runs(a, b, apart, i + 1, moved);
+    if (a.n[i] != b.n[i] || a.s[i] != b.s[i] || a.span(i + 1) > a.s[i] || b.span(i + 1) > b.s[i])
+        return kOthers;
+    const int64_t n = a.n[i], s = a.s[i], down = (apart >= 0 ? apart : apart - (s - 1)) / s;
+    int most = kNone;
+    for (int64_t j : {down, down + 1})
+        if (j > -n && j < n) {
+            const int got = shared_runs(a, b, apart - j * s, i + 1, moved || j != 0);
+            most = got > most ? got : most;
+        }
+    return most;
+}
+
+}  // namespace
+
+// The runs of a token that a compaction in place moves, each in a workgroup of its own:
+// heads that are one move once, and so do values that lie within the keys, or keys
+// within the values.  Runs that share memory otherwise are refused.
+int runs_in_place(const detfold_paged_cache &c, int32_t *keys, int32_t *values)
+{
+    Runs k = all_runs(c, false), v = all_runs(c, true);
+    for (const Runs *r : {&k, &v}) {
+        int64_t dims[3][2] = {{r->n[0], r->s[0]}, {r->n[1], r->s[1]}, {r->n[2], r->s[2]}};
+        if (!distinct3(dims, r->last))
+            return DETFOLD_EOVERLAP;
+    }
+    *keys = (int32_t)k.n[2], *values = (int32_t)v.n[2];
+    for (int i = 0; i < 2; ++i)  // the largest strides first
+        for (int j = 0; j < 2 - i; ++j) {
+            auto stride = [&](int d) { return k.n[d] > 1 ? k.s[d] : v.n[d] > 1 ? v.s[d] : 0; };
+            if (stride(j) < stride(j + 1))
+                for (Runs *r : {&k, &v}) {
+                    const int64_t n = r->n[j], s = r->s[j];
+                    r->n[j] = r->n[j + 1], r->s[j] = r->s[j + 1];
+                    r->n[j + 1] = n, r->s[j + 1] = s;
+                }
+        }
+    const int64_t apart = ((int64_t)(uintptr_t)c.v - (int64_t)(uintptr_t)c.k) / elem_size(c.type);
+    const int shared = shared_runs(k, v, apart);
+    if (shared == kNone)
+        return DETFOLD_OK;
+    if (shared == kSame && apart >= 0 && apart + c.v_dim <= c.dim)
+        *values = 0;
+    else if (shared == kSame && apart <= 0 && c.dim - apart <= c.v_dim)
+        *keys = 0;
+    else
+        return DETFOLD_EOVERLAP;
+    return DETFOLD_OK;
+}
+
+namespace {
+
 int chunks_of(int64_t bytes) { return (int)((bytes + 15) / 16); }
 
 // A token's runs: heads that lie beside each other, on both sides, are one.
@@ -418,14 +502,20 @@ int detfold_cache_copy(const detfold_paged_cache *cache, const detfold_paged_cac
 
 int detfold_cache_compact(const detfold_paged_cache *cache, const detfold_compact *args, void *stream)
 {
-    const int rc = check_compact(cache, args);
+    int rc = check_compact(cache, args);
     if (rc != DETFOLD_OK || args->batch == 0 || args->most == 0)
         return rc;
     CompactArgs k = {};
+    if (!args->to) {
+        int32_t keys = 0, values = 0;
+        if ((rc = runs_in_place(*cache, &keys, &values)) != DETFOLD_OK)
+            return rc;
+        k.k_runs = keys;
+        k.runs = divider((uint32_t)(keys + values));
+    }
     k.a = *args;
     k.m.k = runs_of(*cache, *cache, false), k.m.v = runs_of(*cache, *cache, true);
     k.k = compact_side(*cache, false), k.v = compact_side(*cache, true);
-    k.heads = divider((uint32_t)cache->heads);
     k.pages = cache->pages;
     k.page = divider((uint32_t)cache->page);
     k.most = divider((uint32_t)args->most);

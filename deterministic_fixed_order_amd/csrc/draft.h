@@ -86,7 +86,9 @@ struct CompactArgs {
     detfold_compact a;
     CompactSide k, v;
     int64_t pages;
-    Divider page, most, heads;
+    Divider page, most;
+    Divider runs;     // of a token, in place: its keys', k_runs of them, then its values'
+    int32_t k_runs;
     int64_t row0;
 };
 
@@ -97,6 +99,7 @@ int check_tree(const detfold_paged_cache *c, const detfold_tree *t);
 int check_copy(const detfold_paged_cache *c, const detfold_paged_cache *into, const int32_t *src, const int32_t *dst,
                const int32_t *tokens, int64_t count);
 int check_compact(const detfold_paged_cache *c, const detfold_compact *a);
+int runs_in_place(const detfold_paged_cache &c, int32_t *keys, int32_t *values);
 
 // --- tree_kernels.hip, page_kernels.hip: launches -----------------------------
 int launch_tree(const TreeArgs &a, void *stream);

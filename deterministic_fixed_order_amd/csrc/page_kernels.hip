@@ -149,8 +149,9 @@ template <bool ONCE> __global__ __launch_bounds__(kBlock) void k_gather(CompactA
     move_tokens<ONCE>(look, w.values ? p.m.v : p.m.k, side.head_bytes, side.head_bytes, w.first, w.tokens);
 }
 
-// The compaction in place.  A workgroup takes one head's keys or values of one row,
-// and of these as many tokens at a time as its threads hold, U chunks each.  A move
+// The compaction in place.  A workgroup takes one run, a head's keys or values, of one
+// row, and of its tokens as many at a time as its threads hold, U chunks each.  Nothing
+// orders workgroups, so no two runs share memory (runs_in_place).  A move
 // goes to a lower token: what is read with a tile of moves lies behind all that
 // earlier tiles wrote, and what it writes before all that later tiles read.  So the
 // one barrier between a tile's loads and its stores is enough, and the next tile's
@@ -158,8 +159,10 @@ template <bool ONCE> __global__ __launch_bounds__(kBlock) void k_gather(CompactA
 template <int U> __global__ __launch_bounds__(kBlock) void k_compact(CompactArgs p)
 {
     const detfold_compact &a = p.a;
-    const uint32_t y = divide(blockIdx.x >> 1, p.heads), head = (blockIdx.x >> 1) - y * p.heads.d;
-    const CompactSide &r = blockIdx.x & 1 ? p.v : p.k;
+    const uint32_t y = divide(blockIdx.x, p.runs), run = blockIdx.x - y * p.runs.d;
+    const bool values = run >= (uint32_t)p.k_runs;
+    const uint32_t head = run - (values ? p.k_runs : 0);
+    const CompactSide &r = values ? p.v : p.k;
     const int64_t b = p.row0 + y;
     const int32_t *table = a.table + b * a.table_row;
     const int64_t start = a.starts ? a.starts[b] : 0, n = min((int64_t)a.counts[b], a.most);
@@ -254,7 +257,7 @@ int launch_compact(const CompactArgs &a, void *stream)
 {
     CompactArgs p = a;
     if (!a.a.to) {
-        const int64_t each = 2 * (int64_t)a.heads.d, some = kMaxBlocks / each;
+        const int64_t each = a.runs.d, some = kMaxBlocks / each;
         for (p.row0 = 0; p.row0 < a.a.batch; p.row0 += some)
             if (!launch((const void *)k_compact<4>, (a.a.batch - p.row0 < some ? a.a.batch - p.row0 : some) * each, &p, stream))
                 return DETFOLD_ELAUNCH;

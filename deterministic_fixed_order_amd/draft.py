@@ -232,9 +232,11 @@ def cache_compact(cache, table, picks, counts, *, starts=None, to=None, stream=N
     becomes what token ``starts[b] + picks[b, i]`` was (int32 [batch, most]; ``starts``: int32 [batch], default 0).
     ``table`` (int32 [batch, width]) names the rows' pages.
 
-    In place, as if all tokens were read before any is written; a pick below its own i is left out.  With ``to``
-    (int32 [batch, width]) the tokens go to the pages that it names, of which none may be read in this call.  Moves
-    from or to tokens that the tables, or the cache, do not have are left out.  A written page may be one row's only."""
+    In place, as if all tokens were read before any is written; a pick below its own i is left out.  A cache whose
+    values are a view within its keys, or its keys within its values, or whose heads are one (expanded), moves once;
+    one whose tokens share memory otherwise is refused.  With ``to`` (int32 [batch, width]) the tokens go to the pages
+    that it names, of which none may be read in this call.  Moves from or to tokens that the tables, or the cache, do
+    not have are left out.  A written page may be one row's only."""
     dev = cache.device_index
     native = _native or _bound()
     raw, here, call, of = native[0], native[1], native[6], native[7]

@@ -620,15 +620,17 @@ int detfold_cache_copy(const detfold_paged_cache *cache, const detfold_paged_cac
  *   table   device, int32 [batch][table_width] at table_row: the rows' pages
  *   to      device, int32 [batch][to_width] at to_row, or NULL.  NULL: in place,
  *           as if all tokens were read before any is written; a pick below its own
- *           i is then left out.  Else the moved tokens go to the pages that `to`
- *           names, none of which may be read in this call
+ *           i is then left out, and the cache's slots share no memory, but that a
+ *           slot's heads may be one (a stride of 0), and its values lie within its
+ *           keys or its keys within its values.  Else the moved tokens go to the
+ *           pages that `to` names, none of which may be read in this call
  *   picks   device, int32 [batch][most]; with `to` most is at most 2^22
  *   counts  device, int32 [batch], each taken as 0 .. most
  *   starts  device, int32 [batch], or NULL: 0
  * A move from or to a token that the table, or the cache, does not have is left
  * out.  A page that is written may be one row's only, and there once.
- * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP (an array lies in the cache),
- * DETFOLD_ELAUNCH.
+ * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP (an array lies in the cache, or in place
+ * slots share memory otherwise), DETFOLD_ELAUNCH.
  */
 typedef struct detfold_compact {
     const int32_t *table, *to, *picks, *counts, *starts;
