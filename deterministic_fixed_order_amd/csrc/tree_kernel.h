@@ -23,7 +23,8 @@
 //   1000 25 us, 32 x 64 over 4096 419).  A mask is looked at four tokens at a time.
 // * Values that are infinite or no number are zeroed where some query may not see them
 //   (zero times them is NaN), and added at the end, once, to the sums of those that do.
-// * A capped score takes 9 instructions below half its cap, a polynomial, and 25 above.
+// * A capped score takes 9 instructions below half its cap, a polynomial, and 21 where a
+//   wave has one above.
 #ifndef DETFOLD_TREE_KERNEL_H
 #define DETFOLD_TREE_KERNEL_H
 
@@ -42,17 +43,22 @@ __device__ __forceinline__ const TreeArgs &tree_arguments()
 
 // tanh, held to 24 units of 2^-24 relative.  Below 0.5 x + x^3 P(x^2), whose four
 // coefficients were fitted to the smallest relative error (1.3 units there); above
-// from exp(-2 |x|), of which the largest, e^-1, gives 4.
-__device__ __forceinline__ float tanh_factor(float z)  // P(z)
+// from exp(-2 |x|), of which the largest, e^-1, gives 4.  A capped score takes the one
+// or the other by itself alone: of `line`, the score without its cap, and y, that over
+// the cap, `near_cap` is the same to the last bit where a wave needs the other for some
+// of its scores and where it does not, since what it needs goes by slots that no query
+// sees too.
+__device__ __forceinline__ float near_cap(float line, float y)
 {
-    return __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 0.0172357764f, -0.0530423597f), z, 0.133258238f), z, -0.333331406f);
+    const float z = y * y, p = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 0.0172357764f, -0.0530423597f), z, 0.133258238f), z, -0.333331406f);
+    return __builtin_fmaf(line * z, p, line);
 }
-__device__ __forceinline__ float tanh_any(float x)
+__device__ __forceinline__ float any_cap(float line, float y, float cap)
 {
-    const float z = x * x, e = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * (-2.0f * kLog2e));
-    float near = __builtin_fmaf(x * z, tanh_factor(z), x), far = __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), x);
+    const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(y) * (-2.0f * kLog2e));
+    float near = near_cap(line, y), far = cap * __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), y);
     asm("" : "+v"(near), "+v"(far));  // both, without a branch for each
-    return z < 0.25f ? near : far;
+    return __builtin_fabsf(y) < 0.5f ? near : far;
 }
 
 // The nearest finite number: zero times it is zero.
@@ -562,12 +568,9 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     return z;
                 });
                 if (__any(!(most * __builtin_fabsf(over) < 0.5f)))
-                    every([&](float z) { return cap * kLog2e * tanh_any(z * over); });
+                    every([&](float z) { return any_cap(z * by, z * over, cap * kLog2e); });
                 else
-                    every([&](float z) {
-                        const float y = z * over, straight = z * by;
-                        return __builtin_fmaf(straight * (y * y), tanh_factor(y * y), straight);
-                    });
+                    every([&](float z) { return near_cap(z * by, z * over); });
             } else {
                 every([&](float z) { return z * by; });
             }
