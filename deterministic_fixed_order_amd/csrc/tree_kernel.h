@@ -23,7 +23,7 @@
 //   1000 25 us, 32 x 64 over 4096 419).  A mask is looked at four tokens at a time.
 // * Values that are infinite or no number are zeroed where some query may not see them
 //   (zero times them is NaN), and added at the end, once, to the sums of those that do.
-// * A capped score takes 9 instructions below half its cap, a polynomial, and 21 where a
+// * A capped score takes 9 instructions below half its cap, a polynomial, and 19 where a
 //   wave has one above.
 #ifndef DETFOLD_TREE_KERNEL_H
 #define DETFOLD_TREE_KERNEL_H
@@ -43,11 +43,10 @@ __device__ __forceinline__ const TreeArgs &tree_arguments()
 
 // tanh, held to 24 units of 2^-24 relative.  Below 0.5 x + x^3 P(x^2), whose four
 // coefficients were fitted to the smallest relative error (1.3 units there); above
-// from exp(-2 |x|), of which the largest, e^-1, gives 4.  A capped score takes the one
-// or the other by itself alone: of `line`, the score without its cap, and y, that over
-// the cap, `near_cap` is the same to the last bit where a wave needs the other for some
-// of its scores and where it does not, since what it needs goes by slots that no query
-// sees too.
+// from exp(-2 |x|), of which the largest, e^-1, gives 4.  `line` is a score without its
+// cap, y that over the cap.  A score's bits are its own: whether a wave takes near_cap
+// for all of its scores or any_cap goes by the largest, and so by slots that no query
+// sees, but below 0.5 both give the same to the last bit.
 __device__ __forceinline__ float near_cap(float line, float y)
 {
     const float z = y * y, p = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(z, 0.0172357764f, -0.0530423597f), z, 0.133258238f), z, -0.333331406f);
@@ -60,9 +59,6 @@ __device__ __forceinline__ float any_cap(float line, float y, float cap)
     asm("" : "+v"(near), "+v"(far));  // both, without a branch for each
     return __builtin_fabsf(y) < 0.5f ? near : far;
 }
-
-// The nearest finite number: zero times it is zero.
-__device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -0x1.fffffep127f), 0x1.fffffep127f); }
 
 // Scores are held times log2 e here, so that a weight is exp2 of a distance: a score
 // of more than 2^127 / log2 e counts as infinite.
@@ -198,8 +194,15 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         const int c_dim = c.dim;
         const float cap = p.cap;
         const bool biased = p.slopes != nullptr, placed = biased || p.window > 0;  // whether positions matter
-        const float scale = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f), by = finite(scale * kLog2e);
-        const float over = cap > 0.0f ? finite(scale / cap) : 0.0f;  // of a product, to the argument of the tanh
+        // What products become scores by, times log2 e.  The host has looked at the scale
+        // and the cap; a key scale that is no number, or takes the factor past binary32,
+        // makes its head's scores no numbers.
+        const float factor = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f) * kLog2e;
+        const float by = __builtin_fabsf(factor) < INFINITY ? factor : __builtin_nanf("");
+        // What products become arguments of the tanh by: its largest value where it passes
+        // binary32, which makes one of all but subnormal products all the same.
+        const float bound = cap * kLog2e, ratio = by / bound;
+        const float over = __builtin_fabsf(ratio) == INFINITY ? __builtin_copysignf(0x1.fffffep127f, ratio) : ratio;
         const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;
 
         // Where a lane's loads lie within a key and a value.
@@ -568,7 +571,10 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                     return z;
                 });
                 if (__any(!(most * __builtin_fabsf(over) < 0.5f)))
-                    every([&](float z) { return any_cap(z * by, z * over, cap * kLog2e); });
+                    every([&](float z) {
+                        asm("" : "+v"(z));  // what both paths compute does not move before the branch, which would copy all scores
+                        return any_cap(z * by, z * over, bound);
+                    });
                 else
                     every([&](float z) { return near_cap(z * by, z * over); });
             } else {

@@ -117,8 +117,9 @@ def attend_tree(out, q, cache, table, lens, *, masks=None, counts=None, depths=N
     them where there are masks.  With ``window`` a token sees less than so many positions back.
 
     ``cap`` > 0: scores become cap * tanh(score / cap); then ``slopes`` (float32 [q_heads]) add slope * (position of
-    the token seen - own position); none of these, nor ``scale``, may pass 2^127.  A token that sees nothing gives 0 and
-    -infinity.  All else as ``attend_paged``, the ``workspace`` from ``attend_workspace(..., drafts=drafts)``."""
+    the token seen - own position); none of these, nor ``scale``, may pass 2^127.  A key scale that is no number, or
+    takes ``scale`` past that, gives NaN.  A token that sees nothing gives 0 and -infinity.  All else as
+    ``attend_paged``, the ``workspace`` from ``attend_workspace(..., drafts=drafts)``."""
     dev = cache.device_index
     raw, here, call, of = (_native or _bound())[:4]
     if here() == dev:

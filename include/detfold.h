@@ -558,7 +558,8 @@ int detfold_fold_softmax(void *out, const void *outs, const float *lses, float *
  *   attend    as detfold_attend_paged's arguments; q and out are [batch][drafts]
  *             [q_heads][...], lse is [batch][drafts][q_heads]; lens count the
  *             drafted tokens.  A length or page out of range gives NaN in that
- *             row's out and lse
+ *             row's out and lse; a key scale that is no number, or that times
+ *             scale passes 2^127, in its head's
  *   masks     device, int64 [batch][drafts], or NULL: a chain, whose token i sees
  *             the drafted tokens 0 .. i.  A token sees itself only if its own bit
  *             says so
