@@ -270,8 +270,9 @@ typedef int (*CopyFn)(const detfold_paged_cache *, const detfold_paged_cache *, 
                       void *);
 typedef int (*CompactFn)(const detfold_paged_cache *, const detfold_compact *, void *);
 
-// A float, or a whole number in place of one.
-bool real(PyObject *o, float *to)
+// A float, or a whole number in place of one.  One that binary32 takes for another
+// kind of number, infinity or, where that means something else, zero, is left.
+bool real(PyObject *o, float *to, bool zero_means_none = false)
 {
     double v = 0.0;
     if (PyFloat_Check(o)) {
@@ -286,7 +287,7 @@ bool real(PyObject *o, float *to)
         return false;
     }
     *to = (float)v;
-    return std::isfinite(v) == std::isfinite(*to);
+    return std::isfinite(v) == std::isfinite(*to) && !(zero_means_none && v != 0.0 && *to == 0.0f);
 }
 
 // An optional contiguous tensor.
@@ -316,7 +317,7 @@ PyObject *tree(PyObject *, PyObject *const *args, Py_ssize_t n)
     detfold_attend &a = t.attend;
     a.window = num.whole(args[14]), a.max_len = num.whole(args[15]);
     const int64_t split = num.whole(args[18]);
-    if (!num.ok || !real(args[11], &t.cap) || !real(args[13], &a.scale) || split < 0 || split > INT32_MAX || !q.on(dev) || !out.on(dev))
+    if (!num.ok || !real(args[11], &t.cap, true) || !real(args[13], &a.scale) || split < 0 || split > INT32_MAX || !q.on(dev) || !out.on(dev))
         return not_taken();
     const int64_t dims = num.whole(args[19]), batch = q.t->size(0);
     if ((dims != 3 && dims != 4) || q.t->dim() != dims || out.t->dim() != dims)

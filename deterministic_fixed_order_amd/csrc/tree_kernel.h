@@ -199,8 +199,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
         // makes its head's scores no numbers.
         const float factor = a.scale * (c.k_scale ? scalar_load(c.k_scale + h) : 1.0f) * kLog2e;
         const float by = __builtin_fabsf(factor) < INFINITY ? factor : __builtin_nanf("");
-        // What products become arguments of the tanh by: its largest value where it passes
-        // binary32, which makes one of all but subnormal products all the same.
+        // What products become arguments of the tanh by: where that passes binary32 its
+        // largest value, with which only products near the smallest are not past 4.
         const float bound = cap * kLog2e, ratio = by / bound;
         const float over = __builtin_fabsf(ratio) == INFINITY ? __builtin_copysignf(0x1.fffffep127f, ratio) : ratio;
         const float v_scale = c.v_scale ? scalar_load(c.v_scale + h) : 1.0f;

@@ -172,6 +172,8 @@ def _attend(what, out, q, cache, table, lens, masks, counts, depths, cap, slopes
         for t, name, kind, shape in ((masks, "masks", "int64", (batch, drafts)), (counts, "counts", "int32", (batch,)),
                                      (depths, "depths", "int32", (batch, drafts)), (slopes, "slopes", "float32", (q_heads,)),
                                      (lse, "lse", "float32", (batch, drafts, q_heads))))
+    if cap and ctypes.c_float(cap).value == 0.0:  # in the library 0 is no cap at all
+        raise ValueError("cap must be 0 or a normal float32, got %r" % (cap,))
     if masks is not None and depths is None and (window or slopes is not None):
         raise ValueError("masks with a window or slopes need depths")
     if max_len is None:
