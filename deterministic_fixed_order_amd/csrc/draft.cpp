@@ -214,66 +214,6 @@ int check_tree(const detfold_paged_cache *c, const detfold_tree *t)
     return DETFOLD_OK;
 }
 
-int check_copy(const detfold_paged_cache *c, const detfold_paged_cache *into, const int32_t *src, const int32_t *dst,
-               const int32_t *tokens, int64_t count)
-{
-    int rc = check_cache(c);
-    if (rc != DETFOLD_OK || (into && (rc = check_cache(into)) != DETFOLD_OK))
-        return rc;
-    if (into && (into->page != c->page || into->heads != c->heads || into->dim != c->dim || into->v_dim != c->v_dim || into->type != c->type))
-        return DETFOLD_EINVAL;
-    if (count < 0 || count >= kMaxCount || c->page > kMaxMoved)
-        return DETFOLD_EINVAL;
-    if (count == 0)
-        return DETFOLD_OK;
-    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(tokens, 4))
-        return DETFOLD_EINVAL;
-    const Range from[] = {cache_range(*c, false), cache_range(*c, true)};
-    const detfold_paged_cache &w = into ? *into : *c;
-    const Range to[] = {cache_range(w, false), cache_range(w, true)};
-    const Range lists[] = {range(src, count, 4), range(dst, count, 4), range(tokens, count, 4)};
-    for (const Range &t : to) {
-        for (const Range &r : lists)
-            if (meet(t, r))
-                return DETFOLD_EOVERLAP;
-        if (into && !same_cache(*c, *into))
-            for (const Range &r : from)
-                if (meet(t, r))
-                    return DETFOLD_EOVERLAP;
-    }
-    return DETFOLD_OK;
-}
-
-int check_compact(const detfold_paged_cache *c, const detfold_compact *a)
-{
-    int rc = check_cache(c);
-    if (rc != DETFOLD_OK)
-        return rc;
-    if (!a || a->batch < 0 || a->batch >= kMaxCount || a->most < 0 || a->most >= kMaxCount || a->table_row < 0 || a->table_width < 0 ||
-        (a->to && (a->to_row < 0 || a->to_width < 0)))
-        return DETFOLD_EINVAL;
-    if (a->batch == 0 || a->most == 0)
-        return DETFOLD_OK;
-    if (!a->picks || !a->counts || (a->table_width > 0 && !a->table))
-        return DETFOLD_EINVAL;
-    for (const void *p : {a->table, a->to, a->picks, a->counts, a->starts})
-        if (!aligned(p, 4))
-            return DETFOLD_EINVAL;
-    if (a->to && a->most > kMaxMoved)
-        return DETFOLD_EINVAL;
-    const int64_t ts = a->table_width > 0 ? span2(a->batch, a->table_row, 1, 0, a->table_width) : 0;
-    const int64_t os = a->to && a->to_width > 0 ? span2(a->batch, a->to_row, 1, 0, a->to_width) : 0;
-    if (ts < 0 || os < 0 || a->most > kMaxElems / a->batch)
-        return DETFOLD_EINVAL;
-    const Range in[] = {range(a->table, ts, 4), range(a->to, os, 4), range(a->picks, a->batch * a->most, 4), range(a->counts, a->batch, 4),
-                        range(a->starts, a->batch, 4)};
-    const Range k = cache_range(*c, false), v = cache_range(*c, true);
-    for (const Range &r : in)
-        if (meet(k, r) || meet(v, r))
-            return DETFOLD_EOVERLAP;
-    return DETFOLD_OK;
-}
-
 namespace {
 
 // The runs of a cache's keys or values, [pages][page][heads] of `last` elements each.
@@ -355,6 +295,84 @@ int runs_in_place(const detfold_paged_cache &c, int32_t *keys, int32_t *values)
         *keys = 0;
     else
         return DETFOLD_EOVERLAP;
+    return DETFOLD_OK;
+}
+
+namespace {
+
+// Whether a token copied from c to w writes no element of w with two values: what is one
+// memory in w, heads or keys and values, is so in c.
+bool takes_copies(const detfold_paged_cache &c, const detfold_paged_cache &w)
+{
+    int32_t ck, cv, wk, wv;
+    const intptr_t c_apart = (intptr_t)c.v - (intptr_t)c.k, w_apart = (intptr_t)w.v - (intptr_t)w.k;
+    if (runs_in_place(w, &wk, &wv) != DETFOLD_OK)  // as it is in c, if that lies the same
+        return c_apart == w_apart && c.k_page == w.k_page && c.k_token == w.k_token && c.k_head == w.k_head && c.v_page == w.v_page &&
+               c.v_token == w.v_token && c.v_head == w.v_head;
+    if (wk == w.heads && wv == w.heads)
+        return true;
+    return runs_in_place(c, &ck, &cv) == DETFOLD_OK && ck == wk && cv == wv && (wk * wv != 0 || c_apart == w_apart);
+}
+
+}  // namespace
+
+int check_copy(const detfold_paged_cache *c, const detfold_paged_cache *into, const int32_t *src, const int32_t *dst,
+               const int32_t *tokens, int64_t count)
+{
+    int rc = check_cache(c);
+    if (rc != DETFOLD_OK || (into && (rc = check_cache(into)) != DETFOLD_OK))
+        return rc;
+    if (into && (into->page != c->page || into->heads != c->heads || into->dim != c->dim || into->v_dim != c->v_dim || into->type != c->type))
+        return DETFOLD_EINVAL;
+    if (count < 0 || count >= kMaxCount || c->page > kMaxMoved)
+        return DETFOLD_EINVAL;
+    if (count == 0)
+        return DETFOLD_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(tokens, 4))
+        return DETFOLD_EINVAL;
+    const Range from[] = {cache_range(*c, false), cache_range(*c, true)};
+    const detfold_paged_cache &w = into ? *into : *c;
+    const Range to[] = {cache_range(w, false), cache_range(w, true)};
+    const Range lists[] = {range(src, count, 4), range(dst, count, 4), range(tokens, count, 4)};
+    for (const Range &t : to) {
+        for (const Range &r : lists)
+            if (meet(t, r))
+                return DETFOLD_EOVERLAP;
+        if (into && !same_cache(*c, *into))
+            for (const Range &r : from)
+                if (meet(t, r))
+                    return DETFOLD_EOVERLAP;
+    }
+    return into && !takes_copies(*c, *into) ? DETFOLD_EOVERLAP : DETFOLD_OK;
+}
+
+int check_compact(const detfold_paged_cache *c, const detfold_compact *a)
+{
+    int rc = check_cache(c);
+    if (rc != DETFOLD_OK)
+        return rc;
+    if (!a || a->batch < 0 || a->batch >= kMaxCount || a->most < 0 || a->most >= kMaxCount || a->table_row < 0 || a->table_width < 0 ||
+        (a->to && (a->to_row < 0 || a->to_width < 0)))
+        return DETFOLD_EINVAL;
+    if (a->batch == 0 || a->most == 0)
+        return DETFOLD_OK;
+    if (!a->picks || !a->counts || (a->table_width > 0 && !a->table))
+        return DETFOLD_EINVAL;
+    for (const void *p : {a->table, a->to, a->picks, a->counts, a->starts})
+        if (!aligned(p, 4))
+            return DETFOLD_EINVAL;
+    if (a->to && a->most > kMaxMoved)
+        return DETFOLD_EINVAL;
+    const int64_t ts = a->table_width > 0 ? span2(a->batch, a->table_row, 1, 0, a->table_width) : 0;
+    const int64_t os = a->to && a->to_width > 0 ? span2(a->batch, a->to_row, 1, 0, a->to_width) : 0;
+    if (ts < 0 || os < 0 || a->most > kMaxElems / a->batch)
+        return DETFOLD_EINVAL;
+    const Range in[] = {range(a->table, ts, 4), range(a->to, os, 4), range(a->picks, a->batch * a->most, 4), range(a->counts, a->batch, 4),
+                        range(a->starts, a->batch, 4)};
+    const Range k = cache_range(*c, false), v = cache_range(*c, true);
+    for (const Range &r : in)
+        if (meet(k, r) || meet(v, r))
+            return DETFOLD_EOVERLAP;
     return DETFOLD_OK;
 }
 

@@ -206,7 +206,8 @@ def _table(t, name: str, dev: int, batch: int):
 def cache_copy(cache, src, dst, *, tokens=None, into=None, stream=None) -> None:
     """Copy pages: page ``dst[i]`` becomes what page ``src[i]`` holds, keys and values (int32 [count] each).  With
     ``tokens`` (int32 [count]) only the first ``tokens[i]`` slots of a page; with ``into``, another ``PagedCache`` of
-    the same page size, heads, head sizes and type, the pages of that one are written.
+    the same page size, heads, head sizes and type, the pages of that one are written; one whose values are a view of
+    its keys takes copies of such caches alone.
 
     A pair of which either page is not in its cache (-1) is left out.  The copies run in no order: no page may be both
     written and read, or written twice, in one call.  Scales are not copied."""

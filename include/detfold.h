@@ -599,7 +599,8 @@ int detfold_tree_workspace(const detfold_paged_cache *cache, int64_t batch, int3
  * page src[i] of `cache`, keys and values, for each i below count (a request's
  * fork, which copies its last page; a pool that is moved or closed up).
  *   into    a cache of the same page size, heads, head sizes and type, whose pages
- *           may lie in another order of memory; NULL: `cache` itself
+ *           may lie in another order of memory; NULL: `cache` itself.  Where its
+ *           heads, or its keys and values, are one memory, those of `cache` are too
  *   src,    device, int32 [count].  A pair of which either page is not in its
  *   dst     cache is left out (padding of a list)
  *   tokens  device, int32 [count], or NULL: only the first tokens[i] slots of the
@@ -608,7 +609,8 @@ int detfold_tree_workspace(const detfold_paged_cache *cache, int64_t batch, int3
  * twice, in one call.  Scales of 8-bit caches are not touched.  A page has at most
  * 2^22 tokens.
  * Errors: DETFOLD_EINVAL, DETFOLD_EOVERLAP (`into` shares memory with `cache`
- * and is not it; a list lies in a cache), DETFOLD_ELAUNCH.
+ * and is not it, or within itself what `cache` does not; a list lies in a cache),
+ * DETFOLD_ELAUNCH.
  */
 int detfold_cache_copy(const detfold_paged_cache *cache, const detfold_paged_cache *into, const int32_t *src,
                        const int32_t *dst, const int32_t *tokens, int64_t count, void *stream);
