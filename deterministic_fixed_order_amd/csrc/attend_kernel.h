@@ -140,12 +140,6 @@ template <typename F> __device__ __forceinline__ float over_groups(float x, F f)
 // would wait for them.
 template <typename T> __device__ __forceinline__ T scalar_load(const T *p) { return *(const __attribute__((address_space(4))) T *)p; }
 
-__device__ __forceinline__ int64_t from_lane(int64_t x, int l)
-{
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)x), hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)(x >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 // The kernel's arguments, read anew: held across a loop they would fill the
 // scalar registers, and then vector ones.
 typedef const __attribute__((address_space(4))) AttendArgs *ArgsPtr;

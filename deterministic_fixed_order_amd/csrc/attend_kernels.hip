@@ -8,8 +8,6 @@
 namespace detfold_impl {
 namespace {
 
-constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds at most 2^32 threads
-
 // One workgroup per query head and row, or share that a row may begin in without
 // ending there.  A lane takes four dims, LANES lanes a part, and the groups of
 // lanes every GROUPS-th part; their sums are added in order.  Parts that are

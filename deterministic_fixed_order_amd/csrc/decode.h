@@ -19,6 +19,7 @@ constexpr int elem_size(int type)
 }
 
 constexpr float kE4m3Max = 448.0f;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // workgroups of a launch: a grid holds at most 2^32 threads
 
 // x / d for 0 <= x < 2^31 and 1 <= d < 2^31 as a multiply and a shift: with
 // s = ceil(log2 d) and m = ceil(2^(31+s) / d) (below 2^32), x * m >> (31 + s)

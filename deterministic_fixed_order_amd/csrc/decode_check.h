@@ -24,7 +24,6 @@ constexpr int64_t kShortRow = 512;                // tokens that are not worth c
 constexpr int64_t kStepBytes = 32768;
 constexpr int64_t kMaxEven = 4096;                // rows that every workgroup adds up the lengths of
 constexpr int64_t kLongPart = 8192;               // tokens of a part where there are more rows
-constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // workgroups of a launch, well below what a grid takes
 
 inline bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 

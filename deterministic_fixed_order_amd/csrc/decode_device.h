@@ -37,6 +37,13 @@ __device__ __forceinline__ uint32_t divide(uint32_t x, const Divider &d)
     return (uint32_t)(((uint64_t)x * d.magic) >> d.shift);
 }
 
+// A value of lane l.
+__device__ __forceinline__ int64_t from_lane(int64_t x, int l)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)x), hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 }  // namespace detfold_impl
 
 #endif  // DETFOLD_DECODE_DEVICE_H

@@ -14,7 +14,6 @@ namespace detfold_impl {
 namespace {
 
 constexpr int64_t kFewSteps = 4;
-constexpr int64_t kMaxMoved = (int64_t)1 << 22;  // tokens of a page, or of a row, that one launch moves
 
 // Whether a written [n0][n1][n2][last] buffer has no element twice: in the order
 // of the strides, each passes what lies within it.
@@ -48,10 +47,6 @@ bool same_cache(const detfold_paged_cache &a, const detfold_paged_cache &b)
     return a.k == b.k && a.v == b.v && a.pages == b.pages && a.k_page == b.k_page && a.k_token == b.k_token && a.k_head == b.k_head &&
            a.v_page == b.v_page && a.v_token == b.v_token && a.v_head == b.v_head;
 }
-
-}  // namespace
-
-namespace {
 
 // Whether heads are whole chunks of 16 bytes, at such addresses, and pages and tokens
 // less than 2^31 bytes apart.
@@ -118,7 +113,8 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     p->brief = seen <= 32;
     const int64_t groups = units / p->beside;
     const int fit = 1024 / (wide_head * elem_size(c.type)), most_tiles = tiles > 1 || wide_head == 256 ? 2 : 4;
-    // Three steps of a wave take less than a join, as for one token.
+    // Three steps of each of four waves take less than a join, as for one token.  Straight
+    // to registers trees have eight waves to a workgroup, for which it is half of that.
     const int64_t few = p->shared ? 3 * 32 * (p->waves / p->shared) : 3 * 16 * (fit < most_tiles ? fit : most_tiles) * (4 / p->beside);
     int64_t part = split > 0 ? split : kLongPart;
     if (split == 0) {

@@ -9,6 +9,8 @@
 
 namespace detfold_impl {
 
+constexpr int64_t kMaxMoved = (int64_t)1 << 22;  // tokens of a page, or of a row, that one launch moves
+
 // Kernel arguments of the attention of drafted tokens.  The base's window is
 // widened by the drafted tokens, so that a row's first seen token is one that
 // any of its queries may see; `window` is the caller's.

@@ -10,9 +10,7 @@ namespace detfold_impl {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int64_t kMaxItems = (int64_t)1 << 22;  // tokens of a launch, or one row's or page's
-constexpr int64_t kMaxBlocks = (int64_t)1 << 22; // workgroups of a launch
-constexpr int64_t kOnceBytes = 8 << 20;          // that are not kept in the caches
+constexpr int64_t kOnceBytes = 8 << 20;  // that are not kept in the caches
 
 // 16 bytes at any alignment, as one wide load or store; once: not kept in the caches.
 typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(1)));
@@ -23,12 +21,6 @@ template <bool ONCE> __device__ __forceinline__ void store16(char *p, u4 x)
         __builtin_nontemporal_store(x, (u4 *)p);
     else
         *(u4 *)p = x;
-}
-
-__device__ __forceinline__ int64_t from_lane(int64_t x, int l)
-{
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)x), hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * l, (int)(x >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
 // What a copy, or a compaction into other pages, moves: token by token, each token a
@@ -150,13 +142,14 @@ template <bool ONCE> __global__ __launch_bounds__(kBlock) void k_gather(CompactA
 }
 
 // The compaction in place.  A workgroup takes one run, a head's keys or values, of one
-// row, and of its tokens as many at a time as its threads hold, U chunks each.  Nothing
+// row, and of its tokens as many at a time as its threads hold, kTurns chunks each.  Nothing
 // orders workgroups, so no two runs share memory (runs_in_place).  A move
 // goes to a lower token: what is read with a tile of moves lies behind all that
 // earlier tiles wrote, and what it writes before all that later tiles read.  So the
 // one barrier between a tile's loads and its stores is enough, and the next tile's
 // loads go out before this one's stores.
-template <int U> __global__ __launch_bounds__(kBlock) void k_compact(CompactArgs p)
+constexpr int kTurns = 4;
+__global__ __launch_bounds__(kBlock) void k_compact(CompactArgs p)
 {
     const detfold_compact &a = p.a;
     const uint32_t y = divide(blockIdx.x, p.runs), run = blockIdx.x - y * p.runs.d;
@@ -171,13 +164,13 @@ template <int U> __global__ __launch_bounds__(kBlock) void k_compact(CompactArgs
     const Places places = {r.pool + head * r.head_bytes + at, r.page_bytes, r.token_bytes, (int32_t)p.pages, p.page};
 
     struct Tile {
-        u4 data[U];
-        char *put[U];
+        u4 data[kTurns];
+        char *put[kTurns];
     };
     auto load = [&](int64_t i0) {
         Tile x;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
+        for (int j = 0; j < kTurns; ++j) {
             const int64_t i = i0 + j * beside + t;
             x.put[j] = nullptr;
             x.data[j] = u4{};
@@ -198,14 +191,14 @@ template <int U> __global__ __launch_bounds__(kBlock) void k_compact(CompactArgs
     if (n <= 0)
         return;
     Tile now = load(0);
-    for (int64_t i0 = 0; i0 < n; i0 += beside * U) {
-        Tile next = load(i0 + beside * U);
+    for (int64_t i0 = 0; i0 < n; i0 += beside * kTurns) {
+        Tile next = load(i0 + beside * kTurns);
 #pragma unroll
-        for (int j = 0; j < U; ++j)  // what this tile read is there before any of it is written over
+        for (int j = 0; j < kTurns; ++j)  // what this tile read is there before any of it is written over
             asm volatile("" : "+v"(now.data[j]));
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < U; ++j)
+        for (int j = 0; j < kTurns; ++j)
             if (now.put[j])
                 *(u4 *)now.put[j] = now.data[j];
         now = next;
@@ -217,10 +210,6 @@ bool launch(const void *k, int64_t blocks, void *args, void *stream)
     void *list[] = {args};
     return hipLaunchKernel(k, dim3((unsigned)blocks), dim3(kBlock), list, 0, static_cast<hipStream_t>(stream)) == hipSuccess;
 }
-
-}  // namespace
-
-namespace {
 
 // How a launch's tokens are dealt out: a wave takes up to 64, but no more than leave
 // waves four times over what the device holds at once, nor than 2048 chunks (110.7 us
@@ -243,7 +232,7 @@ MoveArgs deal(MoveArgs m, int64_t tokens)
 int launch_copy_pages(const CopyArgs &a, int64_t count, void *stream)
 {
     CopyArgs p = a;
-    const int64_t some = kMaxItems / a.page.d;  // pages of a launch
+    const int64_t some = kMaxMoved / a.page.d;  // pages of a launch
     const bool once = count * a.page.d * (int64_t)(a.m.k.token.d + a.m.v.token.d) * 16 >= kOnceBytes;
     for (p.first = 0; p.first < count; p.first += some) {
         p.m = deal(a.m, (count - p.first < some ? count - p.first : some) * a.page.d);
@@ -259,11 +248,11 @@ int launch_compact(const CompactArgs &a, void *stream)
     if (!a.a.to) {
         const int64_t each = a.runs.d, some = kMaxBlocks / each;
         for (p.row0 = 0; p.row0 < a.a.batch; p.row0 += some)
-            if (!launch((const void *)k_compact<4>, (a.a.batch - p.row0 < some ? a.a.batch - p.row0 : some) * each, &p, stream))
+            if (!launch((const void *)k_compact, (a.a.batch - p.row0 < some ? a.a.batch - p.row0 : some) * each, &p, stream))
                 return DETFOLD_ELAUNCH;
         return DETFOLD_OK;
     }
-    const int64_t some = a.a.most < kMaxItems ? kMaxItems / a.a.most : 1;  // rows of a launch
+    const int64_t some = a.a.most < kMaxMoved ? kMaxMoved / a.a.most : 1;  // rows of a launch
     const bool once = a.a.batch * a.a.most * (int64_t)(a.m.k.token.d + a.m.v.token.d) * 16 >= kOnceBytes;
     for (p.row0 = 0; p.row0 < a.a.batch; p.row0 += some) {
         p.m = deal(a.m, (a.a.batch - p.row0 < some ? a.a.batch - p.row0 : some) * a.a.most);

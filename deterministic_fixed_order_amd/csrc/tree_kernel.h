@@ -310,7 +310,7 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
                 const char *k = k0 + (TILED ? valid(g.id[u % IDS]) * k_page + g.off[u % IDS] * k_token : from_lane(at, 16 * u + col));
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
-                    kw[u][i] = load_words<16, KEEP == kNothing>(k + anew(k_at[i]));
+                    kw[u][i] = load_words<16, false>(k + anew(k_at[i]));
             }
         };
         auto load_values = [&](const Pages &g) {
@@ -869,7 +869,8 @@ __global__ __launch_bounds__(tree_heavy(QT, D) ? 256 : 512) void k_tree(TreeArgs
 }
 
 // The kernel of a call and the LDS it takes: for a unit's queries and columns, and
-// for the sums of a wave's tile.
+// for the sums of a wave's tile.  Keys stay in the caches, also where attend_keep would
+// rather have nothing kept: trees have no instance for that.
 template <typename C, int QK, int PV, int D, int QT, int MOST, int KEEP> TreeKernel pick_tree_tiled(const TreeArgs &a)
 {
     typedef Attend<C, QK, PV, D, true, MOST, KEEP> S;

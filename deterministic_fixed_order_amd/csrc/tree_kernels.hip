@@ -8,8 +8,7 @@
 namespace detfold_impl {
 namespace {
 
-constexpr int kBlock = 256;                       // threads of the join
-constexpr int64_t kMaxBlocks = (int64_t)1 << 22;  // of a launch: a grid holds at most 2^32 threads
+constexpr int kBlock = 256;  // threads of the join
 
 // The sums of each query of a row, or of the row that a share begins without
 // ending it, joined in order.  A lane takes four dims, LANES lanes a part, and
