@@ -96,7 +96,7 @@ int plan_tree(const detfold_paged_cache &c, int64_t batch, int32_t drafts, int32
     int64_t of_head = (cols + 16 * tiles - 1) / (16 * tiles);  // units of a key-value head
     // More units than one of a key-value head take its tokens from LDS together: 2, 4 or
     // 8 to a workgroup (1 x 16 tokens over 131072, two units: 122 us, 128 straight to
-    // registers; 32 x 64 over 4096, eight: 279 and 377).
+    // registers; 32 x 64 over 4096, eight: 281 and 377).
     const int most_shared = wide_head * elem_size(c.type) >= 128 ? 8 : 4;
     p->shared = tiles < 2 || of_head < 2 || !tree_staged(c) ? 0 : of_head <= 2 ? 2 : of_head <= 4 || most_shared == 4 ? 4 : 8;
     if (p->shared)

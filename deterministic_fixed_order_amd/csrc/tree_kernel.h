@@ -12,10 +12,10 @@
 //
 // What bounds it.  Up to 32 queries of a key-value head: the cache's bytes, read once
 // straight to registers (64 ragged rows of 8 drafted tokens over 8192 bfloat16 tokens
-// of 8 heads of 128: 182 us, 5.5 TB/s; of one capped token each over their last 4096:
-// 125 us, 5.9; 32 x 8192 e4m3: 94 us, 5.7).  Above: the instructions around the
+// of 8 heads of 128: 181 us, 5.5 TB/s; of one capped token each over their last 4096:
+// 126 us, 5.8; 32 x 8192 e4m3: 93 us, 5.8).  Above: the instructions around the
 // products, 8 cycles a score and lane, so that waves which take the same tokens share
-// them through LDS (32 rows of 64 drafted tokens over 4096, capped: 279 us, 490
+// them through LDS (32 rows of 64 drafted tokens over 4096, capped: 281 us, 488
 // TFLOP/s with the vector units busy three quarters of the time; 377 us straight to
 // registers).  Small calls: the code, run once (1 x 8 over 1000: 17 us).  So:
 // * Steps all of whose tokens all queries see hold no code for masks, or jump over it;
@@ -25,6 +25,15 @@
 //   (zero times them is NaN), and added at the end, once, to the sums of those that do.
 // * A capped score takes 9 instructions below half its cap, a polynomial, and 19 where a
 //   wave has one above.
+//
+// Fewer bits.  As in attend_kernel.h the weights are rounded to the 16-bit type that the
+// matrix units multiply where the output is of 16 bits too, and a float32 output takes
+// them whole.  Against the definition the measured bfloat16 cases are off by 0.0017 to
+// 0.0018 relative, where weights of 32 bits and the output's rounding alone give 0.0016
+// to 0.0017; a model in 64 bits of flat scores over 8192 tokens, whose outputs are small
+// beside the values, 0.0022 and 0.0016 (scores of a spread of 0.5: 0.0024 and 0.0017).
+// The other choice, a second product for what the rounding leaves, would double the
+// second products and their weights' conversions.
 #ifndef DETFOLD_TREE_KERNEL_H
 #define DETFOLD_TREE_KERNEL_H
 
@@ -131,7 +140,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0
 // registers meanwhile.  Straight to registers, as for fewer queries, every wave would
 // load all of it, and a load of keys, 16 tokens by 4 chunks, is 64 accesses of the
 // compute unit's cache where one of neighbours is 16: 32 rows of 64 drafted tokens
-// over 4096 kept it 81% busy and took 377 us, 279 so; 1 x 16 over 131072 128 us, 122
+// over 4096 kept it 81% busy and took 377 us, 281 so; 1 x 16 over 131072 128 us, 122
 // so.  Keys lie so that the 16 tokens' same chunks are on different banks: a token's
 // chunk c in the place of c ^ key(token).
 template <typename C, int D, int SHARE> struct Staged {

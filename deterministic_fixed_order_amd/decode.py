@@ -312,7 +312,8 @@ def attend_paged(out, q, cache: PagedCache, table, lens, *, scale=None, window: 
 
     With ``cap`` > 0 a score s becomes cap * tanh(s / cap); then ``slopes``
     (float32 [q_heads]) add slope * (t - (len - 1)) to the score of token t.
-    Here none of these, nor ``scale`` (also times a key scale), may pass 2^127."""
+    Here none of these, nor ``scale`` (also times a key scale), may pass 2^127, nor
+    ``max_len`` 2^31 - 65."""
     if cap or slopes is not None:
         return _draft().scored(out, q, cache, table, lens, cap, slopes, scale, window, max_len, lse, workspace, split, stream)
     dev = cache.device_index
