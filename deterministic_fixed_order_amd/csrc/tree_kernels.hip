@@ -13,8 +13,10 @@ constexpr int kBlock = 256;  // threads of the join
 // The sums of each query of a row, or of the row that a share begins without
 // ending it, joined in order.  A lane takes four dims, LANES lanes a part, and
 // GROUPS groups of lanes every GROUPS-th part of a query; the loads of DEEP parts
-// go out together.  Parts that are empty add zeros, so with the same GROUPS a row's
-// bits do not depend on how many follow its last one.
+// go out together.  Parts that are empty add zeros, so with the same GROUPS and DEEP a
+// row's bits do not depend on how many follow its last one.  Nor do they on whether
+// there are groups, where these have one part each and one group takes as many at a time:
+// the same sums in the same order, each product added by one rounding.
 template <int LANES, int GROUPS, int DEEP> __global__ __launch_bounds__(kBlock) void k_join_tree(TreeArgs p)
 {
     constexpr int QUERIES = kBlock / (LANES * GROUPS);  // of a workgroup
@@ -75,8 +77,8 @@ template <int LANES, int GROUPS, int DEEP> __global__ __launch_bounds__(kBlock) 
 #pragma unroll
         for (int j = 0; j < DEEP; ++j) {
             const float w = weight2_of(s[j].x - origin);
-            l += s[j].y * w;
-            acc += x[j] * w;
+            l = __builtin_fmaf(s[j].y, w, l);
+            acc = __builtin_elementwise_fma(x[j], f4{w, w, w, w}, acc);
         }
     }
     float top = m;
@@ -95,8 +97,8 @@ template <int LANES, int GROUPS, int DEEP> __global__ __launch_bounds__(kBlock) 
         acc = f4{0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
         for (int i = 0; i < GROUPS; ++i) {
             const float w = weight2_of(mls[own][i].x - origin);
-            l += mls[own][i].y * w;
-            acc += accs[own][i][lane] * w;
+            l = __builtin_fmaf(mls[own][i].y, w, l);
+            acc = __builtin_elementwise_fma(accs[own][i][lane], f4{w, w, w, w}, acc);
         }
     }
     if (!there)
@@ -110,7 +112,7 @@ template <int LANES, int GROUPS, int DEEP> __global__ __launch_bounds__(kBlock) 
 
 template <int GROUPS, int DEEP> const void *pick_join(int dim)
 {
-    if constexpr (GROUPS <= 4)
+    if constexpr (GROUPS == 4 || DEEP == 4)
         if (dim > 128)
             return (const void *)k_join_tree<64, GROUPS, DEEP>;
     return dim <= 64 ? (const void *)k_join_tree<16, GROUPS, DEEP> : (const void *)k_join_tree<32, GROUPS, DEEP>;
@@ -140,15 +142,18 @@ int launch_tree(const TreeArgs &a, void *stream)
     if (!a.shares.d && a.parts.d <= 1)
         return DETFOLD_OK;
     // Where rows have many parts, and few queries wait for them, several groups of
-    // lanes take a query's.  Groups add in another order than one does, so where
-    // `split` fixes a row's parts, and its bits with them, they do whatever the number
-    // of parts, which goes by max_len.
-    const int lanes = a.c.v_dim <= 64 ? 16 : a.c.v_dim <= 128 ? 32 : 64;
+    // lanes take a query's.  With `split` a row's bits must not go by the number of parts,
+    // which max_len sets: there groups begin where they have more than one part each, and
+    // up to there one group takes all parts at once, which adds the same (16 x 64 tokens
+    // over 2048 in 2 parts: 88 us, 128 with groups; 64 x 8 over 4096 in 8: 224 and 249).
+    const int lanes = a.c.v_dim <= 64 ? 16 : a.c.v_dim <= 128 ? 32 : 64, most = 256 / lanes < 8 ? 4 : 8;
     const int64_t parts = a.shares.d ? a.shares.d / a.a.batch : a.parts.d, queries_all = (int64_t)a.drafts * a.a.q_heads;
-    const int groups = a.a.split > 0 || parts > 8 ? 256 / lanes < 8 ? 4 : 8 : 1, per = kBlock / (lanes * groups);
+    const int groups = parts > (a.a.split > 0 ? most : 8) ? most : 1, per = kBlock / (lanes * groups);
+    const bool at_once = a.a.split > 0 && parts > 4;
     const int64_t each = (queries_all + per - 1) / per;
     copy.join_blocks = divider((uint32_t)each);
-    const void *join = groups == 8 ? pick_join<8, 8>(a.c.v_dim) : groups == 4 ? pick_join<4, 8>(a.c.v_dim) : pick_join<1, 4>(a.c.v_dim);
+    const void *join = groups == 8 ? pick_join<8, 8>(a.c.v_dim) : groups == 4 ? pick_join<4, 8>(a.c.v_dim)
+                       : at_once   ? pick_join<1, 8>(a.c.v_dim) : pick_join<1, 4>(a.c.v_dim);
     if (!(a.shares.d ? launch(join, (a.by_row ? a.a.batch : a.shares.d) * each, kBlock, 0) : rows(each, join, kBlock, 0)))
         return DETFOLD_ELAUNCH;
     return DETFOLD_OK;
